@@ -1,0 +1,350 @@
+"""What the operators around an expert-parallel rank's MoE share cost, case by case.
+
+Three families:
+
+* ``few``: the rank's whole share of an MoE layer (router, selection, expert
+  MLPs, weighted return) for at most 32 tokens, as one decode step calls it;
+* ``linear_i8`` and ``ffn_i8``: products of 8-bit integers with one scale per
+  token and one per weight channel, for one weight matrix and for the grouped
+  SwiGLU MLPs of a rank's experts;
+* ``norm_pre`` and ``norm_post``: the RMS norms before and after the block,
+  the second fused with the block's gate, the scaled residual and the norm
+  before the next block.
+
+``run`` computes a case in plain torch operations, or, where ``own`` is true,
+through the package's entry points.
+"""
+import torch
+
+own = False
+
+EPS = 1e-6
+
+
+def _few(name, T, H, I, E, El, e0, k, out="bf16", bias=False):
+    return {"name": name, "op": "few", "T": T, "H": H, "I": I, "E": E, "El": El, "e0": e0, "k": k, "out": out,
+            "bias": bias}
+
+
+def listed():
+    return [
+        # one token of one user: the DeepSeek-R1-shaped layer with all experts
+        # on the rank, each cut to an eighth of its intermediate size (EP=1 x TP=8)
+        _few("few_dsr1_tp8_t1", 1, 7168, 256, 256, 256, 0, 8),
+        # a small decode batch on the DeepSeek-R1-shaped EP=8 rank share
+        _few("few_dsr1_ep8_t16", 16, 7168, 2048, 256, 32, 64, 8, bias=True),
+        # the GPT-OSS-20B-shaped EP=2 x TP=4 rank share, a handful of tokens
+        _few("few_gptoss_t7", 7, 2880, 768, 32, 16, 16, 4),
+        # the small top-2 layer, a full batch, the share kept in float32
+        _few("few_small_t32", 32, 1024, 2816, 8, 8, 0, 2, out="f32"),
+        # one decode token through a DeepSeek-R1-shaped gate/up projection
+        {"name": "linear_i8_m1", "op": "linear_i8", "M": 1, "K": 7168, "N": 4096},
+        # an odd batch through a GPT-OSS-20B-shaped slice (EP=2 x TP=4)
+        {"name": "linear_i8_m333", "op": "linear_i8", "M": 333, "K": 2880, "N": 1536},
+        # a prefill chunk through a DeepSeek-R1-shaped gate/up projection
+        {"name": "linear_i8_m8192", "op": "linear_i8", "M": 8192, "K": 7168, "N": 4096},
+        # a decode batch's rows on the GPT-OSS-20B-shaped EP=2 x TP=4 experts
+        {"name": "ffn_i8_gptoss_r61", "op": "ffn_i8", "rows": 61, "H": 2880, "I": 768, "El": 16, "even": False},
+        # a prefill chunk's rows on the DeepSeek-R1-shaped EP=8 rank's experts
+        {"name": "ffn_i8_dsr1_r16384", "op": "ffn_i8", "rows": 16384, "H": 7168, "I": 2048, "El": 32, "even": True},
+        # after the block for one decode token: norm, token gate, residual, next norm
+        {"name": "norm_post_t1", "op": "norm_post", "T": 1, "H": 7168, "y": "bf16", "r": "bf16", "gate": "token",
+         "post": True, "next": True, "scale": 1.0},
+        # after the block for a prefill chunk, the summed shares in float32
+        {"name": "norm_post_t16384", "op": "norm_post", "T": 16384, "H": 7168, "y": "f32", "r": "bf16",
+         "gate": "channel", "post": True, "next": True, "scale": 0.5},
+        # before the block for an odd prefill batch of the GPT-OSS-20B width
+        {"name": "norm_pre_t1001", "op": "norm_pre", "T": 1001, "H": 2880, "r": "bf16"},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    """An integer of [lo, hi], spread over its logarithm."""
+    v = lo * (hi / lo) ** rng.random()
+    return max(lo, min(hi, int(round(v))))
+
+
+def draw(rng):
+    op = rng.choice(["few", "few", "linear_i8", "ffn_i8", "norm_post", "norm_pre"])
+    if op == "few":
+        while True:
+            T = _log_int(rng, 1, 32)
+            H = 8 * _log_int(rng, 16, 7168 // 8)
+            I = 8 * _log_int(rng, 4, 2816 // 8)
+            E = _log_int(rng, 4, 256)
+            k = rng.randint(1, min(8, E))
+            El = max(1, E // rng.choice([1, 2, 4, 8]))
+            # at most the largest listed case's expected weight bytes
+            if El * H * I <= 32 * 7168 * 2048 and _used(T, E, El, k) * H * I <= 12.5 * 7168 * 2048:
+                break
+        e0 = El * rng.randrange(E // El)
+        return {"op": op, "T": T, "H": H, "I": I, "E": E, "El": El, "e0": e0, "k": k,
+                "out": rng.choice(["bf16", "f32"]), "bias": rng.random() < 0.5}
+    if op == "linear_i8":
+        return {"op": op, "M": _log_int(rng, 1, 8192), "K": 16 * _log_int(rng, 8, 448),
+                "N": 8 * _log_int(rng, 16, 512)}
+    if op == "ffn_i8":
+        return {"op": op, "rows": _log_int(rng, 1, 8192), "H": 16 * _log_int(rng, 8, 448),
+                "I": 16 * _log_int(rng, 2, 128), "El": _log_int(rng, 1, 32), "even": rng.random() < 0.5}
+    T, H = _log_int(rng, 1, 16384), 8 * _log_int(rng, 8, 896)
+    if op == "norm_pre":
+        return {"op": op, "T": T, "H": H, "r": rng.choice(["bf16", "f32"])}
+    return {"op": op, "T": T, "H": H, "y": rng.choice(["bf16", "f32"]), "r": "bf16",
+            "gate": rng.choice(["none", "channel", "token", "full"]) if T * H <= 8192 * 7168 else "channel",
+            "post": rng.random() < 0.7, "next": rng.random() < 0.7, "scale": rng.choice([1.0, 0.5, 0.7071])}
+
+
+def _used(T, E, El, k):
+    """Local experts that at least one of T tokens selects, expected for even routing."""
+    return El * (1.0 - (1.0 - k / E) ** T)
+
+
+_TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _int8_weights(g, E, N, K, dev):
+    """Per-channel 8-bit weights [E, N, K] and their scales [E, N], from normal draws."""
+    q = torch.empty((E, N, K), dtype=torch.int8, device=dev)
+    s = torch.empty((E, N), dtype=torch.float32, device=dev)
+    step = max(1, (1 << 27) // (N * K))
+    for a in range(0, E, step):
+        w = torch.randn((min(step, E - a), N, K), generator=g, device=dev) * K ** -0.5
+        top = w.abs().amax(-1)
+        s[a:a + step] = top / 127
+        q[a:a + step] = torch.round(w * (127 / top)[..., None]).clamp(-127, 127).to(torch.int8)
+    return q, s
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+
+    def randn(*shape, scale=1.0, dtype=torch.float32):
+        return torch.randn(shape, generator=g, device=dev, dtype=dtype) * scale
+
+    st = {"case": case}
+    op = case["op"]
+    if op == "few":
+        T, H, I, E, El = (case[n] for n in ("T", "H", "I", "E", "El"))
+        bf = torch.bfloat16
+        st["x"] = randn(T, H, scale=H ** -0.5).to(bf)
+        st["w_router"] = randn(E, H)
+        st["bias"] = randn(E, scale=0.1) if case["bias"] else None
+        st["w_gate_up"] = randn(El, H, 2 * I, scale=H ** -0.5, dtype=bf)
+        st["w_down"] = randn(El, I, H, scale=I ** -0.5, dtype=bf)
+    elif op == "linear_i8":
+        st["x"] = randn(case["M"], case["K"]).to(torch.bfloat16)
+        st["w_q"], st["w_s"] = _int8_weights(g, 1, case["N"], case["K"], dev)
+    elif op == "ffn_i8":
+        rows, H, I, El = case["rows"], case["H"], case["I"], case["El"]
+        st["x"] = randn(rows, H).to(torch.bfloat16)
+        p = torch.rand(El, generator=g, device=dev) ** (0.0 if case["even"] else 2.0) + 1e-3
+        pick = torch.multinomial(p, rows, replacement=True, generator=g)
+        ends = torch.bincount(pick, minlength=El).cumsum(0)
+        st["offsets"] = torch.cat([ends.new_zeros(1), ends]).to(torch.int32)
+        st["gu_q"], st["gu_s"] = _int8_weights(g, El, 2 * I, H, dev)
+        st["dn_q"], st["dn_s"] = _int8_weights(g, El, H, I, dev)
+    else:
+        T, H = case["T"], case["H"]
+        st["r"] = randn(T, H).to(_TYPES[case["r"]])
+        st["w"] = 1 + randn(H, scale=0.1)
+        if op == "norm_post":
+            st["y"] = randn(T, H, scale=0.3).to(_TYPES[case["y"]])
+            st["w_post"] = 1 + randn(H, scale=0.1) if case["post"] else None
+            shape = {"none": None, "channel": (H,), "token": (T,), "full": (T, H)}[case["gate"]]
+            st["gate"] = None if shape is None else randn(*shape, scale=0.5)
+    return st
+
+
+# --------------------------------------------------------------------------- #
+# The plain forms                                                              #
+# --------------------------------------------------------------------------- #
+def _silu_mul(gu, I):
+    g, u = gu[..., :I], gu[..., I:]
+    return g / (1 + torch.exp(-g)) * u
+
+
+def _plain_few(st):
+    c = st["case"]
+    # the selection compares neighbouring logits: 64 bits
+    logits = st["x"].double() @ st["w_router"].double().T
+    if st["bias"] is not None:
+        logits = logits + st["bias"]
+    val, idx = torch.sort(logits, dim=1, descending=True, stable=True)
+    val, idx = val[:, :c["k"]], idx[:, :c["k"]]
+    p = torch.exp(val - val[:, :1])
+    p = (p / p.sum(1, keepdim=True)).float()
+    w = torch.zeros_like(logits, dtype=torch.float32).scatter(1, idx, p)[:, c["e0"]:c["e0"] + c["El"]]
+    # every local expert on every token, weighted with zero where not selected
+    h = _silu_mul(torch.matmul(st["x"].float(), st["w_gate_up"].float()), c["I"])
+    out = torch.matmul(h, st["w_down"].float())
+    return (w.T[:, :, None] * out).sum(0).to(_TYPES[c["out"]])
+
+
+def _plain_quantize(x):
+    """Symmetric 8-bit values of each row (as float32) and the rows' scales.
+    127 x / max |x| may sit next to a half: 64 bits, halves to even."""
+    top = x.double().abs().amax(-1, keepdim=True)
+    q = torch.round(127 * x.double() / torch.where(top > 0, top, 1.0))
+    return q.float(), (top / 127).float()
+
+
+def _plain_linear_i8(st):
+    q, s = _plain_quantize(st["x"])
+    return (q @ st["w_q"][0].float().T * s * st["w_s"][0]).to(torch.bfloat16)
+
+
+def _plain_ffn_i8(st):
+    c = st["case"]
+    off = st["offsets"].long()
+    # the ragged rows in a padded [expert, row] grid
+    row = torch.arange(c["rows"], device=off.device)
+    e = torch.searchsorted(off[1:], row, right=True)
+    at = row - off[e]
+    most = int((off[1:] - off[:-1]).max())
+
+    def grid(a):
+        return a.new_zeros((c["El"], most, a.shape[-1])).index_put((e, at), a)
+
+    q, s = _plain_quantize(st["x"])
+    gu = torch.matmul(grid(q), st["gu_q"].float().transpose(1, 2).contiguous()) * grid(s) * st["gu_s"][:, None]
+    q, s = _plain_quantize(_silu_mul(gu, c["I"]))
+    out = torch.matmul(q, st["dn_q"].float().transpose(1, 2).contiguous()) * s * st["dn_s"][:, None]
+    return out[e, at].to(torch.bfloat16)
+
+
+def _plain_norm(v, w):
+    return v / torch.sqrt((v * v).mean(-1, keepdim=True) + EPS) * w
+
+
+def _plain_norm_post(st):
+    c = st["case"]
+    z = st["y"].float()
+    if st["w_post"] is not None:
+        z = _plain_norm(z, st["w_post"])
+    if st["gate"] is not None:
+        z = z * (st["gate"][:, None] if c["gate"] == "token" else st["gate"])
+    r = c["scale"] * st["r"].float() + z
+    out = r.to(st["r"].dtype)
+    return [out, _plain_norm(r, st["w"]).to(torch.bfloat16)] if c["next"] else [out]
+
+
+# --------------------------------------------------------------------------- #
+# One pass                                                                     #
+# --------------------------------------------------------------------------- #
+def run(st):
+    c = st["case"]
+    op = c["op"]
+    if own:
+        import expert_token_routing_amd as M
+        if op == "few":
+            f = M.moe_forward_few if c["out"] == "bf16" else M.moe_forward_few_f32
+            return f(st["x"], st["w_router"], st["bias"], st["w_gate_up"], st["w_down"], c["k"], c["e0"])[0]
+        if op == "linear_i8":
+            q, s = M.moe_quantize_rows(st["x"])
+            return M.moe_gemm_i8(q, s, st["w_q"], st["w_s"])
+        if op == "ffn_i8":
+            return M.moe_expert_ffn_i8(st["x"], st["offsets"], st["gu_q"], st["gu_s"], st["dn_q"], st["dn_s"])[0]
+        if op == "norm_pre":
+            return M.moe_norm_pre(st["r"], st["w"], EPS)
+        out, normed = M.moe_norm_post(st["y"], st["r"], st["w_post"], gate=st["gate"], residual_scale=c["scale"],
+                                      w_next=st["w"] if c["next"] else None, eps=EPS)
+        return [out, normed] if c["next"] else [out]
+    if op == "few":
+        return _plain_few(st)
+    if op == "linear_i8":
+        return _plain_linear_i8(st)
+    if op == "ffn_i8":
+        return _plain_ffn_i8(st)
+    if op == "norm_pre":
+        return _plain_norm(st["r"].float(), st["w"]).to(torch.bfloat16)
+    return _plain_norm_post(st)
+
+
+def work(case):
+    """Each input once, each output once; of the experts, the ones that even
+    routing is expected to use."""
+    op = case["op"]
+    if op == "few":
+        T, H, I, E, El, k = (case[n] for n in ("T", "H", "I", "E", "El", "k"))
+        y = 2 if case["out"] == "bf16" else 4
+        picks = T * k * El / E
+        return {"bytes": E * H * 4 + _used(T, E, El, k) * 3 * H * I * 2 + T * H * (2 + y),
+                "flops": 2 * T * H * E + picks * 6 * H * I}
+    if op == "linear_i8":
+        M, K, N = case["M"], case["K"], case["N"]
+        return {"bytes": M * K * 2 + N * K + N * 4 + M * N * 2, "flops": 2 * M * N * K}
+    if op == "ffn_i8":
+        R, H, I, El = case["rows"], case["H"], case["I"], case["El"]
+        used = _used(R, El, El, 1)
+        return {"bytes": R * H * 4 + used * (3 * H * I + 8 * I + 4 * H), "flops": 6 * R * H * I}
+    size = {"bf16": 2, "f32": 4}
+    T, H = case["T"], case["H"]
+    if op == "norm_pre":
+        return {"bytes": T * H * (size[case["r"]] + 2) + 4 * H, "flops": 4 * T * H}
+    gate = {"none": 0, "channel": 4 * H, "token": 4 * T, "full": 4 * T * H}[case["gate"]]
+    nb = T * H * (size[case["y"]] + 2 * size[case["r"]] + (2 if case["next"] else 0)) + gate + 8 * H
+    return {"bytes": nb, "flops": 10 * T * H}
+
+
+# --------------------------------------------------------------------------- #
+# The definitions in 64 bits                                                   #
+# --------------------------------------------------------------------------- #
+def exact(case, seed):
+    st = prepare(case, seed)
+    op = case["op"]
+    f64 = torch.float64
+    if op == "few":
+        T, H, I, k, e0 = case["T"], case["H"], case["I"], case["k"], case["e0"]
+        x = st["x"].to(f64)
+        lg = (x[:, None, :] * st["w_router"].to(f64)[None]).sum(-1)
+        if st["bias"] is not None:
+            lg += st["bias"].to(f64)
+        y = torch.zeros((T, H), dtype=f64, device=x.device)
+        for t in range(T):
+            order = sorted(range(case["E"]), key=lambda e, v=lg[t].tolist(): (-v[e], e))[:k]
+            p = torch.softmax(lg[t, order], 0)
+            for j, e in enumerate(order):
+                if e0 <= e < e0 + case["El"]:
+                    gu = x[t] @ st["w_gate_up"][e - e0].to(f64)
+                    h = gu[:I] * torch.sigmoid(gu[:I]) * gu[I:]
+                    y[t] += p[j] * (h @ st["w_down"][e - e0].to(f64))
+        return y
+
+    def quant(v):
+        top = v.abs().amax(1)
+        sc = top / 127
+        q = torch.round(v * 127 / top[:, None])
+        q[top == 0] = 0
+        return q, sc[:, None]
+
+    if op == "linear_i8":
+        q, s = quant(st["x"].to(f64))
+        return (q @ st["w_q"][0].to(f64).T) * s * st["w_s"][0].to(f64)
+    if op == "ffn_i8":
+        I = case["I"]
+        out = torch.zeros((case["rows"], case["H"]), dtype=f64, device=st["x"].device)
+        off = st["offsets"].tolist()
+        for e in range(case["El"]):
+            a, b = off[e], off[e + 1]
+            if a == b:
+                continue
+            q, s = quant(st["x"][a:b].to(f64))
+            gu = (q @ st["gu_q"][e].to(f64).T) * s * st["gu_s"][e].to(f64)
+            q, s = quant(gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:])
+            out[a:b] = (q @ st["dn_q"][e].to(f64).T) * s * st["dn_s"][e].to(f64)
+        return out
+
+    def norm(v, w):
+        return v * torch.rsqrt(v.square().mean(1, keepdim=True) + EPS) * w.to(f64)
+
+    if op == "norm_pre":
+        return norm(st["r"].to(f64), st["w"])
+    z = st["y"].to(f64)
+    if st["w_post"] is not None:
+        z = norm(z, st["w_post"])
+    if st["gate"] is not None:
+        gate = st["gate"].to(f64)
+        z = z * (gate.reshape(-1, 1) if case["gate"] == "token" else gate)
+    r = case["scale"] * st["r"].to(f64) + z
+    return [r, norm(r, st["w"])] if case["next"] else [r]
