@@ -151,7 +151,7 @@ def prepare(case, seed):
         if op == "norm_post":
             st["y"] = randn(T, H, scale=0.3).to(_TYPES[case["y"]])
             st["w_post"] = 1 + randn(H, scale=0.1) if case["post"] else None
-            shape = {"none": None, "channel": (H,), "token": (T,), "full": (T, H)}[case["gate"]]
+            shape = {"none": None, "channel": (H,), "token": (T, 1), "full": (T, H)}[case["gate"]]
             st["gate"] = None if shape is None else randn(*shape, scale=0.5)
     return st
 
@@ -223,7 +223,7 @@ def _plain_norm_post(st):
     if st["w_post"] is not None:
         z = _plain_norm(z, st["w_post"])
     if st["gate"] is not None:
-        z = z * (st["gate"][:, None] if c["gate"] == "token" else st["gate"])
+        z = z * st["gate"]
     r = c["scale"] * st["r"].float() + z
     out = r.to(st["r"].dtype)
     return [out, _plain_norm(r, st["w"]).to(torch.bfloat16)] if c["next"] else [out]
@@ -344,7 +344,6 @@ def exact(case, seed):
     if st["w_post"] is not None:
         z = norm(z, st["w_post"])
     if st["gate"] is not None:
-        gate = st["gate"].to(f64)
-        z = z * (gate.reshape(-1, 1) if case["gate"] == "token" else gate)
+        z = z * st["gate"].to(f64)
     r = case["scale"] * st["r"].to(f64) + z
     return [r, norm(r, st["w"])] if case["next"] else [r]
