@@ -7,9 +7,10 @@ no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import numbers
 import pathlib
-from ctypes import c_int, c_int64, c_size_t, c_void_p
+from ctypes import c_float, c_int, c_int64, c_size_t, c_void_p
 
 LIB_PATH = pathlib.Path(__file__).resolve().parent / "libmoe.so"
 
@@ -45,6 +46,8 @@ SIGNATURES = {
                                            c_int, _P, _P, c_size_t, _P, _P]),
     "moe_forward_noalloc": (c_int, [_P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                     _P, _P]),
+    "moe_norm_pre": (c_int, [_P, c_int, _P, c_float, c_int, c_int, _P, _P]),
+    "moe_norm_post": (c_int, [_P, c_int, _P, c_int, _P, _P, c_int, c_float, _P, c_float, c_int, c_int, _P, _P, _P]),
 }
 
 # bytes of the static scratch moe_forward_noalloc works in (MOE_NOALLOC_SCRATCH_BYTES)
@@ -414,3 +417,107 @@ def moe_forward_noalloc(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize
                                    e0, E_local, int(bool(renormalize)), _ptr(y), _stream(stream, dev))
     check(st, "moe_forward_noalloc")
     return y
+
+
+def _on_stream(fn):
+    """Runs ``fn`` with the device of its first tensor current and, where the
+    caller gave a ``stream``, with that stream current: what ``fn`` allocates
+    then belongs to the stream its kernels run on, so the memory cannot be
+    handed to them while another stream still uses it."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        dev = getattr(first, "device", None)
+        if dev is None or dev.type != "cuda":
+            return fn(first, *args, **kw)  # refused by fn's checks
+        cuda = _torch().cuda
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the call's tensors on {dev}")
+            with cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if dev.index != cuda.current_device():
+            with cuda.device(dev):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+    return call
+
+
+# --------------------------------------------------------------------------- #
+# Norms before and after the block                                             #
+# --------------------------------------------------------------------------- #
+# element types and gate shapes (MOE_TYPE_*, MOE_GATE_*)
+TYPE_BF16, TYPE_F32 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+def _need_either(t, name, shape):
+    """``t`` must be a bf16 or float32 tensor of ``shape``; returns its MOE_TYPE."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    _need(t, t.dtype, name, shape)
+    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+
+
+@_on_stream
+def moe_norm_pre(r, w, eps=1e-6, *, out=None):
+    """The norm before the block: out [T, H] bf16 = r / sqrt(mean(r^2) + eps) * w.
+    ``r`` [T, H] is bf16 or float32, ``w`` [H] float32. Takes ``stream``."""
+    torch = _torch()
+    rt = _need_either(r, "r", (None, None))
+    T, H = r.shape
+    _need(w, torch.float32, "w", (H,))
+    if out is not None:
+        _need(out, torch.bfloat16, "out", (T, H))
+    dev = r.device
+    _placed(dev, r=r, w=w)
+    out = _out(out, (T, H), torch.bfloat16, dev, "out")
+    check(lib().moe_norm_pre(_ptr(r), rt, _ptr(w), eps, T, H, _ptr(out), _stream(None, dev)), "moe_norm_pre")
+    return out
+
+
+@_on_stream
+def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_next=None, eps=1e-6, out=None,
+                  normed=None):
+    """out = residual_scale * residual + gate * norm(y; w_post), of the
+    residual's type, and with ``w_next`` also normed [T, H] bf16 =
+    norm(out before its rounding; w_next). Returns (out, normed or None).
+
+    ``y`` and ``residual`` [T, H] are bf16 or float32; ``w_post`` and
+    ``w_next`` [H] float32 (``w_post`` None: y as it is). ``gate`` float32 is
+    [H] (per channel), [T, 1] (per token) or [T, H]. ``out`` may be
+    ``residual``. Takes ``stream``."""
+    torch = _torch()
+    yt = _need_either(y, "y", (None, None))
+    T, H = y.shape
+    rt = _need_either(residual, "residual", (T, H))
+    if w_post is not None:
+        _need(w_post, torch.float32, "w_post", (H,))
+    kind = GATE_NONE
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        got = tuple(gate.shape)
+        kind = {(T, H): GATE_FULL, (T, 1): GATE_TOKEN, (H,): GATE_CHANNEL}.get(got)
+        if kind is None:
+            raise ValueError(f"gate has shape {got}, expected shape ({H},), ({T}, 1) or ({T}, {H})")
+        _need(gate, torch.float32, "gate")
+    if w_next is not None:
+        _need(w_next, torch.float32, "w_next", (H,))
+    elif normed is not None:
+        raise ValueError("normed is given without w_next")
+    if out is not None:
+        _need(out, residual.dtype, "out", (T, H))
+    if normed is not None:
+        _need(normed, torch.bfloat16, "normed", (T, H))
+    dev = y.device
+    _placed(dev, y=y, residual=residual, w_post=w_post, gate=gate, w_next=w_next)
+    out = _out(out, (T, H), residual.dtype, dev, "out")
+    if w_next is not None:
+        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+    st = lib().moe_norm_post(_ptr(y), yt, _ptr(residual), rt, _ptr(w_post), _ptr(gate), kind, residual_scale,
+                             _ptr(w_next), eps, T, H, _ptr(out), _ptr(normed), _stream(None, dev))
+    check(st, "moe_norm_post")
+    return out, normed

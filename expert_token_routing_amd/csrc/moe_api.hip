@@ -1,5 +1,6 @@
 // C-ABI of the MoE rank-share library: argument checks, workspace layout and
 // the one-stream forward pass. Every check runs on the host before any launch.
+#include <cmath>
 #include <mutex>
 
 #include "moe.h"
@@ -346,6 +347,42 @@ int moe_forward_fused_profiled(const moe_bf16* x, const float* w_router, const f
     if (!events[i]) return MOE_ERR_INVALID_ARG;
   return forward_impl(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, false,
                       workspace, workspace_bytes, events, stream, true);
+}
+
+static int check_norm(int T, int H, float eps) {
+  if (T < 0 || H <= 0 || (H % 8) != 0 || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+static bool type_ok(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
+
+int moe_norm_pre(const void* r, int r_type, const float* w, float eps, int T, int H, moe_bf16* out,
+                 hipStream_t stream) {
+  const int st = check_norm(T, H, eps);
+  if (st != MOE_OK) return st;
+  if (!type_ok(r_type)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!r || !w || !out || !aligned16(r) || !aligned16(w) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_block_norm(nullptr, 0, r, r_type == MOE_TYPE_F32, nullptr, nullptr, MOE_GATE_NONE, 1.f, w,
+                                      eps, T, H, nullptr, out, stream));
+}
+
+int moe_norm_post(const void* y, int y_type, const void* residual, int r_type, const float* w_post,
+                  const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
+                  int H, void* out, moe_bf16* normed, hipStream_t stream) {
+  const int st = check_norm(T, H, eps);
+  if (st != MOE_OK) return st;
+  if (!type_ok(y_type) || !type_ok(r_type) || gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // (empty arrays may be NULL)
+  if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr) || (w_next == nullptr) != (normed == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!y || !residual || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(out) || !aligned16(w_post) || !aligned16(w_next) ||
+      !aligned16(normed) || (gate_kind != MOE_GATE_TOKEN && !aligned16(gate)))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_block_norm(y, y_type == MOE_TYPE_F32 ? 2 : 1, residual, r_type == MOE_TYPE_F32, w_post,
+                                      gate, gate_kind, residual_scale, w_next, eps, T, H, out, normed, stream));
 }
 
 }  // extern "C"

@@ -33,6 +33,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+// The same rounding by the conversion instruction, for values that may be
+// infinite or NaN (a NaN stays one).
+__device__ __forceinline__ uint16_t cvt_bf16(float f) { return __builtin_bit_cast(uint16_t, __bf16(f)); }
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  return uint32_t(cvt_bf16(lo)) | (uint32_t(cvt_bf16(hi)) << 16);
+}
+
 // ---------------------------------------------------------------------------
 // Matrix-core tile: v_mfma_f32_32x32x16_bf16.
 //   A fragment: lane l holds A[l % 32][8*(l/32) .. 8*(l/32)+7]

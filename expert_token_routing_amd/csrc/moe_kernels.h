@@ -99,6 +99,13 @@ hipError_t launch_dispatch_index(const int32_t* topk_idx, int T, int E, int k, i
 hipError_t launch_combine(const uint16_t* expert_out, const int32_t* inv, const float* topk_w, int T, int H, int k,
                           void* y, bool y_f32, hipStream_t stream, bool skip_single = false);
 
+// Norms around a block (norm.hip). y_type: 0 none (norm of r alone into
+// normed), 1 bf16, 2 float32; gate_kind: 0 none, 1 per channel [H], 2 per
+// token [T], 3 per value [T, H].
+hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f32, const float* w_post,
+                             const float* gate, int gate_kind, float scale, const float* w_next, float eps, int T,
+                             int H, void* out, uint16_t* normed, hipStream_t stream);
+
 // Cached device facts of the current device.
 int device_cu_count();
 

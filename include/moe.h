@@ -313,6 +313,62 @@ int moe_forward_fused_profiled(const moe_bf16* x, const float* w_router, const f
 int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
                                  size_t* offsets_out);
 
+/* ------------------------------------------------------------------------ */
+/* Norms before and after the block, with its gate and residual scale.       */
+/* ------------------------------------------------------------------------ */
+
+/* Element types of arguments that may have either. */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F32 1
+
+/* Shapes of the gate of moe_norm_post. */
+#define MOE_GATE_NONE 0    /* no gate (1) */
+#define MOE_GATE_CHANNEL 1 /* [H]: one value per channel */
+#define MOE_GATE_TOKEN 2   /* [T]: one value per token */
+#define MOE_GATE_FULL 3    /* [T, H]: one value per token and channel */
+
+/* Largest hidden size of the norms (a row is held on chip). */
+#define MOE_NORM_MAX_H 32768
+
+/*
+ * The norm before the block: out[t] = rms(r[t]) * w, with
+ * rms(v) = v / sqrt(mean(v^2) + eps); float32 arithmetic, one rounding.
+ *
+ *   r    [T, H] bf16 or f32 (r_type: MOE_TYPE_BF16 or MOE_TYPE_F32)
+ *   w    [H]    f32
+ *   eps         >= 0, finite
+ *   out  [T, H] bf16 OUT; may be r itself where r is bf16
+ * H is a multiple of 8 and at most MOE_NORM_MAX_H (MOE_ERR_UNSUPPORTED above);
+ * r, w and out are 16-byte aligned. An infinity or NaN in a row makes that
+ * row's outputs what the formula gives (NaN or 0) and touches no other row.
+ */
+int moe_norm_pre(const void* r, int r_type, const float* w, float eps, int T, int H, moe_bf16* out,
+                 hipStream_t stream);
+
+/*
+ * What follows the block, in one pass over its output:
+ *   z   = rms(y[t]) * w_post                       (w_post NULL: z = y[t])
+ *   r'  = residual_scale * residual[t] + gate * z  (out)
+ *   n'  = rms(r') * w_next                         (normed, of the unrounded r')
+ * float32 arithmetic, each output rounded once.
+ *
+ *   y        [T, H] bf16 or f32 (y_type): the block's output, e.g. moe_forward's,
+ *                   or the sum of every rank's moe_forward_f32 share
+ *   residual [T, H] bf16 or f32 (r_type)
+ *   w_post   [H] f32 or NULL
+ *   gate     f32, shaped by gate_kind (MOE_GATE_*); NULL exactly with MOE_GATE_NONE
+ *   w_next   [H] f32, or NULL for no second norm (normed is then NULL too)
+ *   out      [T, H] of r_type OUT; may be residual itself, or y itself where
+ *                   their types are equal
+ *   normed   [T, H] bf16 OUT; overlaps no other argument, except that it may
+ *                   be y itself where y is bf16 and out is not y
+ * Sizes, eps and alignment (all matrix and vector pointers but a token gate)
+ * as for moe_norm_pre.
+ */
+int moe_norm_post(const void* y, int y_type, const void* residual, int r_type, const float* w_post,
+                  const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
+                  int H, void* out, moe_bf16* normed, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
