@@ -46,6 +46,14 @@ SIGNATURES = {
                                            c_int, _P, _P, c_size_t, _P, _P]),
     "moe_forward_noalloc": (c_int, [_P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                     _P, _P]),
+    "moe_quantize_rows": (c_int, [_P, c_int64, c_int, _P, _P, _P]),
+    "moe_quantize_weights": (c_int, [_P, c_int, c_int, c_int, _P, _P, _P]),
+    "moe_gemm_i8": (c_int, [_P, _P, _P, _P, _P, c_int64, c_int, c_int, c_int, _P, _P]),
+    "moe_expert_ffn_i8_workspace_size": (c_size_t, [c_int, c_int, c_int64]),
+    "moe_expert_ffn_i8": (c_int, [_P, _P, _P, _P, _P, _P, c_int, c_int, c_int, c_int64, _P, _P, c_size_t, _P]),
+    "moe_forward_i8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "moe_forward_i8": (c_int, [_P, _P, _P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                               _P, _P, c_size_t, _P]),
     "moe_norm_pre": (c_int, [_P, c_int, _P, c_float, c_int, c_int, _P, _P]),
     "moe_norm_post": (c_int, [_P, c_int, _P, c_int, _P, _P, c_int, c_float, _P, c_float, c_int, c_int, _P, _P, _P]),
 }
@@ -521,3 +529,150 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
                              _ptr(w_next), eps, T, H, _ptr(out), _ptr(normed), _stream(None, dev))
     check(st, "moe_norm_post")
     return out, normed
+
+
+# --------------------------------------------------------------------------- #
+# 8-bit integer products                                                       #
+# --------------------------------------------------------------------------- #
+@_on_stream
+def moe_quantize_rows(x, *, q=None, scale=None):
+    """q [M, K] int8 and scale [M] float32 of x [M, K] bf16: scale = max|x| / 127
+    per row, q = x / scale to the nearest integer. Takes ``stream``."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x", (None, None))
+    M, K = x.shape
+    if q is not None:
+        _need(q, torch.int8, "q", (M, K))
+    if scale is not None:
+        _need(scale, torch.float32, "scale", (M,))
+    dev = x.device
+    _placed(dev, x=x)
+    q = _out(q, (M, K), torch.int8, dev, "q")
+    scale = _out(scale, (M,), torch.float32, dev, "scale")
+    check(lib().moe_quantize_rows(_ptr(x), M, K, _ptr(q), _ptr(scale), _stream(None, dev)), "moe_quantize_rows")
+    return q, scale
+
+
+@_on_stream
+def moe_quantize_weights(w, *, q=None, scale=None):
+    """q [E_local, N, K] int8 and scale [E_local, N] float32 of the weights w
+    [E_local, K, N] bf16 (the layout of w_gate_up and w_down), a scale per
+    output channel. Takes ``stream``."""
+    torch = _torch()
+    _need(w, torch.bfloat16, "w", (None, None, None))
+    E_local, K, N = w.shape
+    if q is not None:
+        _need(q, torch.int8, "q", (E_local, N, K))
+    if scale is not None:
+        _need(scale, torch.float32, "scale", (E_local, N))
+    dev = w.device
+    _placed(dev, w=w)
+    q = _out(q, (E_local, N, K), torch.int8, dev, "q")
+    scale = _out(scale, (E_local, N), torch.float32, dev, "scale")
+    st = lib().moe_quantize_weights(_ptr(w), E_local, K, N, _ptr(q), _ptr(scale), _stream(None, dev))
+    check(st, "moe_quantize_weights")
+    return q, scale
+
+
+@_on_stream
+def moe_gemm_i8(a, a_scale, w, w_scale, offsets=None, *, out=None):
+    """out [M, N] bf16 = (a @ w[e].T) * a_scale[:, None] * w_scale[e] for the
+    rows of segment e of ``offsets`` [E_local + 1] int32 (None: one weight
+    matrix for all rows). a [M, K] and w [E_local, N, K] are int8, the scales
+    [M] and [E_local, N] float32. Takes ``stream``."""
+    torch = _torch()
+    _need(a, torch.int8, "a", (None, None))
+    M, K = a.shape
+    _need(a_scale, torch.float32, "a_scale", (M,))
+    _need(w, torch.int8, "w", (None, None, K))
+    E_local, N, _ = w.shape
+    _need(w_scale, torch.float32, "w_scale", (E_local, N))
+    if offsets is not None:
+        _need(offsets, torch.int32, "offsets", (E_local + 1,))
+    elif E_local != 1:
+        raise ValueError(f"w holds {E_local} matrices: offsets is required")
+    if out is not None:
+        _need(out, torch.bfloat16, "out", (M, N))
+    dev = a.device
+    _placed(dev, a=a, a_scale=a_scale, w=w, w_scale=w_scale, offsets=offsets)
+    out = _out(out, (M, N), torch.bfloat16, dev, "out")
+    st = lib().moe_gemm_i8(_ptr(a), _ptr(a_scale), _ptr(offsets), _ptr(w), _ptr(w_scale), M, N, K, E_local, _ptr(out),
+                           _stream(None, dev))
+    check(st, "moe_gemm_i8")
+    return out
+
+
+def _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down):
+    torch = _torch()
+    _need(w_gate_up, torch.int8, "w_gate_up", (None, None, H))
+    E_local, I2, _ = w_gate_up.shape
+    if I2 % 2:
+        raise ValueError(f"w_gate_up's second dimension 2I must be even, got {I2}")
+    I = I2 // 2
+    _need(s_gate_up, torch.float32, "s_gate_up", (E_local, I2))
+    _need(w_down, torch.int8, "w_down", (E_local, H, I))
+    _need(s_down, torch.float32, "s_down", (E_local, H))
+    return E_local, I
+
+
+def expert_ffn_i8_workspace_size(H, I, capacity) -> int:
+    return int(lib().moe_expert_ffn_i8_workspace_size(H, I, capacity))
+
+
+@_on_stream
+def moe_expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, *, out=None, workspace=None):
+    """moe_expert_ffn with 8-bit weights (moe_quantize_weights) and activations
+    quantised per row: expert outputs [cap, H] bf16 for the segments in
+    ``offsets``. Returns (out, workspace). Takes ``stream``."""
+    torch = _torch()
+    _need(x_perm, torch.bfloat16, "x_perm", (None, None))
+    cap, H = x_perm.shape
+    E_local, I = _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down)
+    _need(offsets, torch.int32, "offsets", (E_local + 1,))
+    if out is not None:
+        _need(out, torch.bfloat16, "out", (cap, H))
+    dev = x_perm.device
+    _placed(dev, x_perm=x_perm, offsets=offsets, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
+            s_down=s_down)
+    out = _out(out, (cap, H), torch.bfloat16, dev, "out")
+    L = lib()
+    ws = _workspace(L.moe_expert_ffn_i8_workspace_size(H, I, cap), dev, workspace)
+    st = L.moe_expert_ffn_i8(_ptr(x_perm), _ptr(offsets), _ptr(w_gate_up), _ptr(s_gate_up), _ptr(w_down), _ptr(s_down),
+                             H, I, E_local, cap, _ptr(out), _ptr(ws), _nbytes(ws), _stream(None, dev))
+    check(st, "moe_expert_ffn_i8")
+    return out, ws
+
+
+def forward_i8_workspace_size(T, H, I, E, k, E_local) -> int:
+    return int(lib().moe_forward_i8_workspace_size(T, H, I, E, k, E_local))
+
+
+@_on_stream
+def moe_forward_i8(x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, k, e0, renormalize=True, *, y=None,
+                   workspace=None):
+    """moe_forward with the expert MLPs of moe_expert_ffn_i8: y [T, H] bf16.
+    Returns (y, workspace). Takes ``stream``."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x", (None, None))
+    T, H = x.shape
+    _need(w_router, torch.float32, "w_router", (None, H))
+    E = w_router.shape[0]
+    if bias is not None:
+        _need(bias, torch.float32, "bias", (E,))
+    E_local, I = _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down)
+    _check_k(k, E)
+    if not (0 <= e0 and e0 + E_local <= E):
+        raise ValueError(f"local experts [e0, e0 + E_local) = [{e0}, {e0 + E_local}) must lie in [0, E = {E})")
+    if y is not None:
+        _need(y, torch.bfloat16, "y", (T, H))
+    dev = x.device
+    _placed(dev, x=x, w_router=w_router, bias=bias, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
+            s_down=s_down)
+    y = _out(y, (T, H), torch.bfloat16, dev, "y")
+    L = lib()
+    ws = _workspace(L.moe_forward_i8_workspace_size(T, H, I, E, k, E_local), dev, workspace)
+    st = L.moe_forward_i8(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(s_gate_up), _ptr(w_down),
+                          _ptr(s_down), T, H, I, E, k, e0, E_local, int(bool(renormalize)), _ptr(y), _ptr(ws),
+                          _nbytes(ws), _stream(None, dev))
+    check(st, "moe_forward_i8")
+    return y, ws

@@ -349,6 +349,195 @@ int moe_forward_fused_profiled(const moe_bf16* x, const float* w_router, const f
                       workspace, workspace_bytes, events, stream, true);
 }
 
+// Sizes of the 8-bit products: an exact int32 sum needs K < 2^17; 32-bit
+// offsets into one expert's matrix need rows * K < 2^31.
+static int check_i8(int K, int64_t channels) {
+  if (K <= 0 || (K % 16) != 0 || channels <= 0 || (channels % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (K >= (1 << 17) || channels * K >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_quantize_rows(const moe_bf16* x, int64_t M, int K, int8_t* q, float* scale, hipStream_t stream) {
+  if (M < 0 || K <= 0 || (K % 16) != 0) return MOE_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_rows(x, false, nullptr, M, K, q, scale, stream));
+}
+
+int moe_quantize_weights(const moe_bf16* w, int E_local, int K, int N, int8_t* q, float* scale, hipStream_t stream) {
+  if (E_local < 1) return MOE_ERR_INVALID_ARG;
+  const int st = check_i8(K, N);
+  if (st != MOE_OK) return st;
+  if (E_local > kMaxE) return MOE_ERR_UNSUPPORTED;
+  if (!w || !q || !scale || !aligned16(w) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_weights(w, E_local, K, N, q, scale, stream));
+}
+
+int moe_gemm_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, const int8_t* w, const float* w_scale,
+                int64_t capacity, int N, int K, int E_local, moe_bf16* out, hipStream_t stream) {
+  if (E_local < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
+  const int st = check_i8(K, N);
+  if (st != MOE_OK) return st;
+  if (E_local > kMaxE || capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!offsets && E_local != 1) return MOE_ERR_INVALID_ARG;
+  if (capacity == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(w) || !aligned16(w_scale) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_gemm_i8(a, a_scale, offsets, E_local, capacity, w, w_scale, K, N, out,
+                                   ceil_div(capacity, E_local), stream));
+}
+
+}  // extern "C"
+
+namespace moe {
+// The grouped MLPs' intermediates: quantised rows in, h, quantised h.
+struct FfnI8Layout {
+  size_t xq, xs, h, hq, hs, total;
+};
+static FfnI8Layout ffn_i8_layout(size_t at, int64_t x_rows, int64_t cap, int H, int I) {
+  FfnI8Layout L{};
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = align_up(at + bytes);
+    return o;
+  };
+  L.xq = take(size_t(x_rows) * H);
+  L.xs = take(size_t(x_rows) * sizeof(float));
+  L.h = take(size_t(cap) * I * sizeof(float));
+  L.hq = take(size_t(cap) * I);
+  L.hs = take(size_t(cap) * sizeof(float));
+  L.total = at;
+  return L;
+}
+
+// quantise -> gate/up -> quantise -> down. x: x_rows rows, of which row n of a
+// segment is gather_src[n] / gather_k (gather_src given) or row n.
+static hipError_t ffn_i8(const moe_bf16* x, int64_t x_rows, const int32_t* gather_src, int gather_k,
+                         const int32_t* offsets, const int8_t* w_gate_up, const float* s_gate_up,
+                         const int8_t* w_down, const float* s_down, int H, int I, int E_local, int64_t cap,
+                         const FfnI8Layout& L, char* ws, moe_bf16* out, int64_t rows_hint, hipStream_t stream) {
+  int8_t* xq = reinterpret_cast<int8_t*>(ws + L.xq);
+  float* xs = reinterpret_cast<float*>(ws + L.xs);
+  float* h = reinterpret_cast<float*>(ws + L.h);
+  int8_t* hq = reinterpret_cast<int8_t*>(ws + L.hq);
+  float* hs = reinterpret_cast<float*>(ws + L.hs);
+  const int32_t* end = offsets + E_local;
+  hipError_t err = launch_quantize_rows(x, false, gather_src ? nullptr : end, x_rows, H, xq, xs, stream);
+  if (err == hipSuccess)
+    err = launch_gate_up_i8(xq, xs, gather_src, gather_k, int(x_rows), offsets, E_local, cap, w_gate_up, s_gate_up, H,
+                            I, h, rows_hint, stream);
+  if (err == hipSuccess) err = launch_quantize_rows(h, true, end, cap, I, hq, hs, stream);
+  if (err == hipSuccess)
+    err = launch_gemm_i8(hq, hs, offsets, E_local, cap, w_down, s_down, I, H, out, rows_hint, stream);
+  return err;
+}
+
+static int check_ffn_i8(int H, int I) {
+  const int st = check_i8(H, int64_t(2) * I);
+  if (st != MOE_OK) return st;
+  return check_i8(I, H);
+}
+
+struct ForwardI8Layout {
+  size_t planes, part, logits, topk_idx, topk_w, counts, offsets, perm_src, inv, chunks, out;
+  FfnI8Layout ffn;
+};
+static ForwardI8Layout forward_i8_layout(int T, int H, int I, int E, int k, int E_local) {
+  ForwardI8Layout L{};
+  const int64_t cap = min_capacity(T, k, E_local);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes);
+    return at;
+  };
+  L.planes = take(size_t(3) * E * H * sizeof(uint16_t));
+  L.part = take(size_t(route_k_parts(T, H, E) - 1) * T * E * sizeof(float));
+  L.logits = take(size_t(T) * E * sizeof(float));
+  L.topk_idx = take(size_t(T) * k * sizeof(int32_t));
+  L.topk_w = take(size_t(T) * k * sizeof(float));
+  L.counts = take(size_t(E) * sizeof(int32_t));
+  L.offsets = take(size_t(E_local + 1) * sizeof(int32_t));
+  L.perm_src = take(size_t(cap) * sizeof(int32_t));
+  L.inv = take(size_t(T) * k * sizeof(int32_t));
+  L.chunks = take(dispatch_table_bytes(T, E));
+  L.out = take(size_t(cap) * H * sizeof(uint16_t));
+  L.ffn = ffn_i8_layout(o, T, cap, H, I);
+  return L;
+}
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_expert_ffn_i8_workspace_size(int H, int I, int64_t capacity) {
+  if (H <= 0 || I <= 0 || capacity < 0) return 0;
+  return ffn_i8_layout(0, capacity, capacity, H, I).total;
+}
+
+int moe_expert_ffn_i8(const moe_bf16* x_perm, const int32_t* offsets, const int8_t* w_gate_up,
+                      const float* s_gate_up, const int8_t* w_down, const float* s_down, int H, int I, int E_local,
+                      int64_t capacity, moe_bf16* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (E_local < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
+  const int st = check_ffn_i8(H, I);
+  if (st != MOE_OK) return st;
+  if (E_local > kMaxE || capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (capacity == 0) return MOE_OK;
+  if (!x_perm || !offsets || !w_gate_up || !s_gate_up || !w_down || !s_down || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x_perm) || !aligned16(w_gate_up) || !aligned16(s_gate_up) || !aligned16(w_down) ||
+      !aligned16(s_down) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  const FfnI8Layout L = ffn_i8_layout(0, capacity, capacity, H, I);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < L.total)
+    return MOE_ERR_WORKSPACE;
+  return hip_status(ffn_i8(x_perm, capacity, nullptr, 1, offsets, w_gate_up, s_gate_up, w_down, s_down, H, I, E_local,
+                           capacity, L, static_cast<char*>(workspace), out, ceil_div(capacity, E_local), stream));
+}
+
+size_t moe_forward_i8_workspace_size(int T, int H, int I, int E, int k, int E_local) {
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0 || E_local <= 0) return 0;
+  return forward_i8_layout(T, H, I, E, k, E_local).ffn.total;
+}
+
+int moe_forward_i8(const moe_bf16* x, const float* w_router, const float* bias, const int8_t* w_gate_up,
+                   const float* s_gate_up, const int8_t* w_down, const float* s_down, int T, int H, int I, int E,
+                   int k, int e0, int E_local, int renormalize, moe_bf16* y, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
+  if ((st = check_ffn_i8(H, I)) != MOE_OK) return st;
+  if (min_capacity(T, k, E_local) >= (int64_t(1) << 31) || int64_t(T) * H >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router || !w_gate_up || !s_gate_up || !w_down || !s_down || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(s_gate_up) || !aligned16(w_down) ||
+      !aligned16(s_down) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  const ForwardI8Layout L = forward_i8_layout(T, H, I, E, k, E_local);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < L.ffn.total)
+    return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  auto at = [&](size_t off) { return static_cast<void*>(ws + off); };
+  int32_t* topk_idx = static_cast<int32_t*>(at(L.topk_idx));
+  float* topk_w = static_cast<float*>(at(L.topk_w));
+  int32_t* offsets = static_cast<int32_t*>(at(L.offsets));
+  int32_t* perm_src = static_cast<int32_t*>(at(L.perm_src));
+  int32_t* inv = static_cast<int32_t*>(at(L.inv));
+  uint16_t* out = static_cast<uint16_t*>(at(L.out));
+  hipError_t err = launch_route(x, w_router, bias, T, H, E, k, renormalize, static_cast<float*>(at(L.logits)),
+                                topk_idx, topk_w, static_cast<uint16_t*>(at(L.planes)),
+                                static_cast<float*>(at(L.part)), stream);
+  if (err == hipSuccess)
+    err = launch_dispatch_index(topk_idx, T, E, k, e0, E_local, static_cast<int32_t*>(at(L.counts)), offsets,
+                                perm_src, inv, static_cast<int32_t*>(at(L.chunks)), stream);
+  if (err == hipSuccess)
+    err = ffn_i8(x, T, perm_src, k, offsets, w_gate_up, s_gate_up, w_down, s_down, H, I, E_local,
+                 min_capacity(T, k, E_local), L.ffn, ws, out, ceil_div(int64_t(T) * k, E), stream);
+  if (err == hipSuccess) err = launch_combine(out, inv, topk_w, T, H, k, y, false, stream, false);
+  return hip_status(err);
+}
+
 static int check_norm(int T, int H, float eps) {
   if (T < 0 || H <= 0 || (H % 8) != 0 || !(eps >= 0.f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
   if (H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;

@@ -106,6 +106,25 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
                              const float* gate, int gate_kind, float scale, const float* w_next, float eps, int T,
                              int H, void* out, uint16_t* normed, hipStream_t stream);
 
+// 8-bit integer products (gemm_i8.hip). Rows of x quantised with a scale each;
+// rows at and past *end (device memory; NULL: none) are left alone.
+hipError_t launch_quantize_rows(const void* x, bool x_f32, const int32_t* end, int64_t M, int K, int8_t* q,
+                                float* scale, hipStream_t stream);
+// w [E_local, K, N] bf16 -> q [E_local, N, K] and a scale per channel.
+hipError_t launch_quantize_weights(const uint16_t* w, int E_local, int K, int N, int8_t* q, float* scale,
+                                   hipStream_t stream);
+// C [capacity, N] bf16 over the segments of offsets (NULL: one segment).
+// rows_hint: rows a segment is expected to hold; it picks the kernel, any
+// segment lengths give the same bits.
+hipError_t launch_gemm_i8(const int8_t* A, const float* sa, const int32_t* offsets, int E_local, int64_t capacity,
+                          const int8_t* W, const float* sw, int K, int N, uint16_t* C, int64_t rows_hint,
+                          hipStream_t stream);
+// h [capacity, I] float32 = silu(gate) * up, W [E_local, 2 I, H]; row n of a
+// segment is row gather_src[n] / gather_k of A when gather_src is given.
+hipError_t launch_gate_up_i8(const int8_t* A, const float* sa, const int32_t* gather_src, int gather_k,
+                             int gather_rows, const int32_t* offsets, int E_local, int64_t capacity, const int8_t* W,
+                             const float* sw, int H, int I, float* h, int64_t rows_hint, hipStream_t stream);
+
 // Cached device facts of the current device.
 int device_cu_count();
 

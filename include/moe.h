@@ -314,6 +314,74 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
                                  size_t* offsets_out);
 
 /* ------------------------------------------------------------------------ */
+/* 8-bit integer products with a scale per token and per weight channel.     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * x [M, K] bf16 -> q [M, K] int8 and scale [M] f32, per row:
+ *   top = max |x[m]|,  scale = top / 127,  q = 127 x / top to the nearest
+ *   integer, halves to even; a row of zeros gets q = 0, scale = 0.
+ * A row that holds an infinity or a NaN gets q = 0 and scale = inf or NaN, so
+ * that whatever is computed from it is NaN. K is a multiple of 16; x and q are
+ * 16-byte aligned. M < 2^31, M = 0 is a no-op.
+ */
+int moe_quantize_rows(const moe_bf16* x, int64_t M, int K, int8_t* q, float* scale, hipStream_t stream);
+
+/*
+ * Weights w [E_local, K, N] bf16 (the layout of w_gate_up and w_down) ->
+ * q [E_local, N, K] int8 (a channel per row) and scale [E_local, N] f32, each
+ * channel as moe_quantize_rows treats a row. Run once per set of weights.
+ * K is a multiple of 16, N of 8, E_local <= 1024; w and q are 16-byte aligned.
+ */
+int moe_quantize_weights(const moe_bf16* w, int E_local, int K, int N, int8_t* q, float* scale, hipStream_t stream);
+
+/*
+ * out[m, n] = (sum_k a[m, k] w[e, n, k]) a_scale[m] w_scale[e, n], rounded once
+ * to bf16, for the rows m of segment e; the integer sum is exact.
+ *   a       [capacity, K] int8, a_scale [capacity] f32
+ *   offsets [E_local+1] i32 DEVICE memory as for moe_expert_ffn, or NULL with
+ *           E_local = 1: all capacity rows
+ *   w       [E_local, N, K] int8, w_scale [E_local, N] f32
+ *   out     [capacity, N] bf16 OUT; rows >= offsets[E_local] untouched
+ * K is a multiple of 16 and below 131072, N a multiple of 8, N * K < 2^31,
+ * E_local <= 1024, capacity < 2^31; a, w, w_scale and out are 16-byte aligned.
+ */
+int moe_gemm_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, const int8_t* w, const float* w_scale,
+                int64_t capacity, int N, int K, int E_local, moe_bf16* out, hipStream_t stream);
+
+/*
+ * moe_expert_ffn with 8-bit weights and activations:
+ *   h[n]   = silu(g) * u, g and u the two halves of the product of
+ *            quantised x_perm[n] with w_gate_up[e] (float32, scaled)
+ *   out[n] = quantised h[n] times w_down[e]         (bf16)
+ * x_perm and h are quantised per row as by moe_quantize_rows; h stays float32
+ * until then.
+ *   w_gate_up [E_local, 2I, H] int8 (channels [0, I) gate, [I, 2I) up),
+ *   s_gate_up [E_local, 2I] f32, w_down [E_local, H, I] int8, s_down
+ *   [E_local, H] f32: what moe_quantize_weights makes of moe_expert_ffn's.
+ * H and I are multiples of 16 below 131072, H * 2I < 2^31. workspace:
+ * moe_expert_ffn_i8_workspace_size bytes, 256-byte aligned. Other arguments
+ * and checks as for moe_expert_ffn.
+ */
+size_t moe_expert_ffn_i8_workspace_size(int H, int I, int64_t capacity);
+int moe_expert_ffn_i8(const moe_bf16* x_perm, const int32_t* offsets, const int8_t* w_gate_up,
+                      const float* s_gate_up, const int8_t* w_down, const float* s_down, int H, int I, int E_local,
+                      int64_t capacity, moe_bf16* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_forward with the expert MLPs of moe_expert_ffn_i8. The router stays
+ * float32 on bf16 x; each token is quantised once, before it is dispatched.
+ * T * H < 2^31 (the token vectors are read in place), else
+ * MOE_ERR_UNSUPPORTED; workspace: moe_forward_i8_workspace_size bytes,
+ * 256-byte aligned. Other arguments and checks as for moe_forward.
+ */
+size_t moe_forward_i8_workspace_size(int T, int H, int I, int E, int k, int E_local);
+int moe_forward_i8(const moe_bf16* x, const float* w_router, const float* bias, const int8_t* w_gate_up,
+                   const float* s_gate_up, const int8_t* w_down, const float* s_down, int T, int H, int I, int E,
+                   int k, int e0, int E_local, int renormalize, moe_bf16* y, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Norms before and after the block, with its gate and residual scale.       */
 /* ------------------------------------------------------------------------ */
 

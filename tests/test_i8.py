@@ -1,0 +1,352 @@
+"""The 8-bit integer products (moe_quantize_rows, moe_quantize_weights,
+moe_gemm_i8, moe_expert_ffn_i8, moe_forward_i8) against their formulas in
+64 bits, and their refusals.
+
+The integer sums are exact in the kernels and in float64 (below 2^31), so a
+product's error is the conversion of the sum to float32, the product of the
+two scales, their product with it (2^-24 each) and the rounding to bf16
+(2^-8): 2^-8 + 4 x 2^-24 relative.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import expert_token_routing_amd as M
+
+BF, F32, F64, I8 = torch.bfloat16, torch.float32, torch.float64, torch.int8
+REL = 2.0 ** -8 + 4 * 2.0 ** -24
+FAKE = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10004)
+WS = ctypes.c_void_p(0x100000)
+gpu = pytest.mark.gpu
+OK, INV, UNS, WSP = M.MOE_OK, M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED, M.MOE_ERR_WORKSPACE
+
+
+# --------------------------------------------------------------------------- #
+# Refusals (CPU)                                                               #
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("args,want", [
+    ((FAKE, -1, 32, FAKE, FAKE, None), INV), ((FAKE, 4, 0, FAKE, FAKE, None), INV), ((FAKE, 4, 24, FAKE, FAKE, None), INV),
+    ((FAKE, 1 << 31, 32, FAKE, FAKE, None), UNS), ((None, 4, 32, FAKE, FAKE, None), INV),
+    ((FAKE, 4, 32, None, FAKE, None), INV), ((FAKE, 4, 32, FAKE, None, None), INV), ((ODD, 4, 32, FAKE, FAKE, None), INV),
+    ((FAKE, 4, 32, ODD, FAKE, None), INV), ((None, 0, 32, None, None, None), OK),
+])
+def test_quantize_rows_rejects(args, want):
+    assert M.lib().moe_quantize_rows(*args) == want
+
+
+@pytest.mark.parametrize("args,want", [
+    ((FAKE, 0, 32, 8, FAKE, FAKE, None), INV), ((FAKE, 1, 24, 8, FAKE, FAKE, None), INV),
+    ((FAKE, 1, 32, 12, FAKE, FAKE, None), INV), ((FAKE, 2000, 32, 8, FAKE, FAKE, None), UNS),
+    ((FAKE, 1, 131072, 8, FAKE, FAKE, None), UNS), ((FAKE, 1, 65536, 32768, FAKE, FAKE, None), UNS),
+    ((None, 1, 32, 8, FAKE, FAKE, None), INV), ((ODD, 1, 32, 8, FAKE, FAKE, None), INV),
+    ((FAKE, 1, 32, 8, FAKE, None, None), INV),
+])
+def test_quantize_weights_rejects(args, want):
+    assert M.lib().moe_quantize_weights(*args) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(E=0), INV), (dict(cap=-1), INV), (dict(K=8), INV), (dict(N=12), INV), (dict(N=0), INV), (dict(K=131072), UNS),
+    (dict(K=65536, N=32768), UNS), (dict(E=1025), UNS), (dict(cap=1 << 31), UNS), (dict(E=2, off=None), INV),
+    (dict(a=None), INV), (dict(s=None), INV), (dict(w=None), INV), (dict(ws=None), INV), (dict(out=None), INV),
+    (dict(a=ODD), INV), (dict(w=ODD), INV), (dict(ws=ODD), INV), (dict(out=ODD), INV), (dict(cap=0, a=None), OK),
+])
+def test_gemm_i8_rejects(kw, want):
+    d = dict(a=FAKE, s=FAKE, off=FAKE, w=FAKE, ws=FAKE, cap=8, N=16, K=32, E=2, out=FAKE)
+    d.update(kw)
+    assert M.lib().moe_gemm_i8(d["a"], d["s"], d["off"], d["w"], d["ws"], d["cap"], d["N"], d["K"], d["E"], d["out"],
+                               None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(E=0), INV), (dict(H=24), INV), (dict(I=24), INV), (dict(cap=-1), INV), (dict(E=1025), UNS),
+    (dict(H=65536, I=16384), UNS), (dict(x=None), INV), (dict(off=None), INV), (dict(sd=None), INV), (dict(gu=ODD), INV),
+    (dict(sg=ODD), INV), (dict(wsb=100), WSP), (dict(ws=None), WSP), (dict(ws=ctypes.c_void_p(0x100010)), WSP),
+    (dict(cap=0, x=None, ws=None), OK),
+])
+def test_expert_ffn_i8_rejects(kw, want):
+    d = dict(x=FAKE, off=FAKE, gu=FAKE, sg=FAKE, dn=FAKE, sd=FAKE, H=32, I=16, E=2, cap=8, out=FAKE, ws=WS, wsb=1 << 20)
+    d.update(kw)
+    assert M.lib().moe_expert_ffn_i8(d["x"], d["off"], d["gu"], d["sg"], d["dn"], d["sd"], d["H"], d["I"], d["E"],
+                                     d["cap"], d["out"], d["ws"], d["wsb"], None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(H=24), INV), (dict(I=8), INV), (dict(k=0), INV), (dict(k=9), INV), (dict(e0=7), INV), (dict(y=None), INV),
+    (dict(sg=None), INV), (dict(dn=ODD), INV), (dict(wsb=64), WSP), (dict(T=1 << 26, H=32), UNS), (dict(E=2000, k=2), UNS),
+    (dict(T=0, x=None, y=None), OK),
+])
+def test_forward_i8_rejects(kw, want):
+    d = dict(x=FAKE, r=FAKE, gu=FAKE, sg=FAKE, dn=FAKE, sd=FAKE, T=8, H=32, I=16, E=8, k=2, e0=0, El=4, y=FAKE, ws=WS,
+             wsb=1 << 30)
+    d.update(kw)
+    assert M.lib().moe_forward_i8(d["x"], d["r"], None, d["gu"], d["sg"], d["dn"], d["sd"], d["T"], d["H"], d["I"], d["E"],
+                                  d["k"], d["e0"], d["El"], 1, d["y"], d["ws"], d["wsb"], None) == want
+
+
+def test_i8_reject_mismatched_tensors():
+    a, w = torch.zeros(4, 32, dtype=I8), torch.zeros(2, 16, 32, dtype=I8)
+    s, sw, off = torch.zeros(4), torch.zeros(2, 16), torch.zeros(3, dtype=torch.int32)
+    for args, exc, match in (((a, s, w, sw), ValueError, "offsets is required"),
+                             ((a, s, w[:, :, :16], sw, off), ValueError, "w has shape"),
+                             ((a, s[:3], w, sw, off), ValueError, "a_scale has shape"),
+                             ((a, s, w, sw[:1], off), ValueError, "w_scale has shape"),
+                             ((a, s, w, sw, off[:2]), ValueError, "offsets has shape"),
+                             ((a.to(torch.int16), s, w, sw, off), TypeError, "a must be"),
+                             ((a, s, w, sw, off), ValueError, "must live on a GPU")):
+        with pytest.raises(exc, match=match):
+            M.moe_gemm_i8(*args)
+    with pytest.raises(TypeError, match="x must be"):
+        M.moe_quantize_rows(a)
+    with pytest.raises(ValueError, match="scale has shape"):
+        M.moe_quantize_rows(a.to(BF), scale=torch.zeros(5))
+    with pytest.raises(ValueError, match="q has shape"):
+        M.moe_quantize_weights(torch.zeros(2, 32, 16, dtype=BF), q=torch.zeros(2, 32, 16, dtype=I8))
+    x = torch.zeros(4, 32, dtype=BF)
+    dn, sd = torch.zeros(2, 32, 8, dtype=I8), torch.zeros(2, 32)
+    with pytest.raises(ValueError, match="w_down has shape"):
+        M.moe_expert_ffn_i8(x, off, w, sw, dn[:, :16], sd)
+    with pytest.raises(ValueError, match="s_down has shape"):
+        M.moe_expert_ffn_i8(x, off, w, sw, dn, sd[:, :16])
+    with pytest.raises(ValueError, match="k must be"):
+        M.moe_forward_i8(x, torch.zeros(4, 32), None, w, sw, dn, sd, 5, 0)
+    with pytest.raises(ValueError, match="local experts"):
+        M.moe_forward_i8(x, torch.zeros(4, 32), None, w, sw, dn, sd, 2, 3)
+
+
+# --------------------------------------------------------------------------- #
+# The kernels (GPU)                                                            #
+# --------------------------------------------------------------------------- #
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rand_i8(g, *shape):
+    return torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int32).to(I8)
+
+
+def _quantized(x):
+    """q (exactly rounded) and scale of the rows of x in 64 bits (torch divides
+    float32 tensors by a number with its reciprocal, which is not rounded right)."""
+    top = x.to(F64).abs().amax(-1, keepdim=True)
+    q = torch.round(x.to(F64) * 127 / torch.where(top > 0, top, 1.0))  # the quotient of two bf16 is a half or 2^-9 off
+    return q, top[..., 0] / 127
+
+
+def _close(got, ref, rel, what):
+    err, tol = (got.to(F64) - ref).abs(), rel * ref.abs() + 1e-37
+    worst = float((err / tol).max()) if ref.numel() else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.2f} of the tolerance"
+
+
+@gpu
+@pytest.mark.parametrize("M_,K", [(1, 16), (1, 7168), (3, 48), (700, 2880), (600, 2048), (1025, 8192), (5, 32768),
+                                  (2, 40000), (600, 9600)])
+def test_quantize_rows(M_, K):
+    g = _gen(1)
+    x = torch.randn((M_, K), generator=g, device="cuda")
+    x = (x * 10.0 ** torch.randint(-36, 37, (M_, 1), generator=g, device="cuda")).to(BF)
+    x[M_ // 2] = 0
+    # exact halves: a row of multiples of 1/254 of its largest value
+    if M_ > 4:
+        x[0] = (torch.arange(K, device="cuda") % 255 - 127).to(BF) / 2
+        x[0, 0] = 127
+    print(f"[gpu] quantize_rows M={M_} K={K}", flush=True)
+    q, s = M.moe_quantize_rows(x)
+    torch.cuda.synchronize()
+    rq, rs = _quantized(x)
+    assert torch.equal(q.to(F64), rq)
+    assert bool((s == rs.float()).all())
+
+
+@gpu
+def test_quantize_rows_edges():
+    x = torch.ones((6, 64), dtype=BF, device="cuda")
+    x[1, 5] = float("inf")
+    x[2, 7] = float("nan")
+    x[3] = 1e-40                # below the normal numbers
+    x[4] = 3e38
+    x[4, 0] = -3.3e38
+    x[5, 1:] = -0.0
+    x[5, 0] = -2.0 ** -133      # the smallest bf16
+    q, s = M.moe_quantize_rows(x)
+    assert q[0].eq(127).all() and q[1].eq(0).all() and q[2].eq(0).all()
+    assert torch.isinf(s[1]) and torch.isnan(s[2])
+    rq, _ = _quantized(x[3:])
+    assert torch.equal(q[3:].to(F64), rq) and q[5, 0] == -127
+    w = torch.ones((1, 8, 64), dtype=I8, device="cuda")
+    out = M.moe_gemm_i8(q, s, w, torch.ones((1, 8), device="cuda"))
+    assert torch.isnan(out[1:3]).all() and torch.isfinite(out[0]).all()
+    e = M.moe_quantize_rows(torch.empty((0, 64), dtype=BF, device="cuda"))
+    assert e[0].shape == (0, 64) and e[1].shape == (0,)
+
+
+@gpu
+@pytest.mark.parametrize("E,K,N", [(1, 16, 8), (3, 272, 136), (2, 2880, 1000), (1, 7168, 64)])
+def test_quantize_weights(E, K, N):
+    w = torch.randn((E, K, N), generator=_gen(2), device="cuda").to(BF)
+    w[0, :, 3] = 0
+    print(f"[gpu] quantize_weights E={E} K={K} N={N}", flush=True)
+    q, s = M.moe_quantize_weights(w)
+    wt = w.transpose(1, 2).contiguous()
+    rq, rs = _quantized(wt)
+    assert torch.equal(q.to(F64), rq)
+    assert bool((s == rs.float()).all())
+
+
+def _check_gemm(M_, K, N, segs=None, seed=3, value=None):
+    g = _gen(seed)
+    E = 1 if segs is None else len(segs)
+    a = _rand_i8(g, M_, K) if value is None else torch.full((M_, K), value, dtype=I8, device="cuda")
+    w = _rand_i8(g, E, N, K) if value is None else torch.full((E, N, K), value, dtype=I8, device="cuda")
+    sa = torch.rand(M_, generator=g, device="cuda") + 0.01
+    sw = torch.rand((E, N), generator=g, device="cuda") + 0.01
+    off = None
+    if segs is not None:
+        off = torch.tensor([0, *segs], device="cuda").cumsum(0).to(torch.int32)
+    out = torch.full((M_, N), 7.0, dtype=BF, device="cuda")
+    print(f"[gpu] gemm_i8 M={M_} K={K} N={N} segs={segs}", flush=True)
+    got = M.moe_gemm_i8(a, sa, w, sw, off, out=out)
+    torch.cuda.synchronize()
+    assert got is out
+    at = 0
+    for e, m in enumerate([M_] if segs is None else segs):
+        ref = (a[at:at + m].to(F64) @ w[e].to(F64).T) * sa[at:at + m, None].to(F64) * sw[e].to(F64)
+        _close(out[at:at + m], ref, REL, f"segment {e}")
+        at += m
+    assert out[at:].eq(7.0).all(), "rows behind the last segment were written"
+
+
+@gpu
+@pytest.mark.parametrize("M_", [1, 15, 16, 17, 33, 64, 65, 100, 333])
+@pytest.mark.parametrize("K,N", [(16, 8), (48, 24), (144, 136), (1008, 520), (2880, 1536)])
+def test_gemm_i8_small(M_, K, N):
+    _check_gemm(M_, K, N)
+
+
+@gpu
+@pytest.mark.parametrize("M_,K,N", [(2049, 272, 4096), (4096, 128, 4104), (1000, 1024, 4096), (8192, 400, 2048),
+                                    (600, 7168, 1024), (1, 7168, 4096), (64, 131056, 8)])
+def test_gemm_i8_large(M_, K, N):
+    _check_gemm(M_, K, N)
+
+
+@gpu
+@pytest.mark.parametrize("segs,K,N,behind", [
+    ([3, 0, 1, 16, 17, 33, 0], 208, 72, 9),           # few rows: one skinny pass, several for the longest
+    ([90, 0, 1, 300, 64, 65, 5, 0], 272, 264, 0),     # small tiles
+    ([200, 0, 129, 1, 500, 128], 400, 2056, 70),      # middle tiles
+    ([600, 0, 17, 289, 1000, 576, 1, 2000], 272, 4096, 11),  # the largest tiles, every block height
+    ([0, 0, 0], 64, 64, 40),                          # no rows at all
+], ids=["skinny", "small", "mid", "big", "none"])
+def test_gemm_i8_segments(segs, K, N, behind):
+    _check_gemm(sum(segs) + behind, K, N, segs)
+
+
+@gpu
+@pytest.mark.parametrize("M_", [3, 100])
+def test_gemm_i8_largest_sum(M_):
+    """-128 x -128 over the longest k: 2^14 x 131056, just below 2^31."""
+    _check_gemm(M_, 131056, 8, value=-128)
+
+
+def _layout(cap, x_rows, H, I):
+    at, out = 0, {}
+    for name, nbytes in (("xq", x_rows * H), ("xs", 4 * x_rows), ("h", 4 * cap * I), ("hq", cap * I), ("hs", 4 * cap)):
+        out[name] = (at, nbytes)
+        at += -(-nbytes // 256) * 256
+    return out
+
+
+def _weights(g, E, H, I):
+    gu = (torch.randn((E, H, 2 * I), generator=g, device="cuda") / H ** 0.5).to(BF)
+    dn = (torch.randn((E, I, H), generator=g, device="cuda") / I ** 0.5).to(BF)
+    return (*M.moe_quantize_weights(gu), *M.moe_quantize_weights(dn))
+
+
+@gpu
+@pytest.mark.parametrize("segs,H,I,behind", [
+    ([1], 16, 16, 0),
+    ([2, 0, 1, 5, 16], 272, 48, 3),
+    ([30, 17, 0, 9], 2880, 768, 0),
+    ([100, 1, 0, 240], 144, 208, 5),
+    ([700, 300, 0, 33, 600], 208, 400, 2),
+    ([520, 480, 0, 700, 511, 512, 513, 1], 256, 2048, 0),
+], ids=["one", "few", "decode", "small", "mid", "big"])
+def test_expert_ffn_i8(segs, H, I, behind):
+    g = _gen(4)
+    E, cap = len(segs), sum(segs) + behind
+    x = torch.randn((cap, H), generator=g, device="cuda").to(BF)
+    guq, gus, dnq, dns = _weights(g, E, H, I)
+    off = torch.tensor([0, *segs], device="cuda").cumsum(0).to(torch.int32)
+    out = torch.full((cap, H), 7.0, dtype=BF, device="cuda")
+    print(f"[gpu] expert_ffn_i8 segs={segs} H={H} I={I}", flush=True)
+    got, ws = M.moe_expert_ffn_i8(x, off, guq, gus, dnq, dns, out=out)
+    torch.cuda.synchronize()
+    lay = _layout(cap, cap, H, I)
+    n = sum(segs)
+
+    def part(name, dtype, *shape):
+        a, b = lay[name]
+        return ws[a:a + b].view(dtype).reshape(shape)[:n]
+
+    xq, xs = part("xq", I8, cap, H), part("xs", F32, cap)
+    rq, _ = _quantized(x[:n])
+    assert torch.equal(xq.to(F64), rq)
+    h, hq, hs = part("h", F32, cap, I), part("hq", I8, cap, I), part("hs", F32, cap)
+    at = 0
+    for e, m in enumerate(segs):
+        s = slice(at, at + m)
+        gu = (xq[s].to(F64) @ guq[e].to(F64).T) * xs[s, None].to(F64) * gus[e].to(F64)
+        ga, up = gu[:, :I], gu[:, I:]
+        ref = ga * torch.sigmoid(ga) * up
+        # g and u: 3 steps of 2^-24 each; exp: |g| steps from its argument and
+        # two of its own; the sum, quotient and product: one each
+        tol = (12 + ga.abs()) * 2.0 ** -23 * (ga * up).abs() + 1e-37
+        assert float(((h[s].to(F64) - ref).abs() / tol).max() if m else 0) <= 1.0, f"h of segment {e}"
+        top = h[s].abs().amax(-1, keepdim=True).to(F64) if m else h[s].to(F64)
+        if m:
+            # three float32 steps of a value up to 127: below 2^-15
+            assert float((hq[s].to(F64) - 127 * h[s].to(F64) / top).abs().max()) <= 0.5 + 2.0 ** -15
+            assert bool((hs[s] == (top[:, 0] / 127).float()).all())
+        _close(out[s], (hq[s].to(F64) @ dnq[e].to(F64).T) * hs[s, None].to(F64) * dns[e].to(F64), REL, f"out {e}")
+        at += m
+    assert out[n:].eq(7.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,E,k,e0,El", [(1, 128, 32, 8, 2, 0, 8), (50, 272, 48, 12, 3, 4, 5), (900, 256, 400, 16, 4, 3, 6),
+                                             (3000, 1024, 2048, 8, 2, 0, 8)])
+def test_forward_i8_equals_its_steps(T, H, I, E, k, e0, El):
+    g = _gen(5)
+    x = (torch.randn((T, H), generator=g, device="cuda") / H ** 0.5).to(BF)
+    wr = torch.randn((E, H), generator=g, device="cuda")
+    w = _weights(g, El, H, I)
+    print(f"[gpu] forward_i8 T={T} H={H} I={I} E={E}", flush=True)
+    y, ws = M.moe_forward_i8(x, wr, None, *w, k, e0)
+    lg, idx, tw = M.moe_route(x, wr, None, k)
+    counts, off, perm, inv, xp = M.moe_dispatch(x, idx, E, e0, El)
+    out, _ = M.moe_expert_ffn_i8(xp, off, *w)
+    ref = M.moe_combine(out, inv, tw)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+    # captured and replayed, on a workspace full of other values
+    y2 = torch.empty_like(y)
+    graph = torch.cuda.CUDAGraph()
+    ws.fill_(0x5A)
+    with torch.cuda.graph(graph):
+        M.moe_forward_i8(x, wr, None, *w, k, e0, y=y2, workspace=ws)
+    for _ in range(3):
+        y2.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y2.view(torch.int16), ref.view(torch.int16))
+        M.moe_forward_i8(x, wr, None, *w, k, e0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y3, _ = M.moe_forward_i8(x, wr, None, *w, k, e0, stream=side)
+    side.synchronize()
+    assert torch.equal(y3.view(torch.int16), ref.view(torch.int16))
+    assert M.moe_forward_i8(x[:0], wr, None, *w, k, e0)[0].shape == (0, H)
