@@ -98,19 +98,26 @@ def check(status: int, where: str) -> None:
 # --------------------------------------------------------------------------- #
 # torch-facing wrappers                                                        #
 # --------------------------------------------------------------------------- #
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle itself: building the torch.cuda.Stream around it takes 3 us
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t, dtype, name, shape=None, dev=None, min_rows=False):
@@ -125,10 +132,14 @@ def _need(t, dtype, name, shape=None, dev=None, min_rows=False):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None:
+    if shape is not None and t.shape != shape:
         got = tuple(t.shape)
-        ok = len(got) == len(shape) and all(
-            want is None or g == want or (min_rows and i == 0 and g >= want) for i, (g, want) in enumerate(zip(got, shape)))
+        ok = len(got) == len(shape)
+        if ok:
+            for i, want in enumerate(shape):
+                if want is not None and got[i] != want and not (min_rows and i == 0 and got[i] >= want):
+                    ok = False
+                    break
         if not ok:
             want_s = "(" + ", ".join("*" if v is None else (f">={v}" if min_rows and i == 0 else str(v))
                                      for i, v in enumerate(shape)) + ")"
@@ -138,14 +149,13 @@ def _need(t, dtype, name, shape=None, dev=None, min_rows=False):
 def _placed(dev, **tensors):
     """Every given tensor (None: skipped) is contiguous and on the GPU dev."""
     for name, t in tensors.items():
-        if t is None:
+        if t is None or (t.is_cuda and t.device == dev and t.is_contiguous()):
             continue
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if not t.is_cuda:
             raise ValueError(f"{name} must live on a GPU (this library has no CPU path)")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
 
 
 def _nbytes(t):
