@@ -46,6 +46,11 @@ SIGNATURES = {
                                            c_int, _P, _P, c_size_t, _P, _P]),
     "moe_forward_noalloc": (c_int, [_P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                     _P, _P]),
+    "moe_few_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "moe_forward_few": (c_int, [_P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                _P, _P, c_size_t, _P]),
+    "moe_forward_few_f32": (c_int, [_P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                    _P, _P, c_size_t, _P]),
     "moe_quantize_rows": (c_int, [_P, c_int64, c_int, _P, _P, _P]),
     "moe_quantize_weights": (c_int, [_P, c_int, c_int, c_int, _P, _P, _P]),
     "moe_gemm_i8": (c_int, [_P, _P, _P, _P, _P, c_int64, c_int, c_int, c_int, _P, _P]),
@@ -58,6 +63,8 @@ SIGNATURES = {
     "moe_norm_post": (c_int, [_P, c_int, _P, c_int, _P, _P, c_int, c_float, _P, c_float, c_int, c_int, _P, _P, _P]),
 }
 
+# most tokens of moe_forward_few (MOE_FEW_TOKENS)
+FEW_TOKENS = 32
 # bytes of the static scratch moe_forward_noalloc works in (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
@@ -539,6 +546,43 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
                              _ptr(w_next), eps, T, H, _ptr(out), _ptr(normed), _stream(None, dev))
     check(st, "moe_norm_post")
     return out, normed
+
+
+# --------------------------------------------------------------------------- #
+# The whole share for a few tokens                                             #
+# --------------------------------------------------------------------------- #
+def few_workspace_size(T, H, I, E, k, E_local) -> int:
+    """Bytes of workspace moe_forward_few needs (0 where T > FEW_TOKENS)."""
+    return int(lib().moe_few_workspace_size(T, H, I, E, k, E_local))
+
+
+def _few(name, out_dtype, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y, workspace):
+    T, H, I, E, E_local, dev = _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
+    if y is not None:
+        _need(y, out_dtype, "y", (T, H))
+    _forward_placed(dev, x, w_router, bias, w_gate_up, w_down)
+    y = _out(y, (T, H), out_dtype, dev, "y")
+    L = lib()
+    ws = _workspace(L.moe_few_workspace_size(T, H, I, E, k, E_local), dev, workspace)
+    st = getattr(L, name)(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down), T, H, I, E, k, e0,
+                          E_local, int(bool(renormalize)), _ptr(y), _ptr(ws), _nbytes(ws), _stream(None, dev))
+    check(st, name)
+    return y, ws
+
+
+@_on_stream
+def moe_forward_few(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None):
+    """moe_forward for at most FEW_TOKENS tokens in two kernels: y [T, H] bf16,
+    rounded once. Returns (y, workspace). Takes ``stream``."""
+    return _few("moe_forward_few", _torch().bfloat16, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
+                workspace)
+
+
+@_on_stream
+def moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None):
+    """moe_forward_few with the share kept in float32 (y [T, H] float32)."""
+    return _few("moe_forward_few_f32", _torch().float32, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
+                workspace)
 
 
 # --------------------------------------------------------------------------- #

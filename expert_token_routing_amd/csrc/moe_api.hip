@@ -349,6 +349,44 @@ int moe_forward_fused_profiled(const moe_bf16* x, const float* w_router, const f
                       workspace, workspace_bytes, events, stream, true);
 }
 
+size_t moe_few_workspace_size(int T, int H, int I, int E, int k, int E_local) {
+  if (T < 0 || T > MOE_FEW_TOKENS || H <= 0 || I <= 0 || E <= 0 || k <= 0 || E_local <= 0) return 0;
+  return few_workspace_bytes(T, H, I, E, k, E_local);
+}
+
+static int few_impl(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                    const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
+                    void* y, bool y_f32, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
+  if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+      workspace_bytes < few_workspace_bytes(T, H, I, E, k, E_local))
+    return MOE_ERR_WORKSPACE;
+  return hip_status(launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, y_f32,
+                               static_cast<char*>(workspace), stream));
+}
+
+int moe_forward_few(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                    const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
+                    moe_bf16* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return few_impl(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, false, workspace,
+                  workspace_bytes, stream);
+}
+
+int moe_forward_few_f32(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                        const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
+                        int renormalize, float* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return few_impl(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, true, workspace,
+                  workspace_bytes, stream);
+}
+
 // Sizes of the 8-bit products: an exact int32 sum needs K < 2^17; 32-bit
 // offsets into one expert's matrix need rows * K < 2^31.
 static int check_i8(int K, int64_t channels) {

@@ -314,6 +314,37 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
                                  size_t* offsets_out);
 
 /* ------------------------------------------------------------------------ */
+/* The whole share for a few tokens, in two kernels.                         */
+/* ------------------------------------------------------------------------ */
+
+/* Most tokens of moe_forward_few. */
+#define MOE_FEW_TOKENS 32
+
+/*
+ * moe_forward for at most MOE_FEW_TOKENS tokens, where reading the used
+ * experts' weights is the whole cost: one kernel for the router's logits, one
+ * for selection, expert MLPs and the weighted return. Arguments and checks are
+ * moe_forward's; T > MOE_FEW_TOKENS is MOE_ERR_UNSUPPORTED. workspace:
+ * moe_few_workspace_size bytes, 256-byte aligned; no part of it needs to start
+ * at zero. Calls that overlap need workspaces of their own.
+ *   - the logits are float32 sums as in moe_route, added in another order, so
+ *     a selection can differ from moe_forward's where two logits are equal to
+ *     within float32 rounding;
+ *   - h and the expert outputs stay float32 (moe_forward rounds both to bf16),
+ *     so y is rounded once;
+ *   - two calls with the same arguments give the same bits.
+ */
+size_t moe_few_workspace_size(int T, int H, int I, int E, int k, int E_local);
+int moe_forward_few(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                    const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
+                    moe_bf16* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* moe_forward_few whose share y [T, H] is float32, as moe_forward_f32's. */
+int moe_forward_few_f32(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                        const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
+                        int renormalize, float* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* 8-bit integer products with a scale per token and per weight channel.     */
 /* ------------------------------------------------------------------------ */
 
