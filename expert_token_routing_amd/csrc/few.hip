@@ -6,28 +6,34 @@
 // and the six launches of the general path cost more than reading them. Here
 // few_logits_kernel scores the tokens and few_experts_kernel does the rest:
 // every workgroup picks the tokens' experts for itself (a few thousand logits)
-// and then takes items from one queue, first all gate/up items, then all down
-// items:
+// and then takes items from queues, first all gate/up items, then all down
+// items, then the weighted return:
 //
-//   gate/up item  (expert, k range, 64 outputs)   -> float32 partial sums; the
-//                 last of an output panel's k ranges adds them in order and
-//                 writes h = silu(g) * u
-//   down item     (expert, k range, 128 outputs)  -> float32 partial sums; the
-//                 last of an output panel's items adds them per token, slot by
-//                 slot, and writes y
+//   gate/up item  (expert, k range, 128 gate or up columns) -> float32 partial
+//                 sums; the last of a block of 128 outputs adds its k ranges
+//                 and writes h = silu(g) * u
+//   down item     (expert, k range, 128 outputs)  -> float32 partial sums
+//   return item   (8 tokens, 128 outputs): adds the partial sums per token,
+//                 slot by slot, weighted, and writes y
 //
-// An item's four waves share its k range and its 128 weight columns; a wave
-// streams the weights into registers in the grouped GEMV's geometry
-// (grouped_gemv.hip: 8 rows x 8 columns per lane and step, transposed in
-// registers, v_mfma_f32_16x16x32_bf16 with the weights as the A operand) and
-// the waves' sums meet in LDS. Two workgroups per CU, so that one streams
-// while the other exchanges its sums. A down item asks for its weights before
-// it waits for h.
+// An item's four waves share its k range and its 128 weight columns (256-byte
+// pieces of every weight row); a wave streams the weights into registers in the
+// grouped GEMV's geometry (grouped_gemv.hip: 8 rows x 8 columns per lane and
+// step, transposed in registers, v_mfma_f32_16x16x32_bf16 with the weights as
+// the A operand) and the waves' sums meet in LDS. Two workgroups per CU, so
+// that one streams while the other exchanges its sums. A down item asks for
+// its weights before it waits for h.
 //
-// Waiting is safe however many workgroups run at a time and whatever else the
-// GPU runs: items are handed out in order, a gate/up item waits for nothing,
-// and a down item waits only for gate/up items, all of which were handed out
-// before it to workgroups that are running.
+// Each kind's items lie in eight queues of consecutive items, one per XCD (every
+// operation on a counter's line takes its turn: 512 workgroups on one counter
+// were served in 7 us; every eighth item to an XCD left it a few 256-byte
+// columns of every weight row, and so a few of its L2's channels). A workgroup
+// takes its own queue's gate/up items, then its down items, then its return
+// items. Waiting is safe however many workgroups run at a time and whatever
+// else the GPU runs: a gate/up item waits for nothing; a workgroup that has
+// waited for kSpins polls puts its item aside and takes what the other queues
+// still hold of the kinds before it, gate/up items first, so all items that
+// anybody waits for are with workgroups that are running.
 //
 // Sums are added in a fixed order by whichever workgroup is last, so y does
 // not depend on the order of the items. h stays float32: it is multiplied as
@@ -54,9 +60,13 @@ constexpr int kMaxSel = 1024;  // T k
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kSub = 512;       // k of a unit: 4 steps of 32 for each of the 4 waves
 constexpr int kCols = 128;      // weight columns of an item
-constexpr int kGateUp = 64;     // outputs of a gate/up item (gate and up columns)
 constexpr int kStride = kCols + 4;
-constexpr int kFewItems = 2048;  // items an operand is cut into where k allows (four per workgroup)
+constexpr int kBatch = 8;       // exchanged values asked for at a time
+constexpr int kTokens = 8;      // tokens of a return item
+constexpr int kItems = 2048;    // items an operand is cut into where k allows (four per workgroup)
+constexpr int kQueues = 8;      // of each kind of item, one per XCD (workgroup b runs on XCD b % 8)
+constexpr int kPitch = 32;      // ints between counters: a 128-byte line each
+constexpr int kSpins = 4096;    // polls before a waiting workgroup looks for items (some 2 ms)
 constexpr int kCoherent = 16;   // buffer cache policy sc1: agent scope
 constexpr int kStream = 2;      // nt: each weight byte is read once
 constexpr uint32_t kOutside = 0x80000000u;  // offset past every buffer: reads zero
@@ -68,11 +78,12 @@ struct Args {
   const uint16_t* w_down;
   int T, H, I, E, k, e0, E_local, renormalize, y_f32;
   void* y;
-  int* ticket;    // next item
-  int* cnt_a;     // [expert][gate/up panel]: k ranges done
-  int* cnt_h;     // [expert][512 of I]: panels of h written
+  // counters, kPitch apart
+  int* queue;     // [kind][queue]: items handed out
+  int* cnt_a;     // [expert][128 of I]: gate and up items done
+  int* cnt_h;     // [expert][512 of I]: blocks of h written
   int* cnt_b;     // [down panel]: items done
-  float* part_a;  // [row][k range][panel][128]
+  float* part_a;  // [row][k range][gate panels, up panels][128]
   float* part_b;  // [row][k range][H]
   float* h;       // [row][I]
 };
@@ -84,7 +95,7 @@ struct Split {
 };
 __host__ __device__ inline Split split(int K, int items) {
   const int u = (K + kSub - 1) / kSub;
-  const int want = items >= kFewItems ? 1 : (kFewItems + items - 1) / items;
+  const int want = items >= kItems ? 1 : (kItems + items - 1) / items;
   const int units = want >= u ? 1 : (u + want - 1) / want;
   return {units, (u + units - 1) / units};
 }
@@ -106,18 +117,21 @@ __global__ void __launch_bounds__(kThreads) few_logits_kernel(const uint16_t* x,
   for (int t = 0; t < TB; ++t) acc[t] = 0.f;
   for (int k = 4 * int(threadIdx.x); k < H; k += 4 * kThreads) {
     const float4 wv = *reinterpret_cast<const float4*>(w + int64_t(e) * H + k);
+    uint2 xv[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) xv[t] = *reinterpret_cast<const uint2*>(x + int64_t(min(t, T - 1)) * H + k);
+    __builtin_amdgcn_sched_barrier(0);  // all loads in flight before the first product
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
-      const uint2 xv = *reinterpret_cast<const uint2*>(x + int64_t(min(t, T - 1)) * H + k);
-      acc[t] = fmaf(bf16_lo(xv.x), wv.x, acc[t]);
-      acc[t] = fmaf(bf16_hi(xv.x), wv.y, acc[t]);
-      acc[t] = fmaf(bf16_lo(xv.y), wv.z, acc[t]);
-      acc[t] = fmaf(bf16_hi(xv.y), wv.w, acc[t]);
+      acc[t] = fmaf(bf16_lo(xv[t].x), wv.x, acc[t]);
+      acc[t] = fmaf(bf16_hi(xv[t].x), wv.y, acc[t]);
+      acc[t] = fmaf(bf16_lo(xv[t].y), wv.z, acc[t]);
+      acc[t] = fmaf(bf16_hi(xv[t].y), wv.w, acc[t]);
     }
   }
 #pragma unroll
   for (int t = 0; t < TB; ++t) {
-    const float v = wave_sum(acc[t]);
+    const float v = wave_sum_dpp(acc[t]);
     if (lane_id() == 0) s[threadIdx.x >> 6][t] = v;
   }
   __syncthreads();
@@ -138,6 +152,9 @@ __device__ __forceinline__ float2 get2(const float* p) {
 }
 // this wave's stores have reached the agent's point of coherence
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ int peek(const int* c) {
+  return __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 __device__ __forceinline__ int raise(int* c, int by) {
   return __hip_atomic_fetch_add(c, by, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -154,66 +171,99 @@ struct Tables {
   uint8_t tok[kMaxSel];   // row: its token
 };
 
-// One wave per token: k rounds of the largest live logit, the lowest expert
-// among equal ones; NQ registers per lane, expert l + 64 q.
-template <int NQ>
+// Largest / smallest value over rows of LANES lanes (16 or the whole wave), on
+// every lane of the row: DPP steps inside 16 lanes, then scalar reads.
+template <int LANES, typename Op>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, Op op) {
+  auto step = [&](auto ctrl) {
+    constexpr int c = decltype(ctrl)::value;
+    v = op(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), c, 0xF, 0xF, false)));
+  };
+  step(std::integral_constant<int, 0xB1>{});   // quad_perm [1,0,3,2]
+  step(std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
+  step(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  step(std::integral_constant<int, 0x140>{});  // row_mirror
+  if constexpr (LANES == 64) {
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16),
+                   c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    v = op(op(a, b), op(c, d));
+  }
+  return v;
+}
+
+// A row of LANES lanes per token, expert li + LANES q in register q of lane
+// li: k rounds of the largest logit left, the lowest expert among equal ones.
+// Logits are compared as unsigned keys of the same order (-0 as +0, NaN as
+// -infinity); a taken one becomes 0, below every key. t >= T: nothing is
+// written.
+template <int LANES, int NQ>
 __device__ __forceinline__ void pick(const Args& a, Tables& s, int t) {
-  const int lane = lane_id();
-  float v[NQ];
-  uint32_t live = 0;
+  const int li = lane_id() & (LANES - 1);
+  uint32_t key[NQ];
+  const float* row = a.logits + min(t, a.T - 1) * a.E;
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
-    const int e = lane + 64 * q;
-    v[q] = -INFINITY;
-    if (e < a.E) {
-      const float f = a.logits[t * a.E + e];
-      v[q] = f == f ? f : -INFINITY;
-      live |= 1u << q;
-    }
+    const int e = li + LANES * q;
+    const float f = row[min(e, a.E - 1)] + 0.f;
+    const uint32_t u = __float_as_uint(f == f ? f : -INFINITY);
+    key[q] = e < a.E ? (u >> 31 ? ~u : u | 0x80000000u) : 0u;
   }
-  float top = 0.f, sum = 0.f, mine = 0.f;
-  int my_e = -1;
+  auto value = [](uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); };
+  auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
+  auto smaller = [](uint32_t x, uint32_t y) { return min(x, y); };
+  auto add = [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) + __uint_as_float(y)); };
+  constexpr int KS = LANES == 16 ? 2 : 1;  // selections a lane keeps (k <= 32)
+  uint32_t got[KS] = {}, at[KS] = {};
+  float top = 0.f, all = 0.f;
   for (int j = 0; j < a.k; ++j) {
-    float best = -INFINITY;
-    int at = 1 << 30;
+    uint32_t best = 0, bq = 0;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      if (((live >> q) & 1u) && (v[q] > best || at == 1 << 30)) {
-        best = v[q];
-        at = lane + 64 * q;
+      if (key[q] > best) {
+        best = key[q];
+        bq = q;
       }
-    const float m = wave_max_dpp(best);
-    uint64_t who = ballot(best == m && at != 1 << 30);
-    int e = shfl(at, __builtin_ctzll(who));
-    who &= who - 1;
-    while (who) {
-      e = min(e, shfl(at, __builtin_ctzll(who)));
-      who &= who - 1;
-    }
-    if (e % 64 == lane) live &= ~(1u << (e / 64));
+    const uint32_t m = row_reduce<LANES>(best, larger);
+    const uint32_t mine = best == m ? uint32_t(li) + LANES * bq : 0xFFFFFFFFu;
+    const uint32_t e = row_reduce<LANES>(mine, smaller);
     if (j == 0) {
-      top = m;
+      top = value(m);
       if (!a.renormalize) {
         float z = 0.f;
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
-          if (lane + 64 * q < a.E) z += expf(v[q] - top);
-        sum = wave_sum(z);
+          if (key[q]) z += expf(value(key[q]) - top);
+        all = __uint_as_float(row_reduce<LANES>(__float_as_uint(z), add));
       }
     }
-    const float p = expf(m - top);
-    if (a.renormalize) sum += p;
-    if (lane == j) {
-      mine = p;
-      my_e = e;
-    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      if (mine == e && bq == uint32_t(q)) key[q] = 0;
+#pragma unroll
+    for (int c = 0; c < KS; ++c)
+      if (li + LANES * c == j) {
+        got[c] = m;
+        at[c] = e;
+      }
   }
-  if (lane < a.k) {
-    const int e = my_e - a.e0;
-    const bool local = e >= 0 && e < a.E_local;
-    s.sel[t * a.k + lane] = int16_t(local ? e : -1);
-    s.wt[t * a.k + lane] = mine / sum;
-    if (local) atomicOr(&s.mask[e], 1u << t);
+  float p[KS], sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    p[c] = li + LANES * c < a.k ? expf(value(got[c]) - top) : 0.f;
+    sum += p[c];
+  }
+  sum = __uint_as_float(row_reduce<LANES>(__float_as_uint(sum), add));
+  if (!a.renormalize) sum = all;
+#pragma unroll
+  for (int c = 0; c < KS; ++c) {
+    const int j = li + LANES * c;
+    if (t < a.T && j < a.k) {
+      const int e = int(at[c]) - a.e0;
+      const bool local = e >= 0 && e < a.E_local;
+      s.sel[t * a.k + j] = int16_t(local ? e : -1);
+      s.wt[t * a.k + j] = p[c] / sum;
+      if (local) atomicOr(&s.mask[e], 1u << t);
+    }
   }
 }
 
@@ -234,30 +284,19 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
-// Sums over k range [unit0, unit0 + units) x 512 of an item's 128 columns for
-// `rows` rows: acc[gi][c][v] of lane 16 g + m is column 8 (4 g + v) + c of row
+// Sums over k range [unit0, unit0 + units) x 512 of the `cols` (at most 128)
+// columns from col0 for `rows` rows: acc[gi][c][v] of lane 16 g + m is column 8 (4 g + v) + c of row
 // 16 gi + m (this wave's share of k). ready(): called once, after the first
 // weights are asked for and before the first activations.
+// Returns false, with nothing added, where ready() did.
 template <bool DOWN, int G, int D, typename Ready>
-__device__ __forceinline__ void stream(const Args& a, const Tables& s, int e, int panel, int unit0, int units,
-                                       int row0, int rows, f32x4v (&acc)[G][8], Ready ready) {
+__device__ __forceinline__ bool stream(const Args& a, const Tables& s, int e, int col0, int cols, int unit0,
+                                       int units, int row0, int rows, f32x4v (&acc)[G][8], Ready ready) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), g = lane >> 4, m = lane & 15;
   const int K = DOWN ? a.I : a.H, ldw = DOWN ? a.H : 2 * a.I;
-  uint32_t wvo;
-  {
-    int col;
-    bool in;
-    if (DOWN) {
-      col = kCols * panel + 8 * m;
-      in = col < a.H;
-    } else {
-      const int o = kGateUp * panel + 16 * (m >> 2) + 8 * (m & 1);
-      in = o < a.I;
-      col = (m & 2) ? a.I + o : o;
-    }
-    wvo = in ? uint32_t(8 * g * ldw + col) * 2u : kOutside;
-  }
+  const int col = 8 * m;
+  const uint32_t wvo = col < cols ? uint32_t(8 * g * ldw + col0 + col) * 2u : kOutside;
   const rsrc_t wr = make_rsrc((DOWN ? a.w_down : a.w_gate_up) + int64_t(e) * K * ldw, int64_t(K) * ldw * 2);
   // activations: x as it is (bf16), h as float32
   const rsrc_t xr = DOWN ? make_rsrc(a.h + int64_t(row0) * a.I, int64_t(rows) * a.I * 4)
@@ -340,10 +379,9 @@ __device__ __forceinline__ void stream(const Args& a, const Tables& s, int e, in
     for (int c = 0; c < 8; ++c) acc[gi][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
   if constexpr (DOWN) {
     static_for<D>([&](auto d) { load_w(d, decltype(d)::value); });
-    ready();
+    if (!ready()) return false;
     static_for<D>([&](auto d) { load_x(d, decltype(d)::value); });
   } else {
-    ready();
     static_for<D>([&](auto d) {
       load_x(d, decltype(d)::value);
       load_w(d, decltype(d)::value);
@@ -355,6 +393,7 @@ __device__ __forceinline__ void stream(const Args& a, const Tables& s, int e, in
       load_x(d, s0 + decltype(d)::value + D);
       load_w(d, s0 + decltype(d)::value + D);
     });
+  return true;
 }
 
 // The item's sums of up to 16 rows over its four waves: thread i < 32 rows
@@ -397,19 +436,33 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   __shared__ Tables s;
   __shared__ __attribute__((aligned(16))) float s_sum[kWaves * 16 * kStride];
   __shared__ int s_tmp[kWaves];
-  __shared__ int s_next, s_last;
+  __shared__ int2 s_item, s_aside;
+  __shared__ int s_last, s_ok;
   const int tid = threadIdx.x;
-  int first = 0;
-  if (tid == 0) first = raise(a.ticket, 1);
+  int my_kind = 0, my_queue = blockIdx.x % kQueues, asked = 0;
+  auto queue = [&](int kind, int q) { return a.queue + (kind * kQueues + q) * kPitch; };
+  auto ask = [&] {
+    if (tid == 0 && my_kind < 3) asked = raise(queue(my_kind, my_queue), 1);
+  };
+  ask();
   for (int i = tid; i < a.E_local; i += kThreads) s.mask[i] = 0;
   __syncthreads();
-  for (int t = tid >> 6; t < a.T; t += kWaves) {
-    if (a.E <= 64)
-      pick<1>(a, s, t);
-    else if (a.E <= 256)
-      pick<4>(a, s, t);
-    else
-      pick<16>(a, s, t);
+  if (a.E <= 256 && a.T > kWaves) {
+    for (int t = tid >> 4; t < ((a.T + 15) & ~15); t += kThreads / 16) {
+      if (a.E <= 32)
+        pick<16, 2>(a, s, t);
+      else if (a.E <= 64)
+        pick<16, 4>(a, s, t);
+      else
+        pick<16, 16>(a, s, t);
+    }
+  } else {  // up to four tokens: a wave each
+    for (int t = tid >> 6; t < a.T; t += kWaves) {
+      if (a.E <= 256)
+        pick<64, 4>(a, s, t);
+      else
+        pick<64, 16>(a, s, t);
+    }
   }
   __syncthreads();
   // rows, expert after expert, tokens in order
@@ -443,62 +496,186 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     const int e = s.sel[i], t = i / a.k;
     if (e >= 0) s.tok[row_of(e, t)] = uint8_t(t);
   }
-  if (tid == 0) s_next = first;
   __syncthreads();
 
-  const int panels_a = (a.I + kGateUp - 1) / kGateUp, panels_b = (a.H + kCols - 1) / kCols;
+  const int blocks = (a.I + kCols - 1) / kCols;  // of 128 outputs of h; a gate and an up panel each
+  const int panels_a = 2 * blocks, panels_b = (a.H + kCols - 1) / kCols;
   const int units_a = (a.H + kSub - 1) / kSub, units_b = (a.I + kSub - 1) / kSub;
   const Split sa = split(a.H, max(1, n_act) * panels_a), sb = split(a.I, max(1, n_act) * panels_b);
-  const int items_a = n_act * sa.ranges * panels_a;
-  // no local selection: the down items only write the zeros
-  const int items = items_a + max(1, n_act) * (n_act ? sb.ranges : 1) * panels_b;
+  const int items_a = n_act * sa.ranges * panels_a, items_b = n_act * sb.ranges * panels_b;
+  const int items_c = (a.T + kTokens - 1) / kTokens * panels_b;
 
-  // y of one down panel, from every row's partial sums
-  auto combine = [&](int panel) {
-    for (int i = tid; i < 32 * a.T; i += kThreads) {
-      const int t = i >> 5, col = kCols * panel + 4 * (i & 31);
-      if (col >= a.H) continue;
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < a.k; ++j) {
-        const int e = s.sel[t * a.k + j];
-        if (e < 0) continue;
-        const float* p = a.part_b + int64_t(row_of(e, t)) * sb.ranges * a.H + col;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int r = 0; r < sb.ranges; ++r, p += a.H) {
-          const float2 lo = get2(p), hi = get2(p + 2);
-          v[0] += lo.x;
-          v[1] += lo.y;
-          v[2] += hi.x;
-          v[3] += hi.y;
-        }
-        const float wt = s.wt[t * a.k + j];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = fmaf(wt, v[q], o[q]);
-      }
-      if (a.y_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + int64_t(t) * a.H + col) =
-            make_float4(o[0], o[1], o[2], o[3]);
-      else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + int64_t(t) * a.H + col) =
-            make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+  auto items_of = [&](int kind) { return kind == 0 ? items_a : kind == 1 ? items_b : items_c; };
+  auto left_of = [&](int kind, int q) {  // items of queue q at the start
+    const int chunk = (items_of(kind) + kQueues - 1) / kQueues;
+    return min(chunk, items_of(kind) - q * chunk);
+  };
+  auto item_at = [&](int kind, int q, int t) { return q * ((items_of(kind) + kQueues - 1) / kQueues) + t; };
+  // The next item, by wave 0: ask() raises its queue's counter, without waiting
+  // for the answer; answer() makes an item of it. kind 3: none left.
+  auto answer = [&]() -> int2 {
+    for (;;) {
+      const int t = __builtin_amdgcn_readfirstlane(asked);
+      if (t < left_of(my_kind, my_queue)) return make_int2(my_kind, item_at(my_kind, my_queue, t));
+      if (++my_kind == 3) return make_int2(3, 0);
+      ask();
     }
   };
+  // An item of a kind before `kind` from any queue (kind 3: none is left), by
+  // wave 0; lane q < 8 looks at queue q.
+  auto rescue = [&](int kind) -> int2 {
+    const int lane = lane_id();
+    for (int kd = 0; kd < kind; ++kd)
+      for (;;) {
+        bool left = false;
+        if (lane < kQueues) left = peek(queue(kd, lane)) < left_of(kd, lane);
+        const uint64_t any = ballot(left);
+        if (any == 0) break;
+        const int q = __builtin_ctzll(any);
+        int t = 0;
+        if (lane == 0) t = raise(queue(kd, q), 1);
+        t = __builtin_amdgcn_readfirstlane(t);
+        if (t < left_of(kd, q)) return make_int2(kd, item_at(kd, q, t));
+      }
+    return make_int2(3, 0);
+  };
+  // Polls until *c reaches n, at most kSpins times.
+  auto poll = [&](const int* c, int n) {
+    for (int i = 0; i < kSpins; ++i) {
+      if (peek(c) >= n) return true;
+      __builtin_amdgcn_s_sleep(1);
+    }
+    return false;
+  };
 
+  // y of one down panel for kTokens tokens, from their rows' partial sums:
+  // slot by slot, k range by k range, kBatch loads at a time
+  auto combine = [&](int panel, int t0) {
+    const int t = t0 + (tid >> 5), col = kCols * panel + 4 * (tid & 31);
+    if (t >= a.T || col >= a.H) return;
+    float o[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+    // the terms in order: (slot, range) pairs of the local slots
+    int j = 0, r = 0;
+    while (j < a.k && s.sel[t * a.k + j] < 0) ++j;
+    while (j < a.k) {
+      float2 q[kBatch][2];
+      int jj[kBatch];
+      bool end[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        jj[i] = -1;
+        end[i] = false;
+        if (j < a.k) {
+          const int e = s.sel[t * a.k + j];
+          const float* p = a.part_b + (int64_t(row_of(e, t)) * sb.ranges + r) * a.H + col;
+          q[i][0] = get2(p);
+          q[i][1] = get2(p + 2);
+          jj[i] = j;
+          if (++r == sb.ranges) {
+            end[i] = true;
+            r = 0;
+            do ++j;
+            while (j < a.k && s.sel[t * a.k + j] < 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (jj[i] >= 0) {
+          v[0] += q[i][0].x;
+          v[1] += q[i][0].y;
+          v[2] += q[i][1].x;
+          v[3] += q[i][1].y;
+          if (end[i]) {
+            const float wt = s.wt[t * a.k + jj[i]];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              o[c] = fmaf(wt, v[c], o[c]);
+              v[c] = 0.f;
+            }
+          }
+        }
+    }
+    if (a.y_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.y) + int64_t(t) * a.H + col) =
+          make_float4(o[0], o[1], o[2], o[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + int64_t(t) * a.H + col) =
+          make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+  };
+
+  // s_item: the item at hand; s_aside: an item that waits while its workgroup
+  // does a rescued one (kind 3: none)
+  if (tid < 64) {
+    const int2 f = answer();
+    if (tid == 0) {
+      s_item = f;
+      s_aside = make_int2(3, 0);
+    }
+  }
+  __syncthreads();
   for (;;) {
-    const int item = __builtin_amdgcn_readfirstlane(s_next);
-    if (item >= items) break;
-    int next = 0;
-    if (item < items_a) {
-      // expert, k range, panel (fastest: neighbours read neighbouring columns)
-      const int panel = item % panels_a, er = item / panels_a;
-      const int ai = er / sa.ranges, range = er - ai * sa.ranges;
-      const int e = __builtin_amdgcn_readfirstlane(s.act[ai]);
-      const int row0 = __builtin_amdgcn_readfirstlane(s.row0[e]);
-      const int rows = __popc(__builtin_amdgcn_readfirstlane(int(s.mask[e])));
-      const int units = min(sa.units, units_a - range * sa.units);
-      auto ready = [&] {
-        if (tid == 0) next = raise(a.ticket, 1);
-      };
+    const int kind = __builtin_amdgcn_readfirstlane(s_item.x), item = __builtin_amdgcn_readfirstlane(s_item.y);
+    const bool rescued = __builtin_amdgcn_readfirstlane(s_aside.x) != 3;
+    if (kind == 3) break;
+    // The end of an item: the one put aside, or the next of the queue. Waves
+    // other than the first see it after the caller's barrier.
+    auto advance = [&] {
+      if (tid >= 64) return;
+      const int2 n = rescued ? s_aside : answer();
+      if (tid == 0) {
+        s_item = n;
+        s_aside = make_int2(3, 0);
+      }
+    };
+    // Nothing came: a rescued item first, this one again after it. (A rescued
+    // down item was found with every gate/up item handed out: it just polls on.)
+    auto put_aside = [&] {
+      __syncthreads();
+      if (tid < 64 && !rescued) {
+        const int2 o = rescue(kind);
+        if (tid == 0 && o.x != 3) {
+          s_aside = make_int2(kind, item);
+          s_item = o;
+        }
+      }
+      __syncthreads();
+    };
+    // Asks for the item after this one: a gate/up item at its start, the
+    // others when they need not wait any more (an item in the hands of a waiting
+    // workgroup would wait with it).
+    auto ask_next = [&] {
+      if (!rescued) ask();
+    };
+    if (kind == 2) {
+      const int panel = item % panels_b;
+      if (tid == 0) s_ok = poll(a.cnt_b + panel * kPitch, n_act * sb.ranges);
+      if (tid == 0 && s_ok) ask_next();
+      __syncthreads();
+      if (!s_ok) {
+        put_aside();
+        continue;
+      }
+      combine(panel, item / panels_b * kTokens);
+      advance();
+      __syncthreads();
+      continue;
+    }
+    // expert, k range, panel (fastest: neighbours read neighbouring columns)
+    const bool down = kind == 1;
+    const int np = down ? panels_b : panels_a, nr = down ? sb.ranges : sa.ranges;
+    const int panel = item % np, er = item / np;
+    const int ai = er / nr, range = er - ai * nr;
+    const int e = __builtin_amdgcn_readfirstlane(s.act[ai]);
+    const int row0 = __builtin_amdgcn_readfirstlane(s.row0[e]);
+    const int rows = __popc(__builtin_amdgcn_readfirstlane(int(s.mask[e])));
+    const int unit0 = range * (down ? sb.units : sa.units);
+    const int units = min(down ? sb.units : sa.units, (down ? units_b : units_a) - unit0);
+    if (!down) {
+      const int block = panel < blocks ? panel : panel - blocks;
+      const int col0 = kCols * block + (panel < blocks ? 0 : a.I), cols = min(kCols, a.I - kCols * block);
+      auto ready = [] { return true; };
+      ask_next();
       auto put = [&](int gi) {
         return [&, gi](int r, int pos, const float4& t) {
           float* p = a.part_a + ((int64_t(row0 + 16 * gi + r) * sa.ranges + range) * panels_a + panel) * kCols + pos;
@@ -508,77 +685,92 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       };
       if (!TWO || rows <= 16) {
         f32x4v acc[1][8];
-        stream<false, 1, 4>(a, s, e, panel, range * sa.units, units, row0, rows, acc, ready);
+        stream<false, 1, 4>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
-        stream<false, 2, 2>(a, s, e, panel, range * sa.units, units, row0, rows, acc, ready);
+        stream<false, 2, 2>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
         gather_sums(s_sum, acc[0], 16, put(0));
         gather_sums(s_sum, acc[1], rows - 16, put(1));
       }
       stores_done();
       __syncthreads();
-      if (tid == 0) {
-        s_last = raise(a.cnt_a + ai * panels_a + panel, 1) == sa.ranges - 1;
-        s_next = next;
-      }
+      if (tid == 0) s_last = raise(a.cnt_a + (int64_t(ai) * blocks + block) * kPitch, 1) == 2 * sa.ranges - 1;
+      advance();
       __syncthreads();
       if (s_last) {
-        // h of the panel's 64 outputs: 16 threads a row, 4 outputs each; the
-        // gate of output o is at position 32 (o / 16) + o % 16, its up 16 on
-        for (int i = tid; i < 16 * rows; i += kThreads) {
-          const int r = i >> 4, o = 4 * (i & 15), oc = kGateUp * panel + o;
-          if (oc >= a.I) continue;
-          const float* p = a.part_a + (int64_t(row0 + r) * sa.ranges * panels_a + panel) * kCols + 32 * (o >> 4) + (o & 15);
-          float gt[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int q = 0; q < sa.ranges; ++q, p += int64_t(panels_a) * kCols) {
-            const float2 g0 = get2(p), g1 = get2(p + 2), u0 = get2(p + 16), u1 = get2(p + 18);
-            gt[0] += g0.x;
-            gt[1] += g0.y;
-            gt[2] += g1.x;
-            gt[3] += g1.y;
-            up[0] += u0.x;
-            up[1] += u0.y;
-            up[2] += u1.x;
-            up[3] += u1.y;
+        // h of the block's 128 outputs, up to 8 rows at a time: 32 threads of 4
+        // outputs per row, and with fewer rows the ranges dealt to the threads
+        // left, whose sums meet in LDS
+        const int rp = min(8, rows <= 1 ? 1 : 1 << (32 - __clz(rows - 1))), ng = 8 / rp;
+        const int slot = tid >> 5, o = 4 * (tid & 31), oc = kCols * block + o;
+        const int grp = slot / rp;
+        for (int r0 = 0; r0 < rows; r0 += rp) {
+          const int r = r0 + slot % rp;
+          float gu[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (r < rows && oc < a.I) {
+            const float* p = a.part_a + (int64_t(row0 + r) * sa.ranges * panels_a + block) * kCols + o;
+            for (int q0 = grp; q0 < sa.ranges; q0 += kBatch * ng) {
+              float2 v[kBatch][4];
+#pragma unroll
+              for (int q = 0; q < kBatch; ++q) {
+                const float* pq = p + int64_t(min(q0 + q * ng, sa.ranges - 1)) * panels_a * kCols;
+                v[q][0] = get2(pq);
+                v[q][1] = get2(pq + 2);
+                v[q][2] = get2(pq + int64_t(blocks) * kCols);
+                v[q][3] = get2(pq + int64_t(blocks) * kCols + 2);
+              }
+#pragma unroll
+              for (int q = 0; q < kBatch; ++q)
+                if (q0 + q * ng < sa.ranges) {
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    gu[2 * c] += v[q][c].x;
+                    gu[2 * c + 1] += v[q][c].y;
+                  }
+                }
+            }
           }
-          float* hp = a.h + int64_t(row0 + r) * a.I + oc;
-          put2(hp, silu_mul(gt[0], up[0]), silu_mul(gt[1], up[1]));
-          put2(hp + 2, silu_mul(gt[2], up[2]), silu_mul(gt[3], up[3]));
+          if (ng > 1) {  // s_sum: [slot][8 values][32 threads]
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) s_sum[(slot * 8 + c) * 32 + (tid & 31)] = gu[c];
+            __syncthreads();
+            if (grp == 0)
+              for (int i = 1; i < ng; ++i)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) gu[c] += s_sum[((slot + i * rp) * 8 + c) * 32 + (tid & 31)];
+          }
+          if (grp == 0 && r < rows && oc < a.I) {
+            float* hp = a.h + int64_t(row0 + r) * a.I + oc;
+            put2(hp, silu_mul(gu[0], gu[4]), silu_mul(gu[1], gu[5]));
+            put2(hp + 2, silu_mul(gu[2], gu[6]), silu_mul(gu[3], gu[7]));
+          }
         }
         stores_done();
         __syncthreads();
-        if (tid == 0) raise(a.cnt_h + ai * units_b + panel * kGateUp / kSub, 1);
+        if (tid == 0) raise(a.cnt_h + (int64_t(ai) * units_b + block * kCols / kSub) * kPitch, 1);
       }
-    } else if (n_act == 0) {
-      combine(item - items_a);
-      if (tid == 0) next = raise(a.ticket, 1);
-      __syncthreads();
-      if (tid == 0) s_next = next;
-      __syncthreads();
     } else {
-      const int bi = item - items_a;
-      const int panel = bi % panels_b, er = bi / panels_b;
-      const int ai = er / sb.ranges, range = er - ai * sb.ranges;
-      const int e = __builtin_amdgcn_readfirstlane(s.act[ai]);
-      const int row0 = __builtin_amdgcn_readfirstlane(s.row0[e]);
-      const int rows = __popc(__builtin_amdgcn_readfirstlane(int(s.mask[e])));
-      const int unit0 = range * sb.units, units = min(sb.units, units_b - unit0);
-      // every panel of h in this k range is written
+      const int col0 = kCols * panel, cols = min(kCols, a.H - col0);
+      // every block of h in this k range is written
       auto ready = [&] {
-        if (tid == 0) next = raise(a.ticket, 1);
-        for (int u = tid; u < units; u += kThreads) {
-          const int need = min(kSub / kGateUp, panels_a - (unit0 + u) * (kSub / kGateUp));
-          while (__hip_atomic_load(a.cnt_h + ai * units_b + unit0 + u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
-            __builtin_amdgcn_s_sleep(1);
+        if (tid < 64) {
+          bool ok = true;
+          for (int u = tid; u < units && ok; u += 64)
+            ok = poll(a.cnt_h + (int64_t(ai) * units_b + unit0 + u) * kPitch,
+                      min(kSub / kCols, blocks - (unit0 + u) * (kSub / kCols)));
+          const uint64_t no = ballot(!ok);
+          if (tid == 0) s_ok = no == 0;
+          if (no == 0) ask_next();
         }
         __syncthreads();
+        return s_ok != 0;
       };
       auto put = [&](int gi) {
         return [&, gi](int r, int pos, const float4& t) {
-          const int col = kCols * panel + pos;
-          if (col < a.H) {
-            float* p = a.part_b + (int64_t(row0 + 16 * gi + r) * sb.ranges + range) * a.H + col;
+          if (pos < cols) {
+            float* p = a.part_b + (int64_t(row0 + 16 * gi + r) * sb.ranges + range) * a.H + col0 + pos;
             put2(p, t.x, t.y);
             put2(p + 2, t.z, t.w);
           }
@@ -586,50 +778,54 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       };
       if (!TWO || rows <= 16) {
         f32x4v acc[1][8];
-        stream<true, 1, 4>(a, s, e, panel, unit0, units, row0, rows, acc, ready);
+        if (!stream<true, 1, 4>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
+          put_aside();
+          continue;
+        }
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
-        stream<true, 2, 2>(a, s, e, panel, unit0, units, row0, rows, acc, ready);
+        if (!stream<true, 2, 2>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
+          put_aside();
+          continue;
+        }
         gather_sums(s_sum, acc[0], 16, put(0));
         gather_sums(s_sum, acc[1], rows - 16, put(1));
       }
       stores_done();
       __syncthreads();
-      if (tid == 0) {
-        s_last = raise(a.cnt_b + panel, 1) == n_act * sb.ranges - 1;
-        s_next = next;
-      }
+      if (tid == 0) raise(a.cnt_b + panel * kPitch, 1);
+      advance();
       __syncthreads();
-      if (s_last) combine(panel);
     }
   }
 }
 
 struct Layout {
   size_t logits, counters, part_a, part_b, h, total;
-  int n_counters, cnt_h, cnt_b;
+  int64_t n_counters, cnt_a, cnt_h, cnt_b;
 };
 // Rows times k ranges of an operand with `panels` panels per expert: with n
 // experts in use there are at most min(cap, n T) rows, and ranges stay below
-// kFewItems / (n panels) + 1.
+// kItems / (n panels) + 1.
 inline int64_t row_ranges(int64_t cap, int T, int K, int panels) {
   const int64_t u = ceil_div(K, kSub);
-  return std::min(cap * u, cap + int64_t(T) * ceil_div(kFewItems, panels));
+  return std::min(cap * u, cap + int64_t(T) * ceil_div(kItems, panels));
 }
 inline Layout layout(int T, int H, int I, int E, int k, int E_local) {
   Layout L{};
   const int64_t cap = int64_t(T) * std::min(k, E_local), act = std::min<int64_t>(E_local, cap);
-  const int pa = int(ceil_div(I, kGateUp)), pb = int(ceil_div(H, kCols));
+  const int blocks = int(ceil_div(I, kCols)), pa = 2 * blocks, pb = int(ceil_div(H, kCols));
   size_t o = 0;
   auto take = [&](int64_t n) {
     const size_t at = o;
     o = (o + size_t(n) * 4 + 255) / 256 * 256;
     return at;
   };
-  L.cnt_h = int(1 + act * pa);
-  L.cnt_b = int(L.cnt_h + act * ceil_div(I, kSub));
-  L.n_counters = L.cnt_b + pb;
+  L.cnt_a = 3 * kQueues * kPitch;
+  L.cnt_h = L.cnt_a + act * blocks * kPitch;
+  L.cnt_b = L.cnt_h + act * ceil_div(I, kSub) * kPitch;
+  L.n_counters = L.cnt_b + int64_t(pb) * kPitch;
   L.logits = take(int64_t(T) * E);
   L.counters = take(L.n_counters);
   L.part_a = take(row_ranges(cap, T, H, pa) * pa * kCols);
@@ -640,6 +836,12 @@ inline Layout layout(int T, int H, int I, int E, int k, int E_local) {
 }
 
 }  // namespace few
+
+bool few_supported(int T, int I, int k, int E_local) {
+  // the counters are indexed with 31 bits: 32 of them per 128 columns of each
+  // expert in use
+  return int64_t(std::min<int64_t>(E_local, int64_t(T) * k)) * I < (int64_t(1) << 32);
+}
 
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {
   return few::layout(T, H, I, E, k, E_local).total;
@@ -654,7 +856,7 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
   int* ctr = reinterpret_cast<int*>(ws + L.counters);
   auto score = [&](auto tb) {
     hipLaunchKernelGGL(few_logits_kernel<decltype(tb)::value>, dim3(unsigned(E)), dim3(few::kThreads), 0, stream, x,
-                       w_router, bias, T, H, E, logits, ctr, L.n_counters);
+                       w_router, bias, T, H, E, logits, ctr, int(L.n_counters));
   };
   if (T == 1)
     score(std::integral_constant<int, 1>{});
@@ -668,7 +870,7 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
     score(std::integral_constant<int, 32>{});
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), y, ctr, ctr + 1,
+  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), y, ctr, ctr + L.cnt_a,
                ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
                reinterpret_cast<float*>(ws + L.part_b), reinterpret_cast<float*>(ws + L.h)};
   hipLaunchKernelGGL(T > 16 ? few_experts_kernel<true> : few_experts_kernel<false>, dim3(unsigned(2 * device_cu_count())), dim3(few::kThreads), 0, stream, a);

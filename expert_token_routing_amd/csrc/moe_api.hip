@@ -361,7 +361,8 @@ static int few_impl(const moe_bf16* x, const float* w_router, const float* bias,
   if (st != MOE_OK) return st;
   if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
   if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
-  if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
+  if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I) || !few_supported(T, I, k, E_local))
+    return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y))

@@ -106,6 +106,22 @@ __device__ __forceinline__ float wave_max_dpp(float v) {
   const float r3 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
+// Sum over the wave the same way (no LDS traffic), the same on every lane.
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+  auto step = [](float x, auto ctrl) {
+    constexpr int c = decltype(ctrl)::value;
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), c, 0xF, 0xF, false));
+  };
+  v = step(v, std::integral_constant<int, 0xB1>{});
+  v = step(v, std::integral_constant<int, 0x4E>{});
+  v = step(v, std::integral_constant<int, 0x141>{});
+  v = step(v, std::integral_constant<int, 0x140>{});
+  const float r0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+  const float r1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+  const float r2 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+  const float r3 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+  return (r0 + r1) + (r2 + r3);
+}
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v += shfl_xor(v, m);

@@ -52,7 +52,7 @@ def test_few_workspace_size():
     assert M.few_workspace_size(33, 64, 64, 8, 2, 8) == 0
     for T, H, I, E, k, El in ((1, 7168, 256, 256, 8, 256), (16, 7168, 2048, 256, 8, 32), (32, 1024, 2816, 8, 2, 8),
                               (32, 1024, 640, 1024, 32, 512), (1, 8, 8, 1, 1, 1), (5, 72, 4104, 6, 3, 2)):
-        cap, pa, pb = T * min(k, El), -(-I // 64), -(-H // 128)
+        cap, pa, pb = T * min(k, El), 2 * -(-I // 128), -(-H // 128)
         need = 0
         for n in range(1, min(El, cap) + 1):
             rows = min(cap, n * T)
