@@ -63,7 +63,7 @@ constexpr int kCols = 128;      // weight columns of an item
 constexpr int kStride = kCols + 4;
 constexpr int kBatch = 8;       // exchanged values asked for at a time
 constexpr int kTokens = 8;      // tokens of a return item
-constexpr int kItems = 2048;    // items an operand is cut into where k allows (four per workgroup)
+constexpr int kItems = 1024;    // items an operand is cut into where k allows (two per workgroup)
 constexpr int kQueues = 8;      // of each kind of item, one per XCD (workgroup b runs on XCD b % 8)
 constexpr int kPitch = 32;      // ints between counters: a 128-byte line each
 constexpr int kSpins = 4096;    // polls before a waiting workgroup looks for items (some 2 ms)
@@ -166,7 +166,7 @@ struct Tables {
   uint32_t mask[kMaxE];   // tokens that picked local expert e (T <= 32 bits)
   int row0[kMaxE];        // first row of local expert e
   int act[kMaxE];         // the local experts that have rows
-  int16_t sel[kMaxSel];   // slot (t, j): local expert or -1
+  int16_t sel[kMaxSel];   // slot (t, j): local expert, then its row, or -1
   float wt[kMaxSel];      // its weight
   uint8_t tok[kMaxSel];   // row: its token
 };
@@ -467,34 +467,37 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   __syncthreads();
   // rows, expert after expert, tokens in order
   constexpr int kPerT = kMaxE / kThreads;
-  int n_rows, n_act;
+  int n_act;
   {
-    int rows[kPerT], sum = 0, act = 0;
+    // both prefixes in one scan: rows (at most T k = 1024) above, experts below
+    int rows[kPerT], sum = 0, total;
 #pragma unroll
     for (int q = 0; q < kPerT; ++q) {
       const int e = tid * kPerT + q;
       rows[q] = e < a.E_local ? __popc(s.mask[e]) : 0;
-      sum += rows[q];
-      act += rows[q] > 0;
+      sum += rows[q] * 65536 + (rows[q] > 0);
     }
-    int r0 = block_exclusive_scan<kThreads>(sum, s_tmp, n_rows);
-    int a0 = block_exclusive_scan<kThreads>(act, s_tmp, n_act);
+    int pre = block_exclusive_scan<kThreads>(sum, s_tmp, total);
+    n_act = total & 0xFFFF;
 #pragma unroll
     for (int q = 0; q < kPerT; ++q) {
       const int e = tid * kPerT + q;
       if (e < a.E_local) {
-        s.row0[e] = r0;
-        if (rows[q] > 0) s.act[a0] = e;
+        s.row0[e] = pre >> 16;
+        if (rows[q] > 0) s.act[pre & 0xFFFF] = e;
       }
-      r0 += rows[q];
-      a0 += rows[q] > 0;
+      pre += rows[q] * 65536 + (rows[q] > 0);
     }
   }
   __syncthreads();
-  auto row_of = [&](int e, int t) { return s.row0[e] + __popc(s.mask[e] & ((1u << t) - 1u)); };
+  // from here on a slot holds its row instead of its expert
   for (int i = tid; i < a.T * a.k; i += kThreads) {
     const int e = s.sel[i], t = i / a.k;
-    if (e >= 0) s.tok[row_of(e, t)] = uint8_t(t);
+    if (e >= 0) {
+      const int r = s.row0[e] + __popc(s.mask[e] & ((1u << t) - 1u));
+      s.tok[r] = uint8_t(t);
+      s.sel[i] = int16_t(r);
+    }
   }
   __syncthreads();
 
@@ -566,8 +569,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         jj[i] = -1;
         end[i] = false;
         if (j < a.k) {
-          const int e = s.sel[t * a.k + j];
-          const float* p = a.part_b + (int64_t(row_of(e, t)) * sb.ranges + r) * a.H + col;
+          const float* p = a.part_b + (int64_t(s.sel[t * a.k + j]) * sb.ranges + r) * a.H + col;
           q[i][0] = get2(p);
           q[i][1] = get2(p + 2);
           jj[i] = j;
@@ -710,24 +712,24 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           float gu[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           if (r < rows && oc < a.I) {
             const float* p = a.part_a + (int64_t(row0 + r) * sa.ranges * panels_a + block) * kCols + o;
-            for (int q0 = grp; q0 < sa.ranges; q0 += kBatch * ng) {
-              float2 v[kBatch][4];
+            constexpr int B = kBatch / 2;  // of four loads each
+            for (int q0 = grp; q0 < sa.ranges; q0 += B * ng) {
+              float2 v[B][4] = {};
 #pragma unroll
-              for (int q = 0; q < kBatch; ++q) {
-                const float* pq = p + int64_t(min(q0 + q * ng, sa.ranges - 1)) * panels_a * kCols;
-                v[q][0] = get2(pq);
-                v[q][1] = get2(pq + 2);
-                v[q][2] = get2(pq + int64_t(blocks) * kCols);
-                v[q][3] = get2(pq + int64_t(blocks) * kCols + 2);
-              }
-#pragma unroll
-              for (int q = 0; q < kBatch; ++q)
+              for (int q = 0; q < B; ++q)
                 if (q0 + q * ng < sa.ranges) {
+                  const float* pq = p + int64_t(q0 + q * ng) * panels_a * kCols;
+                  v[q][0] = get2(pq);
+                  v[q][1] = get2(pq + 2);
+                  v[q][2] = get2(pq + int64_t(blocks) * kCols);
+                  v[q][3] = get2(pq + int64_t(blocks) * kCols + 2);
+                }
 #pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    gu[2 * c] += v[q][c].x;
-                    gu[2 * c + 1] += v[q][c].y;
-                  }
+              for (int q = 0; q < B; ++q)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  gu[2 * c] += v[q][c].x;
+                  gu[2 * c + 1] += v[q][c].y;
                 }
             }
           }
