@@ -16,9 +16,11 @@
 // The weights are always the first operand, so a lane ends with 4 consecutive
 // channels of one token and stores them as one vector.
 //
-// Kernels: tile_kernel (operands through LDS; three tile sizes) and
-// skinny_kernel (few rows: the weight stream is the whole cost, straight into
-// registers).
+// One kernel in six tile shapes, from 16 x 32 (few rows: the weight stream is the
+// whole cost) to 288 x 256. The operands come through LDS by direct-to-LDS loads
+// of whole 128-byte lines. (Weight fragments loaded straight into registers, 16
+// rows x 64 bytes an instruction, streamed a DeepSeek-R1-shaped rank's 1.41 GB at
+// 8 rows per expert in 410 us; the tiles take 254.)
 #include "gemm_dma.h"
 #include "gemm_tile.h"
 #include "moe_kernels.h"
@@ -72,6 +74,15 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int64_t row, int col, 
   for (int v = 0; v < 4; ++v) o[v] = float(c[v]) * (sa * s[v]);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + row * p.N + col) =
       make_uint2(cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3]));
+}
+// 8 consecutive outputs of one row
+__device__ __forceinline__ void store8(const GemmArgs& p, int64_t row, int col, const i32x4& c, const i32x4& d,
+                                       float sa, const float4& s, const float4& t) {
+  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.C) + row * p.N + col) =
+      u32x4{cvt_bf16x2(float(c[0]) * (sa * s.x), float(c[1]) * (sa * s.y)),
+            cvt_bf16x2(float(c[2]) * (sa * s.z), float(c[3]) * (sa * s.w)),
+            cvt_bf16x2(float(d[0]) * (sa * t.x), float(d[1]) * (sa * t.y)),
+            cvt_bf16x2(float(d[2]) * (sa * t.z), float(d[3]) * (sa * t.w))};
 }
 __device__ __forceinline__ void store4_swiglu(const GemmArgs& p, int64_t row, int col, const i32x4& g, const i32x4& u,
                                               float sa, const float4& sg, const float4& su) {
@@ -150,31 +161,44 @@ __device__ __forceinline__ void alternate_mfma_reads() {
   for (int i = NM; i < NR; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 }
 
-// Waves WR x WC; a tile is 16 FM WR rows x 16 FN WC channels, S stages.
-// 16-row fragment f belongs to wave row f % WR; wave column wn holds channels
-// 16 FN wn .. (gate/up: FN / 2 fragments of gate, then the matching up).
-template <int WR_, int WC_, int FN_, int S_>
+// KG groups of WR x WC waves; a tile is 16 FM WR rows x 16 FN WC channels, S
+// stages in LDS per group. Group q takes k stages q, q + KG, ..; the groups'
+// int32 sums meet in LDS (exact in any order). 16-row fragment f belongs to wave
+// row f % WR; wave column wn holds channels 16 FN wn .. (gate/up: 8 FN of gate,
+// then the matching up).
+template <int WR_, int WC_, int FN_, int S_, int KG_>
 struct Shape {
-  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_;
+  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_, KG = KG_;
   static constexpr int W = WR * WC, BN = 16 * FN * WC;
 };
 
 template <typename T, int FM>
 constexpr int stage_bytes() { return (16 * FM * T::WR + T::BN) * kRowB; }
 
+// Which channel of its wave column's C a weight fragment's row r holds: lane
+// group g gets rows 4 g .. 4 g + 3 of each of the C / 16 fragments j, and these
+// are its C / 4 consecutive channels, so that it stores whole vectors.
+template <int C>
+__device__ __forceinline__ int channel_of(int j, int r) { return C / 4 * (r >> 2) + 4 * j + (r & 3); }
+
 template <typename T, int FM, bool SWIGLU, bool TAIL, typename SrcRow>
 __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, const int8_t* a_base, int64_t a_bytes,
                                          SrcRow src_row, int rows, int r0, int e, int nj) {
-  constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN;
+  constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN, KG = T::KG;
   constexpr int BM = 16 * FM * WR;
   constexpr int kA = BM * kRowB, kStage = stage_bytes<T, FM>();
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w % WR, wn = w / WR;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG == 1 ? 0 : wave / W, w = wave % W, wm = w % WR, wn = w / WR;
   const int lane = lane_id();
   const int g = lane >> 4, l16 = lane & 15;
-  const int nk = (p.K + kRowB - 1) / kRowB;
-  const int nvalid = (p.K - (nk - 1) * kRowB) / 16;  // chunks of the last stage (TAIL: fewer than 8)
-  constexpr int kCols = SWIGLU ? BN / 2 : BN;        // outputs of a tile
+  const int nk_all = (p.K + kRowB - 1) / kRowB;
+  const int nvalid = (p.K - (nk_all - 1) * kRowB) / 16;  // chunks of the last stage (TAIL: fewer than 8)
+  const int nk = (nk_all + KG - 1) / KG;                 // iterations of every group
+  const int mine = (nk_all - kg + KG - 1) / KG;          // stages of this one
+  constexpr int kCols = SWIGLU ? BN / 2 : BN;            // outputs of a tile
+  constexpr int kFrags = SWIGLU ? FN / 2 : FN;           // fragments of a wave's outputs
   const int c0 = nj * kCols;
+  MOE_LDS char* const ring = lds + kg * S * kStage;
 
   typedef Loader<BM, W> LA;
   typedef Loader<BN, W> LB;
@@ -182,28 +206,31 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
   LB lb;
   la.init(a_base, a_bytes, p.K, w, [&](int r) { return src_row(min(r, rows - 1)); });
   lb.init(p.W + int64_t(e) * p.wrows * p.K, int64_t(p.wrows) * p.K, p.K, w, [&](int s) {
-    if (SWIGLU) {
-      constexpr int hw = 8 * FN;  // outputs of a wave column
-      const int q = s % (2 * hw), o = min(c0 + s / (2 * hw) * hw + q % hw, p.N - 1);
-      return q < hw ? o : p.up_off + o;
-    }
-    return min(c0 + s, p.N - 1);
+    const int col = s / (16 * FN), j = s / 16 % FN, r = s % 16;  // wave column, fragment, row
+    const int o = min(c0 + 16 * kFrags * col + channel_of<16 * kFrags>(j % kFrags, r), p.N - 1);
+    return j < kFrags ? o : p.up_off + o;
   });
   const uint32_t back = TAIL && LA::chunk(w) >= nvalid ? 16u * uint32_t(LA::chunk(w)) : 0u;
   const int nl = LA::count(w) + LB::count(w);
   auto issue = [&](int st) {
-    if (st < nk) {
-      MOE_LDS char* d = lds + st % S * kStage;
-      const uint32_t b = TAIL && st == nk - 1 ? back : 0u;
-      la.issue(d, w, uint32_t(st) * kRowB, b);
-      lb.issue(d + kA, w, uint32_t(st) * kRowB, b);
+    if (st < mine) {
+      MOE_LDS char* d = ring + st % S * kStage;
+      const int at = kg + KG * st;
+      const uint32_t b = TAIL && at == nk_all - 1 ? back : 0u;
+      la.issue(d, w, uint32_t(at) * kRowB, b);
+      lb.issue(d + kA, w, uint32_t(at) * kRowB, b);
     }
+  };
+  // chunks of k that stage st of this group holds
+  auto chunks = [&](int st) {
+    if (KG > 1 && st >= mine) return 0;
+    return TAIL && kg + KG * st == nk_all - 1 ? nvalid : 8;
   };
   // stage s landed for this wave; up to `last` were issued
   constexpr int kMaxAhead = (S - 1) * (LA::kPer + LB::kPer);
   auto wait_stage = [&](int s, int last) {
     __builtin_amdgcn_sched_barrier(0);
-    const int n = max(0, min(last, nk - 1) - s) * nl;
+    const int n = max(0, min(last, mine - 1) - s) * nl;
     wait_vm_dyn<kMaxAhead>(n);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -234,15 +261,17 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
   for (int st = 0; st < S; ++st) issue(st);
   wait_stage(0, S - 1);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) b[j] = read_b(lds, 0, j);
+  for (int j = 0; j < FN; ++j) b[j] = read_b(ring, 0, j);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) a[i] = read_a(lds, 0, i);
+  for (int i = 0; i < FM; ++i) a[i] = read_a(ring, 0, i);
 
   constexpr int kH1 = (FM + 1) / 2;
   for (int kt = 0; kt < nk; ++kt) {
-    const MOE_LDS char* cur = lds + kt % S * kStage;
-    const bool tail = TAIL && kt == nk - 1;
-    if (TAIL && tail && g >= nvalid) {  // k beyond K counts as zeros (0 times any byte is 0)
+    const MOE_LDS char* cur = ring + kt % S * kStage;
+    // k beyond K, or beyond the group's stages, counts as zeros (0 times any
+    // byte is 0)
+    const int have = TAIL || KG > 1 ? chunks(kt) : 8;
+    if ((TAIL || KG > 1) && have < 8 && g >= have) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) a[i] = i32x4{0, 0, 0, 0};
     }
@@ -258,7 +287,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
     alternate_mfma_reads<FM * FN, FN + FM>();
 #pragma unroll
     for (int j = 0; j < FN; ++j) b[j] = bs[j];
-    if (TAIL && tail && 4 + g >= nvalid) {
+    if ((TAIL || KG > 1) && have < 8 && 4 + g >= have) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) a[i] = i32x4{0, 0, 0, 0};
     }
@@ -273,7 +302,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
     dma::wait_lgkm0();
     wait_stage(min(kt + 1, nk - 1), kt + S - 1);
     issue(kt + S);
-    const MOE_LDS char* nxt = lds + (kt + 1) % S * kStage;
+    const MOE_LDS char* nxt = ring + (kt + 1) % S * kStage;
     i32x4 bn[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) bn[j] = read_b(nxt, 0, j);
@@ -292,7 +321,33 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
   }
   dma::wait_lds_barrier();  // the next tile's loads may overwrite the stages
 
+  if constexpr (KG > 1) {
+    // the other groups' sums into the first: [group - 1][wave][fragment][lane]
+    static_assert((KG - 1) * W * FM * FN * 1024 <= KG * S * kStage, "the sums fit the stages");
+    MOE_LDS i32x4* const sums = (MOE_LDS i32x4*)lds;
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sums[((((kg - 1) * W + w) * FM + i) * FN + j) * 64 + lane] = acc[i][j];
+    }
+    dma::wait_lds_barrier();
+    if (kg == 0) {
+#pragma unroll
+      for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] += sums[(((q * W + w) * FM + i) * FN + j) * 64 + lane];
+    }
+    dma::wait_lds_barrier();
+    if (kg > 0) return;
+  }
+
+  // lane group g holds 4 kFrags consecutive outputs of row l16 of a fragment,
+  // 4 per fragment j
   const float* sw = p.sw + int64_t(e) * p.wrows;
+  const int col = c0 + 16 * kFrags * wn + 4 * kFrags * g;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int row = 16 * (WR * i + wm) + l16;
@@ -300,52 +355,67 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
     const float sa = p.sa[p.gather_src ? p.gather_src[r0 + row] / p.gather_k : r0 + row];
     if constexpr (SWIGLU) {
 #pragma unroll
-      for (int j = 0; j < FN / 2; ++j) {
-        const int col = c0 + 8 * FN * wn + 16 * j + 4 * g;
-        if (col < p.N)
-          store4_swiglu(p, r0 + row, col, acc[i][j], acc[i][j + FN / 2], sa, *reinterpret_cast<const float4*>(sw + col),
-                        *reinterpret_cast<const float4*>(sw + p.up_off + col));
-      }
+      for (int j = 0; j < kFrags; ++j)
+        if (col + 4 * j < p.N)
+          store4_swiglu(p, r0 + row, col + 4 * j, acc[i][j], acc[i][j + kFrags], sa,
+                        *reinterpret_cast<const float4*>(sw + col + 4 * j),
+                        *reinterpret_cast<const float4*>(sw + p.up_off + col + 4 * j));
     } else {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int col = c0 + 16 * FN * wn + 16 * j + 4 * g;
-        if (col < p.N) store4(p, r0 + row, col, acc[i][j], sa, *reinterpret_cast<const float4*>(sw + col));
-      }
+      for (int j = 0; j + 1 < kFrags; j += 2)
+        if (col + 4 * j < p.N)  // N is a multiple of 8, and so is col
+          store8(p, r0 + row, col + 4 * j, acc[i][j], acc[i][j + 1], sa,
+                 *reinterpret_cast<const float4*>(sw + col + 4 * j),
+                 *reinterpret_cast<const float4*>(sw + col + 4 * j + 4));
+      if constexpr (kFrags == 1)
+        if (col < p.N) store4(p, r0 + row, col, acc[i][0], sa, *reinterpret_cast<const float4*>(sw + col));
     }
   }
 }
 
 // Largest tile: 2 x 4 waves, 256 channels, blocks of up to 288 rows.
-typedef Shape<2, 4, 4, 2> Big;
+typedef Shape<2, 4, 4, 2, 1> Big;
 constexpr int kBigFM = 9;
-// 128 rows x 128 channels, 8 waves, four stages; 64 x 64, 4 waves, four
-// stages (two workgroups per CU).
-typedef Shape<2, 4, 2, 4> Mid;
+// 128 rows x 128 channels, 8 waves, four stages.
+typedef Shape<2, 4, 2, 4, 1> Mid;
 constexpr int kMidFM = 4;
-typedef Shape<2, 2, 2, 4> Small;
+// 64 x 64, four groups of 4 waves with two stages each: for few tiles, whose
+// time is the number of stages one after another.
+typedef Shape<2, 2, 2, 2, 4> Small;
 constexpr int kSmallFM = 2;
+
+// Few rows, 16 or 32 of them x 64 channels, where only the weight stream counts:
+// two groups of k and two workgroups per CU, so that one streams while the
+// other starts or ends a tile (Stream); with few tiles, narrow ones with eight
+// groups (Narrow), or four for gate/up.
+typedef Shape<1, 2, 2, 3, 2> Stream;
+typedef Shape<1, 2, 2, 2, 2> Stream64;  // 64 rows
+constexpr int kStreamLocal = 256;  // local experts (two workgroups fill the LDS)
+typedef Shape<1, 2, 1, 2, 8> Narrow;
+typedef Shape<1, 2, 2, 2, 4> NarrowGU;
 
 // Row caps of the largest tile (the fewest rounds of the grid win, weighted by
 // the tallest block, as in the bf16 grouped GEMM); the others have one.
 constexpr int kRowCaps = 6;
 __device__ constexpr int kRowCap[kRowCaps] = {288, 256, 224, 192, 160, 128};
+constexpr int kRowCapMin = 128;
 
-template <typename T, int FMMAX, bool SWIGLU, bool TAIL>
-__global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmArgs p) {
-  constexpr int kThreads = 64 * T::W;
+// MAXE: local experts its tables hold.
+template <typename T, int FMMAX, int MAXE, bool SWIGLU, bool TAIL>
+__global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
+  constexpr int kThreads = 64 * T::W * T::KG;
   constexpr bool kVary = FMMAX == kBigFM;  // block heights vary: a row cap is chosen
   constexpr int kBM = 16 * FMMAX * T::WR;
-  __shared__ __attribute__((aligned(1024))) char smem[T::S * stage_bytes<T, FMMAX>()];
-  __shared__ int s_off[kMaxLocal + 1];
-  __shared__ int s_tpre[kMaxLocal + 1];
-  __shared__ int s_tmp[T::W];
+  __shared__ __attribute__((aligned(1024))) char smem[T::KG * T::S * stage_bytes<T, FMMAX>()];
+  __shared__ int s_off[MAXE + 1];
+  __shared__ int s_tpre[MAXE];
+  __shared__ int s_tmp[T::W * T::KG];
   __shared__ unsigned long long s_ntile[kRowCaps];
   __shared__ int s_cand[kRowCaps];
   MOE_LDS char* lds = (MOE_LDS char*)smem;
   constexpr int kCols = SWIGLU ? T::BN / 2 : T::BN;
   const int ntn = (p.N + kCols - 1) / kCols;
-  constexpr int kPerT = kMaxLocal / kThreads;
+  constexpr int kPerT = (MAXE + kThreads - 1) / kThreads;
   int me[kPerT];
 #pragma unroll
   for (int q = 0; q < kPerT; ++q) {
@@ -466,136 +536,46 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmArgs p) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// Few rows: the weights straight into registers
-// ---------------------------------------------------------------------------
-// A workgroup takes 16 channels (gate/up: 16 gate and the 16 matching up) of
-// one expert for all of its rows, 16 G rows at a time; its 8 waves split k in
-// whole 128-byte lines where K allows, each with all loads of a step group in
-// flight, and their int32 partial sums meet in LDS (exact in any order).
-constexpr int kSkWaves = 8;
-
-template <bool SWIGLU, int G>
-__global__ void __launch_bounds__(64 * kSkWaves) skinny_kernel(GemmArgs p) {
-  constexpr int NB = SWIGLU ? 2 : 1;
-  constexpr int U = 8 / NB;  // steps of 64 k in flight
-  __shared__ int s_part[kSkWaves][NB][G][256];
-  const int ntn = (p.N + 15) / 16;
-  for (int64_t tile = blockIdx.x; tile < int64_t(p.E_local) * ntn; tile += gridDim.x) {
-  const int e = int(tile / ntn), nj = int(tile - int64_t(e) * ntn);
-  int seg0, seg1;
-  segment(p, e, seg0, seg1);
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = lane_id(), g = lane >> 4, l16 = lane & 15;
-  const int steps = (p.K + 63) / 64;
-  const int per = ((steps + kSkWaves - 1) / kSkWaves + 1) & ~1;  // whole lines
-  const int s0 = w * per, s1 = min(steps, s0 + per);
-  const int8_t* We = p.W + int64_t(e) * p.wrows * p.K;
-  const int8_t* wrow[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-    wrow[b] = We + int64_t(min(16 * nj + l16, p.N - 1) + (b ? p.up_off : 0)) * p.K + 16 * g;
-  const float* sw = p.sw + int64_t(e) * p.wrows;
-
-  for (int r0 = seg0; r0 < seg1; r0 += 16 * G) {
-    const int rows = min(16 * G, seg1 - r0);
-    const int8_t* arow[G];
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const int r = r0 + min(16 * i + l16, rows - 1);
-      arow[i] = p.A + int64_t(p.gather_src ? p.gather_src[r] / p.gather_k : r) * p.K + 16 * g;
-    }
-    i32x4 acc[NB][G];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < G; ++i) acc[b][i] = i32x4{0, 0, 0, 0};
-    for (int s = s0; s < s1; s += U) {
-      i32x4 qw[U][NB], qa[U][G];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // a step past this wave's range, or a chunk past K, reads the row's
-        // first chunk and counts as zeros
-        const bool in = s + u < s1 && 64 * (s + u) + 16 * g < p.K;
-        const int k = in ? 64 * (s + u) : -16 * g;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          qw[u][b] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wrow[b] + k));
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          qa[u][i] = *reinterpret_cast<const i32x4*>(arow[i] + k);
-          if (!in) qa[u][i] = i32x4{0, 0, 0, 0};
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < G; ++i) acc[b][i] = mfma(qw[u][b], qa[u][i], acc[b][i]);
-    }
-    // element v of lane (g, l16): channel 4 g + v of row l16, kept as 4 ints
-    // at 4 (l16 * 4 + g)
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        *reinterpret_cast<i32x4*>(&s_part[w][b][i][4 * (l16 * 4 + g)]) = acc[b][i];
-    __syncthreads();
-    for (int t = threadIdx.x; t < 64 * G; t += 64 * kSkWaves) {
-      const int i = t >> 6, slot = t & 63, row = 16 * i + (slot >> 2), col = 16 * nj + 4 * (slot & 3);
-      if (row < rows && col < p.N) {
-        i32x4 c[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          c[b] = i32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int q = 0; q < kSkWaves; ++q) c[b] += *reinterpret_cast<const i32x4*>(&s_part[q][b][i][4 * slot]);
-        }
-        const float sa = p.sa[p.gather_src ? p.gather_src[r0 + row] / p.gather_k : r0 + row];
-        if constexpr (SWIGLU)
-          store4_swiglu(p, r0 + row, col, c[0], c[1], sa, *reinterpret_cast<const float4*>(sw + col),
-                        *reinterpret_cast<const float4*>(sw + p.up_off + col));
-        else
-          store4(p, r0 + row, col, c[0], sa, *reinterpret_cast<const float4*>(sw + col));
-      }
-    }
-    __syncthreads();
-  }
-  }
-}
-
 template <bool SWIGLU>
 hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream) {
-  if (rows_hint <= 64) {
-    const dim3 grid(unsigned(std::min<int64_t>(p.E_local * ceil_div(p.N, 16), kMaxGrid))), block(64 * kSkWaves);
-    if (rows_hint <= 16)
-      hipLaunchKernelGGL((skinny_kernel<SWIGLU, 1>), grid, block, 0, stream, p);
-    else if (rows_hint <= 32)
-      hipLaunchKernelGGL((skinny_kernel<SWIGLU, 2>), grid, block, 0, stream, p);
-    else
-      hipLaunchKernelGGL((skinny_kernel<SWIGLU, 4>), grid, block, 0, stream, p);
-    return hipGetLastError();
-  }
   const bool tail = p.K % kRowB != 0;
   const int64_t cus = device_cu_count() / 8 * 8;
   auto tiles = [&](int bm, int cols) { return ceil_div(rows_hint, bm) * p.E_local * ceil_div(p.N, cols); };
-  auto bound = [&](int bm, int cols) { return (ceil_div(p.capacity, bm) + p.E_local) * ceil_div(p.N, cols); };
   constexpr int d = SWIGLU ? 2 : 1;
-  auto go = [&](auto shape, auto fm_t, int64_t n, int per_cu) {
+  auto go = [&](auto shape, auto fm_t, auto maxe_t, int bm, int per_cu) {
     typedef decltype(shape) T;
-    constexpr int FM = decltype(fm_t)::value;
+    constexpr int FM = decltype(fm_t)::value, MAXE = decltype(maxe_t)::value;
+    const int64_t n = (ceil_div(p.capacity, bm) + p.E_local) * ceil_div(p.N, T::BN / d);
     // the kernels index tiles with 31 bits
     if (n >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     const unsigned grid = unsigned(std::max<int64_t>(8, std::min<int64_t>(cus * per_cu, ceil_div(n, 8) * 8)));
-    auto* kern = tail ? tile_kernel<T, FM, SWIGLU, true> : tile_kernel<T, FM, SWIGLU, false>;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W), 0, stream, p);
+    auto* kern = tail ? tile_kernel<T, FM, MAXE, SWIGLU, true> : tile_kernel<T, FM, MAXE, SWIGLU, false>;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W * T::KG), 0, stream, p);
     return hipGetLastError();
   };
-  if (tiles(256, 256 / d) >= cus) return go(Big{}, std::integral_constant<int, kBigFM>{}, bound(128, 256 / d), 1);
-  if (tiles(128, 128 / d) >= cus / 2)
-    return go(Mid{}, std::integral_constant<int, kMidFM>{}, bound(128, 128 / d), 1);
-  return go(Small{}, std::integral_constant<int, kSmallFM>{}, bound(64, 64 / d), 2);
+  typedef std::integral_constant<int, kMaxLocal> AnyE;
+  typedef std::integral_constant<int, kStreamLocal> StreamE;
+  // Ragged segments spread around the expected length: twice as many rows as
+  // expected still make one block.
+  const int64_t rows = p.offsets ? 2 * rows_hint : rows_hint;
+  if (rows <= 32) {
+    auto few = [&](auto fm_t) {
+      constexpr int FM = decltype(fm_t)::value;
+      if (tiles(16 * FM, 64 / d) >= 2 * cus && p.E_local <= kStreamLocal)
+        return go(Stream{}, fm_t, StreamE{}, 16 * FM, 2);
+      if constexpr (SWIGLU)
+        return go(NarrowGU{}, fm_t, AnyE{}, 16 * FM, 1);
+      else
+        return go(Narrow{}, fm_t, AnyE{}, 16 * FM, 1);
+    };
+    return rows <= 16 ? few(std::integral_constant<int, 1>{}) : few(std::integral_constant<int, 2>{});
+  }
+  if (rows <= 64 && tiles(64, 64 / d) >= 2 * cus && p.E_local <= kStreamLocal)
+    return go(Stream64{}, std::integral_constant<int, 4>{}, StreamE{}, 64, 2);
+  if (tiles(256, 256 / d) >= cus)
+    return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
+  if (tiles(128, 128 / d) >= cus / 2) return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
+  return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
 }
 
 // ---------------------------------------------------------------------------

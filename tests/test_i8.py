@@ -240,7 +240,11 @@ def test_gemm_i8_large(M_, K, N):
     ([200, 0, 129, 1, 500, 128], 400, 2056, 70),      # middle tiles
     ([600, 0, 17, 289, 1000, 576, 1, 2000], 272, 4096, 11),  # the largest tiles, every block height
     ([0, 0, 0], 64, 64, 40),                          # no rows at all
-], ids=["skinny", "small", "mid", "big", "none"])
+    ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 4104, 2),        # streams: 16 rows a block
+    ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 400, 4096, 1),  # 32 rows
+    ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 4096, 3),  # 64 rows
+    ([i % 4 for i in range(300)], 144, 1032, 5),      # more experts than the streams' tables hold
+], ids=["narrow", "small", "mid", "big", "none", "stream16", "stream32", "stream64", "many"])
 def test_gemm_i8_segments(segs, K, N, behind):
     _check_gemm(sum(segs) + behind, K, N, segs)
 
@@ -274,7 +278,10 @@ def _weights(g, E, H, I):
     ([100, 1, 0, 240], 144, 208, 5),
     ([700, 300, 0, 33, 600], 208, 400, 2),
     ([520, 480, 0, 700, 511, 512, 513, 1], 256, 2048, 0),
-], ids=["one", "few", "decode", "small", "mid", "big"])
+    ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 1040, 1),
+    ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 272, 1040, 0),
+    ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 1040, 0),
+], ids=["one", "few", "decode", "small", "mid", "big", "stream16", "stream32", "stream64"])
 def test_expert_ffn_i8(segs, H, I, behind):
     g = _gen(4)
     E, cap = len(segs), sum(segs) + behind
