@@ -155,8 +155,9 @@ def _need(t, dtype, name, shape=None, dev=None, min_rows=False):
 
 def _placed(dev, **tensors):
     """Every given tensor (None: skipped) is contiguous and on the GPU dev."""
+    index = dev.index
     for name, t in tensors.items():
-        if t is None or (t.is_cuda and t.device == dev and t.is_contiguous()):
+        if t is None or (t.get_device() == index and t.is_contiguous() and t.is_cuda):
             continue
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -451,17 +452,17 @@ def _on_stream(fn):
     handed to them while another stream still uses it."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        dev = getattr(first, "device", None)
-        if dev is None or dev.type != "cuda":
+        torch = _torch()
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
             return fn(first, *args, **kw)  # refused by fn's checks
-        cuda = _torch().cuda
+        index = first.get_device()
         if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the call's tensors on {dev}")
-            with cuda.stream(stream):
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the call's tensors on {first.device}")
+            with torch.cuda.stream(stream):
                 return fn(first, *args, **kw)
-        if dev.index != cuda.current_device():
-            with cuda.device(dev):
+        if index != torch._C._cuda_getDevice():
+            with torch.cuda.device(index):
                 return fn(first, *args, **kw)
         return fn(first, *args, **kw)
     return call

@@ -47,7 +47,7 @@ def test_few_rejects(name, kw, want):
 
 def test_few_workspace_size():
     """The partial sums: with n experts in use there are at most min(T k, n T)
-    rows, each in at most ceil(2048 / (n panels)) ranges of at least 512."""
+    rows, each in at most ceil(1024 / (n panels)) ranges of at least 512."""
     assert M.FEW_TOKENS == 32
     assert M.few_workspace_size(33, 64, 64, 8, 2, 8) == 0
     for T, H, I, E, k, El in ((1, 7168, 256, 256, 8, 256), (16, 7168, 2048, 256, 8, 32), (32, 1024, 2816, 8, 2, 8),
@@ -58,7 +58,7 @@ def test_few_workspace_size():
             rows = min(cap, n * T)
 
             def ranges(K, items):
-                u, want = -(-K // 512), -(-2048 // items)
+                u, want = -(-K // 512), -(-1024 // items)
                 units = max(1, -(-u // want))
                 return -(-u // units)
             need = max(need, rows * ranges(H, n * pa) * pa * 128 * 4 + rows * ranges(I, n * pb) * H * 4)
