@@ -59,6 +59,9 @@ SIGNATURES = {
     "moe_forward_i8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
     "moe_forward_i8": (c_int, [_P, _P, _P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                _P, _P, c_size_t, _P]),
+    "moe_block_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "moe_block_forward": (c_int, [_P, c_int, _P, _P, _P, _P, _P, _P, _P, c_int, c_float, _P, c_float, c_int, c_int,
+                                  c_int, c_int, c_int, c_int, _P, _P, _P, c_size_t, _P]),
     "moe_norm_pre": (c_int, [_P, c_int, _P, c_float, c_int, c_int, _P, _P]),
     "moe_norm_post": (c_int, [_P, c_int, _P, c_int, _P, _P, c_int, c_float, _P, c_float, c_int, c_int, _P, _P, _P]),
 }
@@ -487,6 +490,21 @@ def _need_either(t, name, shape):
     return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
 
 
+def _gate_kind(gate, T, H):
+    """The MOE_GATE of a float32 gate by its shape: [H], [T, 1] or [T, H]."""
+    torch = _torch()
+    if gate is None:
+        return GATE_NONE
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
+    got = tuple(gate.shape)
+    kind = {(T, H): GATE_FULL, (T, 1): GATE_TOKEN, (H,): GATE_CHANNEL}.get(got)
+    if kind is None:
+        raise ValueError(f"gate has shape {got}, expected shape ({H},), ({T}, 1) or ({T}, {H})")
+    _need(gate, torch.float32, "gate")
+    return kind
+
+
 @_on_stream
 def moe_norm_pre(r, w, eps=1e-6, *, out=None):
     """The norm before the block: out [T, H] bf16 = r / sqrt(mean(r^2) + eps) * w.
@@ -521,15 +539,7 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
     rt = _need_either(residual, "residual", (T, H))
     if w_post is not None:
         _need(w_post, torch.float32, "w_post", (H,))
-    kind = GATE_NONE
-    if gate is not None:
-        if not isinstance(gate, torch.Tensor):
-            raise TypeError("gate must be a torch.Tensor")
-        got = tuple(gate.shape)
-        kind = {(T, H): GATE_FULL, (T, 1): GATE_TOKEN, (H,): GATE_CHANNEL}.get(got)
-        if kind is None:
-            raise ValueError(f"gate has shape {got}, expected shape ({H},), ({T}, 1) or ({T}, {H})")
-        _need(gate, torch.float32, "gate")
+    kind = _gate_kind(gate, T, H)
     if w_next is not None:
         _need(w_next, torch.float32, "w_next", (H,))
     elif normed is not None:
@@ -731,3 +741,56 @@ def moe_forward_i8(x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, k, e
                           _nbytes(ws), _stream(None, dev))
     check(st, "moe_forward_i8")
     return y, ws
+
+
+def block_workspace_size(T, H, I, E, k) -> int:
+    return int(lib().moe_block_workspace_size(T, H, I, E, k))
+
+
+@_on_stream
+def moe_block_forward(residual, w_pre, w_router, bias, w_gate_up, w_down, k, w_post=None, *, gate=None,
+                      residual_scale=1.0, w_next=None, eps=1e-6, renormalize=True, out=None, normed=None,
+                      workspace=None):
+    """A whole block with every expert on this GPU: moe_norm_pre of
+    ``residual`` [T, H], the MoE layer, moe_norm_post. Returns (out, normed or
+    None, workspace). Takes ``stream``."""
+    torch = _torch()
+    rt = _need_either(residual, "residual", (None, None))
+    T, H = residual.shape
+    _need(w_pre, torch.float32, "w_pre", (H,))
+    _need(w_router, torch.float32, "w_router", (None, H))
+    E = w_router.shape[0]
+    if bias is not None:
+        _need(bias, torch.float32, "bias", (E,))
+    _need(w_gate_up, torch.bfloat16, "w_gate_up", (E, H, None))
+    I2 = w_gate_up.shape[2]
+    if I2 % 2:
+        raise ValueError(f"w_gate_up's last dimension 2I must be even, got {I2}")
+    I = I2 // 2
+    _need(w_down, torch.bfloat16, "w_down", (E, I, H))
+    _check_k(k, E)
+    if w_post is not None:
+        _need(w_post, torch.float32, "w_post", (H,))
+    kind = _gate_kind(gate, T, H)
+    if w_next is not None:
+        _need(w_next, torch.float32, "w_next", (H,))
+    elif normed is not None:
+        raise ValueError("normed is given without w_next")
+    if out is not None:
+        _need(out, residual.dtype, "out", (T, H))
+    if normed is not None:
+        _need(normed, torch.bfloat16, "normed", (T, H))
+    dev = residual.device
+    _placed(dev, residual=residual, w_pre=w_pre, w_router=w_router, bias=bias, w_gate_up=w_gate_up, w_down=w_down,
+            w_post=w_post, gate=gate, w_next=w_next)
+    out = _out(out, (T, H), residual.dtype, dev, "out")
+    if w_next is not None:
+        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+    L = lib()
+    ws = _workspace(L.moe_block_workspace_size(T, H, I, E, k), dev, workspace)
+    st = L.moe_block_forward(_ptr(residual), rt, _ptr(w_pre), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down),
+                             _ptr(w_post), _ptr(gate), kind, residual_scale, _ptr(w_next), eps, T, H, I, E, k,
+                             int(bool(renormalize)), _ptr(out), _ptr(normed), _ptr(ws), _nbytes(ws),
+                             _stream(None, dev))
+    check(st, "moe_block_forward")
+    return out, normed, ws

@@ -1,6 +1,7 @@
 // C-ABI of the MoE rank-share library: argument checks, workspace layout and
 // the one-stream forward pass. Every check runs on the host before any launch.
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "moe.h"
@@ -584,6 +585,19 @@ static int check_norm(int T, int H, float eps) {
 }
 static bool type_ok(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 
+// moe_norm_post's sizes, types and optional arguments.
+static int check_post(int r_type, int y_type, const float* gate, int gate_kind, const float* w_next,
+                      const moe_bf16* normed, int T, int H, float eps) {
+  const int st = check_norm(T, H, eps);
+  if (st != MOE_OK) return st;
+  if (!type_ok(y_type) || !type_ok(r_type) || gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // (empty arrays may be NULL)
+  if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr) || (w_next == nullptr) != (normed == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 int moe_norm_pre(const void* r, int r_type, const float* w, float eps, int T, int H, moe_bf16* out,
                  hipStream_t stream) {
   const int st = check_norm(T, H, eps);
@@ -598,19 +612,74 @@ int moe_norm_pre(const void* r, int r_type, const float* w, float eps, int T, in
 int moe_norm_post(const void* y, int y_type, const void* residual, int r_type, const float* w_post,
                   const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
                   int H, void* out, moe_bf16* normed, hipStream_t stream) {
-  const int st = check_norm(T, H, eps);
-  if (st != MOE_OK) return st;
-  if (!type_ok(y_type) || !type_ok(r_type) || gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL)
-    return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;  // (empty arrays may be NULL)
-  if ((gate_kind == MOE_GATE_NONE) != (gate == nullptr) || (w_next == nullptr) != (normed == nullptr))
-    return MOE_ERR_INVALID_ARG;
+  const int st = check_post(r_type, y_type, gate, gate_kind, w_next, normed, T, H, eps);
+  if (st != MOE_OK || T == 0) return st;
   if (!y || !residual || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(y) || !aligned16(residual) || !aligned16(out) || !aligned16(w_post) || !aligned16(w_next) ||
       !aligned16(normed) || (gate_kind != MOE_GATE_TOKEN && !aligned16(gate)))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_block_norm(y, y_type == MOE_TYPE_F32 ? 2 : 1, residual, r_type == MOE_TYPE_F32, w_post,
                                       gate, gate_kind, residual_scale, w_next, eps, T, H, out, normed, stream));
+}
+
+// The block's own buffers, then the layer's workspace. Up to 16 tokens the
+// two-kernel layer is the faster one at every shape measured (DeepSeek-R1 EP=8
+// share 34 us against 134 at one token, 204 against 257 at 16); at 24 to 32 the
+// two are within 10% of each other either way.
+static bool block_is_few(int T, int I, int E, int k) { return T <= 16 && few_supported(T, I, k, E); }
+struct BlockLayout {
+  size_t x, y, layer, total;
+};
+static BlockLayout block_layout(int T, int H, int I, int E, int k) {
+  BlockLayout L{};
+  L.y = align_up(size_t(T) * H * sizeof(uint16_t));
+  L.layer = L.y + align_up(size_t(T) * H * sizeof(float));
+  L.total = L.layer + (block_is_few(T, I, E, k) ? few_workspace_bytes(T, H, I, E, k, E)
+                                                : forward_layout(T, H, I, E, k, E).total);
+  return L;
+}
+
+size_t moe_block_workspace_size(int T, int H, int I, int E, int k) {
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0) return 0;
+  return block_layout(T, H, I, E, k).total;
+}
+
+int moe_block_forward(const void* residual, int r_type, const float* w_pre, const float* w_router,
+                      const float* bias, const moe_bf16* w_gate_up, const moe_bf16* w_down, const float* w_post,
+                      const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
+                      int H, int I, int E, int k, int renormalize, void* out, moe_bf16* normed, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  // every step's checks before the first launch
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (!expert_weights_fit(H, I) || min_capacity(T, k, E) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if ((st = check_post(r_type, MOE_TYPE_F32, gate, gate_kind, w_next, normed, T, H, eps)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!residual || !w_pre || !w_router || !w_gate_up || !w_down || !out) return MOE_ERR_INVALID_ARG;
+  for (const void* q : {residual, static_cast<const void*>(w_pre), static_cast<const void*>(w_router),
+                        static_cast<const void*>(w_gate_up), static_cast<const void*>(w_down),
+                        static_cast<const void*>(w_post), static_cast<const void*>(w_next),
+                        static_cast<const void*>(out), static_cast<const void*>(normed)})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (gate_kind != MOE_GATE_TOKEN && !aligned16(gate)) return MOE_ERR_INVALID_ARG;
+  const BlockLayout L = block_layout(T, H, I, E, k);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < L.total)
+    return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  moe_bf16* x = reinterpret_cast<moe_bf16*>(ws + L.x);
+  float* y = reinterpret_cast<float*>(ws + L.y);
+  st = moe_norm_pre(residual, r_type, w_pre, eps, T, H, x, stream);
+  if (st == MOE_OK)
+    st = block_is_few(T, I, E, k)
+             ? moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, 0, E, renormalize, y,
+                                   ws + L.layer, workspace_bytes - L.layer, stream)
+             : moe_forward_f32(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, 0, E, renormalize, y,
+                               ws + L.layer, workspace_bytes - L.layer, stream);
+  if (st == MOE_OK)
+    st = moe_norm_post(y, MOE_TYPE_F32, residual, r_type, w_post, gate, gate_kind, residual_scale, w_next, eps, T, H,
+                       out, normed, stream);
+  return st;
 }
 
 }  // extern "C"

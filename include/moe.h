@@ -469,6 +469,26 @@ int moe_norm_post(const void* y, int y_type, const void* residual, int r_type, c
                   const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
                   int H, void* out, moe_bf16* normed, hipStream_t stream);
 
+/*
+ * A whole block on one GPU (all E experts local), on one stream:
+ *   x   = rms(residual) * w_pre                          (moe_norm_pre)
+ *   y   = the MoE layer of x, float32                    (moe_forward_few_f32
+ *         up to 16 tokens, moe_forward_f32 above)
+ *   out = residual_scale * residual + gate * rms(y) * w_post,
+ *   normed = rms(out) * w_next                           (moe_norm_post)
+ * w_post, gate / gate_kind, w_next / normed, r_type, out in place and their
+ * checks are moe_norm_post's; the layer's are moe_forward's with e0 = 0,
+ * E_local = E; w_pre as in moe_norm_pre. Under expert parallelism the shares
+ * are summed over the ranks between the layer and the second norm: call the
+ * three steps. workspace: moe_block_workspace_size bytes, 256-byte aligned.
+ */
+size_t moe_block_workspace_size(int T, int H, int I, int E, int k);
+int moe_block_forward(const void* residual, int r_type, const float* w_pre, const float* w_router,
+                      const float* bias, const moe_bf16* w_gate_up, const moe_bf16* w_down, const float* w_post,
+                      const float* gate, int gate_kind, float residual_scale, const float* w_next, float eps, int T,
+                      int H, int I, int E, int k, int renormalize, void* out, moe_bf16* normed, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
