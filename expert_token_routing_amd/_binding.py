@@ -484,10 +484,12 @@ def _need_either(t, name, shape):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    _need(t, t.dtype, name, shape)
-    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+    dtype = t.dtype
+    kind = TYPE_BF16 if dtype == torch.bfloat16 else TYPE_F32 if dtype == torch.float32 else -1
+    if kind < 0:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    _need(t, dtype, name, shape)
+    return kind
 
 
 def _gate_kind(gate, T, H):
@@ -498,8 +500,13 @@ def _gate_kind(gate, T, H):
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     got = tuple(gate.shape)
-    kind = {(T, H): GATE_FULL, (T, 1): GATE_TOKEN, (H,): GATE_CHANNEL}.get(got)
-    if kind is None:
+    if got == (T, 1):
+        kind = GATE_TOKEN
+    elif got == (H,):
+        kind = GATE_CHANNEL
+    elif got == (T, H):
+        kind = GATE_FULL
+    else:
         raise ValueError(f"gate has shape {got}, expected shape ({H},), ({T}, 1) or ({T}, {H})")
     _need(gate, torch.float32, "gate")
     return kind

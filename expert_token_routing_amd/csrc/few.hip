@@ -840,9 +840,10 @@ inline Layout layout(int T, int H, int I, int E, int k, int E_local) {
 }  // namespace few
 
 bool few_supported(int T, int I, int k, int E_local) {
-  // the counters are indexed with 31 bits: 32 of them per 128 columns of each
-  // expert in use
-  return int64_t(std::min<int64_t>(E_local, int64_t(T) * k)) * I < (int64_t(1) << 32);
+  // the counters are indexed with 31 bits (32 of them per 128 columns of each
+  // expert in use), an expert's rows of h with 32 (in bytes, at most T of them)
+  return int64_t(std::min<int64_t>(E_local, int64_t(T) * k)) * I < (int64_t(1) << 32) &&
+         int64_t(T) * I < (int64_t(1) << 29);
 }
 
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {

@@ -647,47 +647,55 @@ template <bool F32, int NV>
 __global__ void __launch_bounds__(1024) quantize_rows_kernel(const void* x, const int32_t* end, int M, int nvec,
                                                              int8_t* q, float* scale) {
   __shared__ uint32_t s_red[16];
-  const int64_t rows = end != nullptr ? min(M, *end) : M;
-  for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
-  float v[NV ? NV : 1][8];
-  uint32_t top = 0;
-  if constexpr (NV > 0) {
+  constexpr int kKeep = NV ? NV : 1;
+  float v[kKeep][8];
+  auto load_row = [&](int64_t m) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = int(threadIdx.x) + i * int(blockDim.x);
-      if (c < nvec) {
-        load8<F32>(v[i], x, m * nvec + c);
+      if (c < nvec) load8<F32>(v[i], x, m * nvec + c);
+    }
+  };
+  int64_t m = blockIdx.x;
+  load_row(m);  // (m < M: in the array even if it lies past *end, which is still on its way)
+  const int64_t rows = end != nullptr ? min(M, *end) : M;
+  while (m < rows) {
+    uint32_t top = 0;
+    if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[i][j]));
+      for (int i = 0; i < NV; ++i)
+        if (int(threadIdx.x) + i * int(blockDim.x) < nvec)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[i][j]));
+    } else {
+      for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+        load8<F32>(v[0], x, m * nvec + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[0][j]));
       }
     }
-  } else {
-    for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-      load8<F32>(v[0], x, m * nvec + c);
+    const RowScale rs(block_max(top, s_red));
+    if (threadIdx.x == 0) scale[m] = rs.scale;
+    auto put = [&](const float (&f)[8], int c) {
+      reinterpret_cast<uint2*>(q)[m * nvec + c] =
+          make_uint2(pack4(rs.q(f[0]), rs.q(f[1]), rs.q(f[2]), rs.q(f[3])),
+                     pack4(rs.q(f[4]), rs.q(f[5]), rs.q(f[6]), rs.q(f[7])));
+    };
+    if constexpr (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(v[0][j]));
+      for (int i = 0; i < NV; ++i) {
+        const int c = int(threadIdx.x) + i * int(blockDim.x);
+        if (c < nvec) put(v[i], c);
+      }
+    } else {
+      for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
+        load8<F32>(v[0], x, m * nvec + c);
+        put(v[0], c);
+      }
     }
-  }
-  const RowScale rs(block_max(top, s_red));
-  if (threadIdx.x == 0) scale[m] = rs.scale;
-  auto put = [&](const float (&f)[8], int c) {
-    reinterpret_cast<uint2*>(q)[m * nvec + c] =
-        make_uint2(pack4(rs.q(f[0]), rs.q(f[1]), rs.q(f[2]), rs.q(f[3])),
-                   pack4(rs.q(f[4]), rs.q(f[5]), rs.q(f[6]), rs.q(f[7])));
-  };
-  if constexpr (NV > 0) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = int(threadIdx.x) + i * int(blockDim.x);
-      if (c < nvec) put(v[i], c);
-    }
-  } else {
-    for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-      load8<F32>(v[0], x, m * nvec + c);
-      put(v[0], c);
-    }
-  }
-  __syncthreads();  // s_red is free again
+    m += gridDim.x;
+    if (m < rows) load_row(m);
+    __syncthreads();  // s_red is free again
   }
 }
 

@@ -43,10 +43,11 @@ struct Args {
 template <bool F32>
 struct Raw {
   u32x4 v[F32 ? 2 : 1];
+  template <bool NT>
   __device__ __forceinline__ void load(const void* base, int64_t vec) {
     const u32x4* p = static_cast<const u32x4*>(base) + vec * (F32 ? 2 : 1);
-    v[0] = p[0];
-    if constexpr (F32) v[1] = p[1];
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = NT ? __builtin_nontemporal_load(p + i) : p[i];
   }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (F32)
@@ -62,9 +63,17 @@ __device__ __forceinline__ void load8(float (&o)[8], const float* p) {
   o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
 }
 
+template <bool NT>
+__device__ __forceinline__ void store16(u32x4* p, const u32x4& v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+template <bool NT>
 __device__ __forceinline__ void store8_bf16(void* base, int64_t vec, const float (&f)[8]) {
-  static_cast<u32x4*>(base)[vec] = u32x4{cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
-                                         cvt_bf16x2(f[6], f[7])};
+  store16<NT>(static_cast<u32x4*>(base) + vec, u32x4{cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
+                                                     cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7])});
 }
 
 // Sum over the workgroup, the same on every thread. Consecutive calls take
@@ -83,7 +92,8 @@ __device__ __forceinline__ float block_sum(float v, float* s_red, int half) {
 }
 
 // Y: 0 no block output (norm before the block: r alone), 1 bf16, 2 float32.
-template <int Y, bool RF32, int NV>
+// NT: the rows go past the caches (more of them than the caches hold).
+template <int Y, bool RF32, int NV, bool NT>
 __global__ void __launch_bounds__(kThreadsMax<NV>) block_norm_kernel(Args a) {
   constexpr bool kKeep = NV <= 2;  // weights in registers, next row prefetched
   constexpr bool YF32 = Y == 2;
@@ -112,8 +122,8 @@ __global__ void __launch_bounds__(kThreadsMax<NV>) block_norm_kernel(Args a) {
   auto load_row = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (Y != 0) qy[i].load(a.y, row * a.nvec + vec[i]);
-      qr[i].load(a.r, row * a.nvec + vec[i]);
+      if constexpr (Y != 0) qy[i].template load<NT>(a.y, row * a.nvec + vec[i]);
+      qr[i].template load<NT>(a.r, row * a.nvec + vec[i]);
     }
   };
   if constexpr (kKeep) load_row(t);
@@ -174,11 +184,13 @@ __global__ void __launch_bounds__(kThreadsMax<NV>) block_norm_kernel(Args a) {
         if (in[i]) {
           const int64_t at = t * a.nvec + vec[i];
           if constexpr (RF32) {
-            float4* o = reinterpret_cast<float4*>(a.out) + 2 * at;
-            o[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-            o[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+            u32x4* o = static_cast<u32x4*>(a.out) + 2 * at;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              store16<NT>(o + h, u32x4{__float_as_uint(v[i][4 * h]), __float_as_uint(v[i][4 * h + 1]),
+                                       __float_as_uint(v[i][4 * h + 2]), __float_as_uint(v[i][4 * h + 3])});
           } else {
-            store8_bf16(a.out, at, v[i]);
+            store8_bf16<NT>(a.out, at, v[i]);
           }
         }
       }
@@ -200,14 +212,14 @@ __global__ void __launch_bounds__(kThreadsMax<NV>) block_norm_kernel(Args a) {
         float n[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = v[i][j] * inv * wn[kKeep ? i : 0][j];
-        if (in[i]) store8_bf16(a.normed, t * a.nvec + vec[i], n);
+        if (in[i]) store8_bf16<NT>(a.normed, t * a.nvec + vec[i], n);
       }
     }
   }
 }
 
-template <int Y, bool RF32>
-hipError_t launch(const Args& a, hipStream_t stream) {
+template <int Y, bool RF32, bool NT>
+hipError_t launch_as(const Args& a, hipStream_t stream) {
   const int cus = device_cu_count();
   // Few rows: one vector per thread, the shortest chain of a row. Many rows:
   // two vectors per thread from 513 vectors on, so that two or more rows are
@@ -215,15 +227,27 @@ hipError_t launch(const Args& a, hipStream_t stream) {
   const bool many = a.T > 2 * cus;
   const int nv = a.nvec <= (many ? 512 : 1024) ? 1 : a.nvec <= 1024 ? 2 : 4;
   const int nt = int(ceil_div(ceil_div(a.nvec, nv), 64) * 64);
-  const int per_cu = std::max(1, std::min(16, 1024 / nt));
+  const int per_cu = std::max(1, std::min(16, 2048 / nt));
   const unsigned grid = unsigned(std::min<int64_t>(a.T, int64_t(cus) * per_cu));
   if (nv == 1)
-    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 1>), dim3(grid), dim3(nt), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 1, NT>), dim3(grid), dim3(nt), 0, stream, a);
   else if (nv == 2)
-    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 2>), dim3(grid), dim3(nt), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 2, NT>), dim3(grid), dim3(nt), 0, stream, a);
   else
-    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 4>), dim3(grid), dim3(nt), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<Y, RF32, 4, NT>), dim3(grid), dim3(nt), 0, stream, a);
   return hipGetLastError();
+}
+
+// Rows of more than the 256 MB of the last-level cache in all are not there any
+// more when the next kernel reads them: they pass by (16384 x 7168 after a
+// float32 block output: 201 us against 228; norm before it: 84 against 89).
+// Fewer stay cached (16384 x 512: 16.7 us cached, 18.4 passed by).
+constexpr int64_t kPassBy = int64_t(256) << 20;
+
+template <int Y, bool RF32>
+hipError_t launch(const Args& a, hipStream_t stream) {
+  const int64_t per = (Y == 0 ? 0 : Y == 1 ? 2 : 4) + (RF32 ? 4 : 2) + (a.out ? (RF32 ? 4 : 2) : 0) + (a.normed ? 2 : 0);
+  return int64_t(a.T) * a.H * per > kPassBy ? launch_as<Y, RF32, true>(a, stream) : launch_as<Y, RF32, false>(a, stream);
 }
 
 }  // namespace norm

@@ -357,3 +357,27 @@ def test_forward_i8_equals_its_steps(T, H, I, E, k, e0, El):
     side.synchronize()
     assert torch.equal(y3.view(torch.int16), ref.view(torch.int16))
     assert M.moe_forward_i8(x[:0], wr, None, *w, k, e0)[0].shape == (0, H)
+
+
+@gpu
+def test_i8_offsets_beyond_32_bits():
+    """Rows and outputs past 2^31 elements."""
+    M_, K, N = 300001, 7168, 7168
+    g = _gen(6)
+    at = torch.tensor([0, 149797, 299593, M_ - 1], device="cuda")
+    x = torch.zeros((M_, K), dtype=BF, device="cuda")
+    x[at] = torch.randn((4, K), generator=g, device="cuda").to(BF)
+    print(f"[gpu] quantize_rows M={M_} K={K}", flush=True)
+    q, s = M.moe_quantize_rows(x)
+    torch.cuda.synchronize()
+    rq, rs = _quantized(x[at])
+    assert torch.equal(q[at].to(F64), rq) and bool((s[at] == rs.float()).all()) and int(s.ne(0).sum()) == 4
+    del x
+    a = q[:, :32].contiguous()
+    del q
+    w, sw = _rand_i8(g, 1, N, 32), torch.rand((1, N), generator=g, device="cuda") + 0.01
+    print(f"[gpu] gemm_i8 M={M_} K=32 N={N}", flush=True)
+    out = M.moe_gemm_i8(a, s, w, sw)
+    torch.cuda.synchronize()
+    _close(out[at], (a[at].to(F64) @ w[0].to(F64).T) * s[at, None].to(F64) * sw[0].to(F64), REL, "out")
+    assert int(out.abs().amax(1).gt(0).sum()) == 4

@@ -232,3 +232,26 @@ def test_norm_replays_and_other_stream():
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and torch.equal(normed, nref)
         M.moe_norm_post(y, r, wp, gate=ga, w_next=wn)
+
+
+@gpu
+@pytest.mark.parametrize("T,H", [(16384, 4096), (16384, 8200), (70000, 2048)])
+def test_norm_post_past_the_caches(T, H):
+    """More rows than the caches hold take the loads and stores that pass them."""
+    _check_post(T, H, F32, BF, "channel", True, True, 0.5)
+    _check_post(T, H, BF, F32, "token", False, True, 1.0)
+
+
+@gpu
+def test_norm_pre_offsets_beyond_32_bits():
+    T, H = 300001, 7168
+    w = 1 + 0.1 * torch.randn(H, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    r = torch.zeros((T, H), dtype=BF, device="cuda")
+    at = torch.tensor([0, 149796, 149797, 299593, T - 1], device="cuda")  # around 2^30 and 2^31 elements, and the ends
+    r[at] = torch.randn((5, H), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF)
+    print(f"[gpu] norm_pre T={T} H={H}", flush=True)
+    out = M.moe_norm_pre(r, w, EPS)
+    torch.cuda.synchronize()
+    ref = _rms(r[at].to(F64), w)
+    _within(out[at], ref, U * ref.abs(), "out")
+    assert int(out.abs().amax(1).gt(0).sum()) == 5
