@@ -492,6 +492,29 @@ def _need_either(t, name, shape):
     return kind
 
 
+def _fits(*specs):
+    """Whether every (tensor or None, dtype, shape) is a contiguous tensor of
+    that type and shape on the GPU of the first one. Quick, and silent: where it
+    says no, the checks that follow say what is wrong."""
+    try:
+        index = specs[0][0].get_device()
+        if index < 0:
+            return False
+        for t, dtype, shape in specs:
+            if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                                  or not t.is_contiguous()):
+                return False
+    except AttributeError:  # not a tensor
+        return False
+    return True
+
+
+def _dims(t, n):
+    """The shape of an n-dimensional tensor, None for anything else."""
+    shape = getattr(t, "shape", None)
+    return shape if shape is not None and len(shape) == n else None
+
+
 def _gate_kind(gate, T, H):
     """The MOE_GATE of a float32 gate by its shape: [H], [T, 1] or [T, H]."""
     torch = _torch()
@@ -517,14 +540,20 @@ def moe_norm_pre(r, w, eps=1e-6, *, out=None):
     """The norm before the block: out [T, H] bf16 = r / sqrt(mean(r^2) + eps) * w.
     ``r`` [T, H] is bf16 or float32, ``w`` [H] float32. Takes ``stream``."""
     torch = _torch()
-    rt = _need_either(r, "r", (None, None))
-    T, H = r.shape
-    _need(w, torch.float32, "w", (H,))
-    if out is not None:
-        _need(out, torch.bfloat16, "out", (T, H))
+    shape = _dims(r, 2)
+    if not (shape and r.dtype in (torch.bfloat16, torch.float32)
+            and _fits((r, r.dtype, shape), (w, torch.float32, shape[1:]), (out, torch.bfloat16, shape))):
+        _need_either(r, "r", (None, None))
+        shape = r.shape
+        _need(w, torch.float32, "w", shape[1:])
+        if out is not None:
+            _need(out, torch.bfloat16, "out", shape)
+        _placed(r.device, r=r, w=w, out=out)
+    T, H = shape
+    rt = TYPE_BF16 if r.dtype == torch.bfloat16 else TYPE_F32
     dev = r.device
-    _placed(dev, r=r, w=w)
-    out = _out(out, (T, H), torch.bfloat16, dev, "out")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     check(lib().moe_norm_pre(_ptr(r), rt, _ptr(w), eps, T, H, _ptr(out), _stream(None, dev)), "moe_norm_pre")
     return out
 
@@ -541,25 +570,37 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
     [H] (per channel), [T, 1] (per token) or [T, H]. ``out`` may be
     ``residual``. Takes ``stream``."""
     torch = _torch()
-    yt = _need_either(y, "y", (None, None))
-    T, H = y.shape
-    rt = _need_either(residual, "residual", (T, H))
-    if w_post is not None:
-        _need(w_post, torch.float32, "w_post", (H,))
+    shape, f32 = _dims(y, 2), torch.float32
+    types = (torch.bfloat16, f32)
+    if not (shape and y.dtype in types and getattr(residual, "dtype", None) in types
+            and (gate is None or isinstance(gate, torch.Tensor)) and (normed is None or w_next is not None)
+            and _fits((y, y.dtype, shape), (residual, residual.dtype, shape), (w_post, f32, shape[1:]),
+                      (w_next, f32, shape[1:]), (gate, f32, getattr(gate, "shape", None)),
+                      (out, residual.dtype, shape), (normed, torch.bfloat16, shape))):
+        _need_either(y, "y", (None, None))
+        shape = y.shape
+        _need_either(residual, "residual", shape)
+        if w_post is not None:
+            _need(w_post, f32, "w_post", shape[1:])
+        _gate_kind(gate, *shape)
+        if w_next is not None:
+            _need(w_next, f32, "w_next", shape[1:])
+        elif normed is not None:
+            raise ValueError("normed is given without w_next")
+        if out is not None:
+            _need(out, residual.dtype, "out", shape)
+        if normed is not None:
+            _need(normed, torch.bfloat16, "normed", shape)
+        _placed(y.device, y=y, residual=residual, w_post=w_post, gate=gate, w_next=w_next, out=out, normed=normed)
+    T, H = shape
     kind = _gate_kind(gate, T, H)
-    if w_next is not None:
-        _need(w_next, torch.float32, "w_next", (H,))
-    elif normed is not None:
-        raise ValueError("normed is given without w_next")
-    if out is not None:
-        _need(out, residual.dtype, "out", (T, H))
-    if normed is not None:
-        _need(normed, torch.bfloat16, "normed", (T, H))
+    yt = TYPE_BF16 if y.dtype == torch.bfloat16 else TYPE_F32
+    rt = TYPE_BF16 if residual.dtype == torch.bfloat16 else TYPE_F32
     dev = y.device
-    _placed(dev, y=y, residual=residual, w_post=w_post, gate=gate, w_next=w_next)
-    out = _out(out, (T, H), residual.dtype, dev, "out")
-    if w_next is not None:
-        normed = _out(normed, (T, H), torch.bfloat16, dev, "normed")
+    if out is None:
+        out = torch.empty_like(residual)
+    if w_next is not None and normed is None:
+        normed = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     st = lib().moe_norm_post(_ptr(y), yt, _ptr(residual), rt, _ptr(w_post), _ptr(gate), kind, residual_scale,
                              _ptr(w_next), eps, T, H, _ptr(out), _ptr(normed), _stream(None, dev))
     check(st, "moe_norm_post")
@@ -575,11 +616,22 @@ def few_workspace_size(T, H, I, E, k, E_local) -> int:
 
 
 def _few(name, out_dtype, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y, workspace):
-    T, H, I, E, E_local, dev = _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
-    if y is not None:
-        _need(y, out_dtype, "y", (T, H))
-    _forward_placed(dev, x, w_router, bias, w_gate_up, w_down)
-    y = _out(y, (T, H), out_dtype, dev, "y")
+    torch = _torch()
+    mx, mr, mg = _dims(x, 2), _dims(w_router, 2), _dims(w_gate_up, 3)
+    if not (mx and mr and mg and mr[1] == mg[1] == mx[1] and mg[2] % 2 == 0 and type(k) is int and 1 <= k <= mr[0]
+            and 0 <= e0 <= mr[0] - mg[0]
+            and _fits((x, torch.bfloat16, mx), (w_router, torch.float32, mr), (bias, torch.float32, mr[:1]),
+                      (w_gate_up, torch.bfloat16, mg), (w_down, torch.bfloat16, (mg[0], mg[2] // 2, mx[1])),
+                      (y, out_dtype, mx))):
+        _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
+        mx, mr, mg = x.shape, w_router.shape, w_gate_up.shape
+        if y is not None:
+            _need(y, out_dtype, "y", mx)
+        _placed(x.device, x=x, w_router=w_router, bias=bias, w_gate_up=w_gate_up, w_down=w_down, y=y)
+    (T, H), E, E_local, I = mx, mr[0], mg[0], mg[2] // 2
+    dev = x.device
+    if y is None:
+        y = torch.empty(mx, dtype=out_dtype, device=dev)
     L = lib()
     ws = _workspace(L.moe_few_workspace_size(T, H, I, E, k, E_local), dev, workspace)
     st = getattr(L, name)(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down), T, H, I, E, k, e0,
@@ -611,16 +663,21 @@ def moe_quantize_rows(x, *, q=None, scale=None):
     """q [M, K] int8 and scale [M] float32 of x [M, K] bf16: scale = max|x| / 127
     per row, q = x / scale to the nearest integer. Takes ``stream``."""
     torch = _torch()
-    _need(x, torch.bfloat16, "x", (None, None))
-    M, K = x.shape
-    if q is not None:
-        _need(q, torch.int8, "q", (M, K))
-    if scale is not None:
-        _need(scale, torch.float32, "scale", (M,))
+    shape = _dims(x, 2)
+    if not (shape and _fits((x, torch.bfloat16, shape), (q, torch.int8, shape), (scale, torch.float32, shape[:1]))):
+        _need(x, torch.bfloat16, "x", (None, None))
+        shape = x.shape
+        if q is not None:
+            _need(q, torch.int8, "q", shape)
+        if scale is not None:
+            _need(scale, torch.float32, "scale", shape[:1])
+        _placed(x.device, x=x, q=q, scale=scale)
+    M, K = shape
     dev = x.device
-    _placed(dev, x=x)
-    q = _out(q, (M, K), torch.int8, dev, "q")
-    scale = _out(scale, (M,), torch.float32, dev, "scale")
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
     check(lib().moe_quantize_rows(_ptr(x), M, K, _ptr(q), _ptr(scale), _stream(None, dev)), "moe_quantize_rows")
     return q, scale
 
@@ -653,21 +710,28 @@ def moe_gemm_i8(a, a_scale, w, w_scale, offsets=None, *, out=None):
     matrix for all rows). a [M, K] and w [E_local, N, K] are int8, the scales
     [M] and [E_local, N] float32. Takes ``stream``."""
     torch = _torch()
-    _need(a, torch.int8, "a", (None, None))
-    M, K = a.shape
-    _need(a_scale, torch.float32, "a_scale", (M,))
-    _need(w, torch.int8, "w", (None, None, K))
-    E_local, N, _ = w.shape
-    _need(w_scale, torch.float32, "w_scale", (E_local, N))
-    if offsets is not None:
-        _need(offsets, torch.int32, "offsets", (E_local + 1,))
-    elif E_local != 1:
-        raise ValueError(f"w holds {E_local} matrices: offsets is required")
-    if out is not None:
-        _need(out, torch.bfloat16, "out", (M, N))
+    ma, mw = _dims(a, 2), _dims(w, 3)
+    if not (ma and mw and mw[2] == ma[1] and (offsets is not None or mw[0] == 1)
+            and _fits((a, torch.int8, ma), (a_scale, torch.float32, ma[:1]), (w, torch.int8, mw),
+                      (w_scale, torch.float32, mw[:2]), (offsets, torch.int32, (mw[0] + 1,)),
+                      (out, torch.bfloat16, (ma[0], mw[1])))):
+        _need(a, torch.int8, "a", (None, None))
+        ma = a.shape
+        _need(a_scale, torch.float32, "a_scale", ma[:1])
+        _need(w, torch.int8, "w", (None, None, ma[1]))
+        mw = w.shape
+        _need(w_scale, torch.float32, "w_scale", mw[:2])
+        if offsets is not None:
+            _need(offsets, torch.int32, "offsets", (mw[0] + 1,))
+        elif mw[0] != 1:
+            raise ValueError(f"w holds {mw[0]} matrices: offsets is required")
+        if out is not None:
+            _need(out, torch.bfloat16, "out", (ma[0], mw[1]))
+        _placed(a.device, a=a, a_scale=a_scale, w=w, w_scale=w_scale, offsets=offsets, out=out)
+    (M, K), (E_local, N, _) = ma, mw
     dev = a.device
-    _placed(dev, a=a, a_scale=a_scale, w=w, w_scale=w_scale, offsets=offsets)
-    out = _out(out, (M, N), torch.bfloat16, dev, "out")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     st = lib().moe_gemm_i8(_ptr(a), _ptr(a_scale), _ptr(offsets), _ptr(w), _ptr(w_scale), M, N, K, E_local, _ptr(out),
                            _stream(None, dev))
     check(st, "moe_gemm_i8")
@@ -697,16 +761,24 @@ def moe_expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, *, 
     quantised per row: expert outputs [cap, H] bf16 for the segments in
     ``offsets``. Returns (out, workspace). Takes ``stream``."""
     torch = _torch()
-    _need(x_perm, torch.bfloat16, "x_perm", (None, None))
-    cap, H = x_perm.shape
-    E_local, I = _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down)
-    _need(offsets, torch.int32, "offsets", (E_local + 1,))
-    if out is not None:
-        _need(out, torch.bfloat16, "out", (cap, H))
+    mx, mg = _dims(x_perm, 2), _dims(w_gate_up, 3)
+    if not (mx and mg and mg[2] == mx[1] and mg[1] % 2 == 0
+            and _fits((x_perm, torch.bfloat16, mx), (offsets, torch.int32, (mg[0] + 1,)), (w_gate_up, torch.int8, mg),
+                      (s_gate_up, torch.float32, mg[:2]), (w_down, torch.int8, (mg[0], mx[1], mg[1] // 2)),
+                      (s_down, torch.float32, (mg[0], mx[1])), (out, torch.bfloat16, mx))):
+        _need(x_perm, torch.bfloat16, "x_perm", (None, None))
+        mx = x_perm.shape
+        _need_ffn_i8(mx[1], w_gate_up, s_gate_up, w_down, s_down)
+        mg = w_gate_up.shape
+        _need(offsets, torch.int32, "offsets", (mg[0] + 1,))
+        if out is not None:
+            _need(out, torch.bfloat16, "out", mx)
+        _placed(x_perm.device, x_perm=x_perm, offsets=offsets, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
+                s_down=s_down, out=out)
+    (cap, H), E_local, I = mx, mg[0], mg[1] // 2
     dev = x_perm.device
-    _placed(dev, x_perm=x_perm, offsets=offsets, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
-            s_down=s_down)
-    out = _out(out, (cap, H), torch.bfloat16, dev, "out")
+    if out is None:
+        out = torch.empty_like(x_perm)
     L = lib()
     ws = _workspace(L.moe_expert_ffn_i8_workspace_size(H, I, cap), dev, workspace)
     st = L.moe_expert_ffn_i8(_ptr(x_perm), _ptr(offsets), _ptr(w_gate_up), _ptr(s_gate_up), _ptr(w_down), _ptr(s_down),
