@@ -384,15 +384,15 @@ constexpr int kMidFM = 4;
 typedef Shape<2, 2, 2, 2, 4> Small;
 constexpr int kSmallFM = 2;
 
-// Few rows, 16 or 32 of them x 64 channels, where only the weight stream counts:
+// Few rows, where only the weight stream counts: 16 or 32 rows x 64 channels,
 // two groups of k and two workgroups per CU, so that one streams while the
-// other starts or ends a tile (Stream); with few tiles, narrow ones with eight
-// groups (Narrow), or four for gate/up.
+// other starts or ends a tile (Stream; 64 rows: Stream64); with few tiles, 16
+// rows x 32 channels with eight groups (Narrow), or x 64 with four for gate/up.
 typedef Shape<1, 2, 2, 3, 2> Stream;
 typedef Shape<1, 2, 2, 2, 2> Stream64;  // 64 rows
 constexpr int kStreamLocal = 256;  // local experts (two workgroups fill the LDS)
-typedef Shape<1, 2, 1, 2, 8> Narrow;
-typedef Shape<1, 2, 2, 2, 4> NarrowGU;
+typedef Shape<1, 2, 1, 3, 8> Narrow;
+typedef Shape<1, 2, 2, 3, 4> NarrowGU;
 
 // Row caps of the largest tile (the fewest rounds of the grid win, weighted by
 // the tallest block, as in the bf16 grouped GEMM); the others have one.
@@ -416,6 +416,29 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
   constexpr int kCols = SWIGLU ? T::BN / 2 : T::BN;
   const int ntn = (p.N + kCols - 1) / kCols;
   constexpr int kPerT = (MAXE + kThreads - 1) / kThreads;
+  int row_cap = kBM, total = 0;
+  int only0 = 0, only_rows = 0;  // the one segment of a launch without tables
+  const bool tables = p.E_local > 1;
+  if (!tables) {
+    int end;
+    segment(p, 0, only0, end);
+    only_rows = end - only0;
+    if constexpr (kVary) {
+      unsigned long long best = ~0ull;
+#pragma unroll
+      for (int c = 0; c < kRowCaps; ++c) {
+        const int nrt = max(1, (only_rows + kRowCap[c] - 1) / kRowCap[c]);
+        const unsigned long long tl = (unsigned long long)nrt * (unsigned long long)ntn;
+        const int hm = (((only_rows + nrt - 1) / nrt) + 15) & ~15;
+        const unsigned long long est = (tl + gridDim.x - 1) / gridDim.x * (unsigned long long)(hm + T::BN);
+        if (tl < (1ull << 31) && est < best) {
+          best = est;
+          row_cap = kRowCap[c];
+        }
+      }
+    }
+    total = (only_rows + row_cap - 1) / row_cap * ntn;
+  } else {
   int me[kPerT];
 #pragma unroll
   for (int q = 0; q < kPerT; ++q) {
@@ -429,7 +452,6 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
       if (i == p.E_local - 1) s_off[p.E_local] = b;
     }
   }
-  int row_cap = kBM;
   if constexpr (kVary) {
     if (threadIdx.x < kRowCaps) {
       s_ntile[threadIdx.x] = 0;
@@ -472,7 +494,6 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
     mt[q] = (me[q] + row_cap - 1) / row_cap * ntn;
     sum += mt[q];
   }
-  int total;
   int pre = block_exclusive_scan<kThreads>(sum, s_tmp, total);
 #pragma unroll
   for (int q = 0; q < kPerT; ++q) {
@@ -481,6 +502,7 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
     pre += mt[q];
   }
   __syncthreads();
+  }
 
   // each XCD takes a contiguous range of the tiles (workgroup b runs on XCD
   // b % 8); inside an expert, groups of 8 row blocks walk the channel tiles
@@ -489,19 +511,23 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
   const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
   const int lo_t = int((int64_t(total) * xcd) / 8), hi_t = int((int64_t(total) * (xcd + 1)) / 8);
   for (int tile = lo_t + int(blockIdx.x / 8); tile < hi_t; tile += per_xcd) {
-    int lo = 0, hi = p.E_local - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_tpre[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid - 1;
+    int e = 0, seg0 = only0, m_e = only_rows, first = 0;
+    if (tables) {
+      int lo = 0, hi = p.E_local - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_tpre[mid] <= tile)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      e = __builtin_amdgcn_readfirstlane(lo);
+      seg0 = __builtin_amdgcn_readfirstlane(s_off[e]);
+      m_e = __builtin_amdgcn_readfirstlane(s_off[e + 1]) - seg0;
+      first = __builtin_amdgcn_readfirstlane(s_tpre[e]);
     }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int seg0 = __builtin_amdgcn_readfirstlane(s_off[e]);
-    const int m_e = __builtin_amdgcn_readfirstlane(s_off[e + 1]) - seg0;
     const int nrt = (m_e + row_cap - 1) / row_cap;
-    const int local = tile - __builtin_amdgcn_readfirstlane(s_tpre[e]);
+    const int local = tile - first;
     const int grp = local / (kGroup * ntn);
     const int in_grp = min(kGroup, nrt - grp * kGroup);
     const int rest = local - grp * kGroup * ntn;
@@ -558,19 +584,22 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   // Ragged segments spread around the expected length: twice as many rows as
   // expected still make one block.
   const int64_t rows = p.offsets ? 2 * rows_hint : rows_hint;
+  // Streams from the first tile beyond one per CU: a second round of narrow
+  // tiles costs more (16 experts of 2880 x 768, 61 rows: 34.4 us narrow, 31.2 us).
+  const bool streams = p.E_local <= kStreamLocal;
+  if (rows <= 16 && streams && tiles(16, 64 / d) > cus)
+    return go(Stream{}, std::integral_constant<int, 1>{}, StreamE{}, 16, 2);
+  if (rows <= 32 && streams && tiles(32, 64 / d) > cus)
+    return go(Stream{}, std::integral_constant<int, 2>{}, StreamE{}, 32, 2);
   if (rows <= 32) {
-    auto few = [&](auto fm_t) {
-      constexpr int FM = decltype(fm_t)::value;
-      if (tiles(16 * FM, 64 / d) >= 2 * cus && p.E_local <= kStreamLocal)
-        return go(Stream{}, fm_t, StreamE{}, 16 * FM, 2);
-      if constexpr (SWIGLU)
-        return go(NarrowGU{}, fm_t, AnyE{}, 16 * FM, 1);
-      else
-        return go(Narrow{}, fm_t, AnyE{}, 16 * FM, 1);
-    };
-    return rows <= 16 ? few(std::integral_constant<int, 1>{}) : few(std::integral_constant<int, 2>{});
+    // blocks of 16 rows also for 17 to 32: twice the tiles, and both blocks of a
+    // weight tile read it at the same time (32 x 7168 x 4096: 10.7 -> 8.6 us)
+    if constexpr (SWIGLU)
+      return go(NarrowGU{}, std::integral_constant<int, 1>{}, AnyE{}, 16, 1);
+    else
+      return go(Narrow{}, std::integral_constant<int, 1>{}, AnyE{}, 16, 1);
   }
-  if (rows <= 64 && tiles(64, 64 / d) >= 2 * cus && p.E_local <= kStreamLocal)
+  if (rows <= 64 && streams && tiles(64, 64 / d) > cus)
     return go(Stream64{}, std::integral_constant<int, 4>{}, StreamE{}, 64, 2);
   if (tiles(256, 256 / d) >= cus)
     return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
