@@ -267,6 +267,13 @@ __device__ __forceinline__ void pick(const Args& a, Tables& s, int t) {
   }
 }
 
+// The local slots of a return item's tokens.
+struct Returns {
+  int n[kTokens];
+  int16_t row[kTokens][32];
+  float wt[kTokens][32];
+};
+
 // ---------------------------------------------------------------------------
 // Items
 // ---------------------------------------------------------------------------
@@ -436,6 +443,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   __shared__ Tables s;
   __shared__ __attribute__((aligned(16))) float s_sum[kWaves * 16 * kStride];
   __shared__ int s_tmp[kWaves];
+  __shared__ Returns s_ret;
   __shared__ int2 s_item, s_aside;
   __shared__ int s_last, s_ok;
   const int tid = threadIdx.x;
@@ -524,6 +532,14 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       ask();
     }
   };
+  // Once the asked counter's value is there anyway: a queue found empty is left
+  // for the next kind's, whose answer then comes while the sums are exchanged.
+  auto settle = [&] {
+    if (tid < 64 && my_kind < 2 && __builtin_amdgcn_readfirstlane(asked) >= left_of(my_kind, my_queue)) {
+      ++my_kind;
+      ask();
+    }
+  };
   // An item of a kind before `kind` from any queue (kind 3: none is left), by
   // wave 0; lane q < 8 looks at queue q.
   auto rescue = [&](int kind) -> int2 {
@@ -554,47 +570,37 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   // y of one down panel for kTokens tokens, from their rows' partial sums:
   // slot by slot, k range by k range, kBatch loads at a time
   auto combine = [&](int panel, int t0) {
-    const int t = t0 + (tid >> 5), col = kCols * panel + 4 * (tid & 31);
+    const int lt = tid >> 5, t = t0 + lt, col = kCols * panel + 4 * (tid & 31);
     if (t >= a.T || col >= a.H) return;
     float o[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-    // the terms in order: (slot, range) pairs of the local slots
-    int j = 0, r = 0;
-    while (j < a.k && s.sel[t * a.k + j] < 0) ++j;
-    while (j < a.k) {
-      float2 q[kBatch][2];
-      int jj[kBatch];
-      bool end[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        jj[i] = -1;
-        end[i] = false;
-        if (j < a.k) {
-          const float* p = a.part_b + (int64_t(s.sel[t * a.k + j]) * sb.ranges + r) * a.H + col;
-          q[i][0] = get2(p);
-          q[i][1] = get2(p + 2);
-          jj[i] = j;
-          if (++r == sb.ranges) {
-            end[i] = true;
-            r = 0;
-            do ++j;
-            while (j < a.k && s.sel[t * a.k + j] < 0);
-          }
-        }
-      }
+    const int terms = s_ret.n[lt] * sb.ranges;
+    int slot = 0, r = 0;  // of the next term to be added
+    for (int i0 = 0; i0 < terms; i0 += kBatch) {
+      float2 q[kBatch][2] = {};
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (jj[i] >= 0) {
+        if (i0 + i < terms) {
+          const int sl = (i0 + i) / sb.ranges;
+          const float* p = a.part_b + (int64_t(s_ret.row[lt][sl]) * sb.ranges + (i0 + i - sl * sb.ranges)) * a.H + col;
+          q[i][0] = get2(p);
+          q[i][1] = get2(p + 2);
+        }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i0 + i < terms) {
           v[0] += q[i][0].x;
           v[1] += q[i][0].y;
           v[2] += q[i][1].x;
           v[3] += q[i][1].y;
-          if (end[i]) {
-            const float wt = s.wt[t * a.k + jj[i]];
+          if (++r == sb.ranges) {
+            const float wt = s_ret.wt[lt][slot];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               o[c] = fmaf(wt, v[c], o[c]);
               v[c] = 0.f;
             }
+            ++slot;
+            r = 0;
           }
         }
     }
@@ -650,7 +656,22 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       if (!rescued) ask();
     };
     if (kind == 2) {
-      const int panel = item % panels_b;
+      const int panel = item % panels_b, t0 = item / panels_b * kTokens;
+      // the tokens' local slots one after another, while the sums are waited for
+      if (tid >= 64 && tid < 64 + kTokens) {
+        const int lt = tid - 64, t = t0 + lt;
+        int n = 0;
+        if (t < a.T)
+          for (int j = 0; j < a.k; ++j) {
+            const int row = s.sel[t * a.k + j];
+            if (row >= 0) {
+              s_ret.row[lt][n] = int16_t(row);
+              s_ret.wt[lt][n] = s.wt[t * a.k + j];
+              ++n;
+            }
+          }
+        s_ret.n[lt] = n;
+      }
       if (tid == 0) s_ok = poll(a.cnt_b + panel * kPitch, n_act * sb.ranges);
       if (tid == 0 && s_ok) ask_next();
       __syncthreads();
@@ -658,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         put_aside();
         continue;
       }
-      combine(panel, item / panels_b * kTokens);
+      combine(panel, t0);
       advance();
       __syncthreads();
       continue;
@@ -688,17 +709,21 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       if (!TWO || rows <= 16) {
         f32x4v acc[1][8];
         stream<false, 1, 4>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
+        if (!rescued) settle();
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
         stream<false, 2, 2>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
+        if (!rescued) settle();
         gather_sums(s_sum, acc[0], 16, put(0));
         gather_sums(s_sum, acc[1], rows - 16, put(1));
       }
       stores_done();
       __syncthreads();
-      if (tid == 0) s_last = raise(a.cnt_a + (int64_t(ai) * blocks + block) * kPitch, 1) == 2 * sa.ranges - 1;
+      int before = 0;  // (its answer and the next item's arrive together)
+      if (tid == 0) before = raise(a.cnt_a + (int64_t(ai) * blocks + block) * kPitch, 1);
       advance();
+      if (tid == 0) s_last = before == 2 * sa.ranges - 1;
       __syncthreads();
       if (s_last) {
         // h of the block's 128 outputs, up to 8 rows at a time: 32 threads of 4
@@ -784,6 +809,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           put_aside();
           continue;
         }
+        if (!rescued) settle();
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
@@ -791,6 +817,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           put_aside();
           continue;
         }
+        if (!rescued) settle();
         gather_sums(s_sum, acc[0], 16, put(0));
         gather_sums(s_sum, acc[1], rows - 16, put(1));
       }
