@@ -35,6 +35,11 @@
 // still hold of the kinds before it, gate/up items first, so all items that
 // anybody waits for are with workgroups that are running.
 //
+// Bound: HBM from some eight tokens on (DeepSeek-R1-shaped EP=8 share, 16
+// tokens, 1.13 GB of used experts: 198 us, the stream itself at 6 TB/s and
+// more); below that the chain of exchanges (TP=8 share, one token, 95 MB: 38 us
+// of which the weights take 14).
+//
 // Sums are added in a fixed order by whichever workgroup is last, so y does
 // not depend on the order of the items. h stays float32: it is multiplied as
 // three bf16 parts that add up to it (exact products), so y is rounded once.
