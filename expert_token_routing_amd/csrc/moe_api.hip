@@ -397,6 +397,13 @@ static int check_i8(int K, int64_t channels) {
   return MOE_OK;
 }
 
+// Rows and tiles of a grouped product are counted with 31 bits: at the smallest
+// blocks (16 rows) and narrowest tiles (32 channels).
+static bool i8_rows_fit(int64_t capacity, int E_local, int64_t channels) {
+  return capacity < (int64_t(1) << 31) - 1024 &&
+         (ceil_div(capacity, 16) + E_local) * ceil_div(channels, 32) < (int64_t(1) << 31);
+}
+
 int moe_quantize_rows(const moe_bf16* x, int64_t M, int K, int8_t* q, float* scale, hipStream_t stream) {
   if (M < 0 || K <= 0 || (K % 16) != 0) return MOE_ERR_INVALID_ARG;
   if (M >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
@@ -419,7 +426,7 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, c
   if (E_local < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
   const int st = check_i8(K, N);
   if (st != MOE_OK) return st;
-  if (E_local > kMaxE || capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (E_local > kMaxE || !i8_rows_fit(capacity, E_local, N)) return MOE_ERR_UNSUPPORTED;
   if (!offsets && E_local != 1) return MOE_ERR_INVALID_ARG;
   if (capacity == 0) return MOE_OK;
   if (!a || !a_scale || !w || !w_scale || !out) return MOE_ERR_INVALID_ARG;
@@ -521,7 +528,7 @@ int moe_expert_ffn_i8(const moe_bf16* x_perm, const int32_t* offsets, const int8
   if (E_local < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
   const int st = check_ffn_i8(H, I);
   if (st != MOE_OK) return st;
-  if (E_local > kMaxE || capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (E_local > kMaxE || !i8_rows_fit(capacity, E_local, std::max(H, I))) return MOE_ERR_UNSUPPORTED;
   if (capacity == 0) return MOE_OK;
   if (!x_perm || !offsets || !w_gate_up || !s_gate_up || !w_down || !s_down || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(w_gate_up) || !aligned16(s_gate_up) || !aligned16(w_down) ||
@@ -547,7 +554,7 @@ int moe_forward_i8(const moe_bf16* x, const float* w_router, const float* bias, 
   if (st != MOE_OK) return st;
   if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
   if ((st = check_ffn_i8(H, I)) != MOE_OK) return st;
-  if (min_capacity(T, k, E_local) >= (int64_t(1) << 31) || int64_t(T) * H >= (int64_t(1) << 31))
+  if (!i8_rows_fit(min_capacity(T, k, E_local), E_local, std::max(H, I)) || int64_t(T) * H >= (int64_t(1) << 31))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !w_gate_up || !s_gate_up || !w_down || !s_down || !y) return MOE_ERR_INVALID_ARG;

@@ -376,7 +376,9 @@ int moe_quantize_weights(const moe_bf16* w, int E_local, int K, int N, int8_t* q
  *   w       [E_local, N, K] int8, w_scale [E_local, N] f32
  *   out     [capacity, N] bf16 OUT; rows >= offsets[E_local] untouched
  * K is a multiple of 16 and below 131072, N a multiple of 8, N * K < 2^31,
- * E_local <= 1024, capacity < 2^31; a, w, w_scale and out are 16-byte aligned.
+ * E_local <= 1024, capacity < 2^31 - 1024 and (capacity / 16 + E_local) * N / 32
+ * < 2^31 (rounded up), else MOE_ERR_UNSUPPORTED; a, w, w_scale and out are
+ * 16-byte aligned.
  */
 int moe_gemm_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, const int8_t* w, const float* w_scale,
                 int64_t capacity, int N, int K, int E_local, moe_bf16* out, hipStream_t stream);
@@ -391,7 +393,8 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, c
  *   w_gate_up [E_local, 2I, H] int8 (channels [0, I) gate, [I, 2I) up),
  *   s_gate_up [E_local, 2I] f32, w_down [E_local, H, I] int8, s_down
  *   [E_local, H] f32: what moe_quantize_weights makes of moe_expert_ffn's.
- * H and I are multiples of 16 below 131072, H * 2I < 2^31. workspace:
+ * H and I are multiples of 16 below 131072, H * 2I < 2^31, and capacity is
+ * bounded as in moe_gemm_i8 (with the larger of H and I as N). workspace:
  * moe_expert_ffn_i8_workspace_size bytes, 256-byte aligned. Other arguments
  * and checks as for moe_expert_ffn.
  */

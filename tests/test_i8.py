@@ -49,7 +49,8 @@ def test_quantize_weights_rejects(args, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(E=0), INV), (dict(cap=-1), INV), (dict(K=8), INV), (dict(N=12), INV), (dict(N=0), INV), (dict(K=131072), UNS),
-    (dict(K=65536, N=32768), UNS), (dict(E=1025), UNS), (dict(cap=1 << 31), UNS), (dict(E=2, off=None), INV),
+    (dict(K=65536, N=32768), UNS), (dict(E=1025), UNS), (dict(cap=1 << 31), UNS), (dict(cap=(1 << 31) - 1024), UNS), (dict(cap=1 << 30, N=1024), UNS),
+    (dict(E=2, off=None), INV),
     (dict(a=None), INV), (dict(s=None), INV), (dict(w=None), INV), (dict(ws=None), INV), (dict(out=None), INV),
     (dict(a=ODD), INV), (dict(w=ODD), INV), (dict(ws=ODD), INV), (dict(out=ODD), INV), (dict(cap=0, a=None), OK),
 ])
