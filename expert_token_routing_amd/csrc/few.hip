@@ -871,11 +871,12 @@ inline Layout layout(int T, int H, int I, int E, int k, int E_local) {
 
 }  // namespace few
 
-bool few_supported(int T, int I, int k, int E_local) {
+bool few_supported(int T, int H, int I, int k, int E_local) {
   // the counters are indexed with 31 bits (32 of them per 128 columns of each
-  // expert in use), an expert's rows of h with 32 (in bytes, at most T of them)
+  // expert in use); x and an expert's rows of h (float32, at most T of them) end
+  // below the offset that stands for "outside"
   return int64_t(std::min<int64_t>(E_local, int64_t(T) * k)) * I < (int64_t(1) << 32) &&
-         int64_t(T) * I < (int64_t(1) << 29);
+         int64_t(T) * I < (int64_t(1) << 29) && int64_t(T) * H < (int64_t(1) << 30);
 }
 
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {

@@ -362,7 +362,7 @@ static int few_impl(const moe_bf16* x, const float* w_router, const float* bias,
   if (st != MOE_OK) return st;
   if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
   if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
-  if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I) || !few_supported(T, I, k, E_local))
+  if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I) || !few_supported(T, H, I, k, E_local))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
@@ -633,7 +633,7 @@ int moe_norm_post(const void* y, int y_type, const void* residual, int r_type, c
 // two-kernel layer is the faster one at every shape measured (DeepSeek-R1 EP=8
 // share 34 us against 134 at one token, 204 against 257 at 16); at 24 to 32 the
 // two are within 10% of each other either way.
-static bool block_is_few(int T, int I, int E, int k) { return T <= 16 && few_supported(T, I, k, E); }
+static bool block_is_few(int T, int H, int I, int E, int k) { return T <= 16 && few_supported(T, H, I, k, E); }
 struct BlockLayout {
   size_t x, y, layer, total;
 };
@@ -641,7 +641,7 @@ static BlockLayout block_layout(int T, int H, int I, int E, int k) {
   BlockLayout L{};
   L.y = align_up(size_t(T) * H * sizeof(uint16_t));
   L.layer = L.y + align_up(size_t(T) * H * sizeof(float));
-  L.total = L.layer + (block_is_few(T, I, E, k) ? few_workspace_bytes(T, H, I, E, k, E)
+  L.total = L.layer + (block_is_few(T, H, I, E, k) ? few_workspace_bytes(T, H, I, E, k, E)
                                                 : forward_layout(T, H, I, E, k, E).total);
   return L;
 }
@@ -678,7 +678,7 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
   float* y = reinterpret_cast<float*>(ws + L.y);
   st = moe_norm_pre(residual, r_type, w_pre, eps, T, H, x, stream);
   if (st == MOE_OK)
-    st = block_is_few(T, I, E, k)
+    st = block_is_few(T, H, I, E, k)
              ? moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, 0, E, renormalize, y,
                                    ws + L.layer, workspace_bytes - L.layer, stream)
              : moe_forward_f32(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, 0, E, renormalize, y,

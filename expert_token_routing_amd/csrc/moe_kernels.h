@@ -107,7 +107,7 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
                              int H, void* out, uint16_t* normed, hipStream_t stream);
 
 // The whole share for T <= 32 tokens in two kernels (few.hip).
-bool few_supported(int T, int I, int k, int E_local);
+bool few_supported(int T, int H, int I, int k, int E_local);
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local);
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,

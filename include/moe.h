@@ -324,8 +324,8 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
  * moe_forward for at most MOE_FEW_TOKENS tokens, where reading the used
  * experts' weights is the whole cost: one kernel for the router's logits, one
  * for selection, expert MLPs and the weighted return. Arguments and checks are
- * moe_forward's; T > MOE_FEW_TOKENS, T * I >= 2^29 or min(E_local, T k) * I >=
- * 2^32 is MOE_ERR_UNSUPPORTED. workspace:
+ * moe_forward's; T > MOE_FEW_TOKENS, T * H >= 2^30, T * I >= 2^29 or
+ * min(E_local, T k) * I >= 2^32 is MOE_ERR_UNSUPPORTED. workspace:
  * moe_few_workspace_size bytes, 256-byte aligned; no part of it needs to start
  * at zero. Calls that overlap need workspaces of their own.
  *   - the logits are float32 sums as in moe_route, added in another order, so

@@ -31,7 +31,8 @@ INV, UNS, WSP = M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED, M.MOE_ERR_WORKSPAC
 @pytest.mark.parametrize("kw,want", [
     (dict(T=33), UNS), (dict(T=-1), INV), (dict(H=12), INV), (dict(I=12), INV), (dict(I=0), INV), (dict(k=0), INV),
     (dict(k=5), INV), (dict(E=2000), UNS), (dict(E=64, k=33), UNS), (dict(e0=1), INV), (dict(El=0), INV),
-    (dict(H=16384, I=32768), UNS), (dict(I=1 << 25, T=16), UNS), (dict(x=None), INV), (dict(w=None), INV), (dict(gu=None), INV), (dict(d=None), INV),
+    (dict(H=16384, I=32768), UNS), (dict(I=1 << 25, T=16), UNS),
+    (dict(H=1 << 25, T=32), UNS), (dict(x=None), INV), (dict(w=None), INV), (dict(gu=None), INV), (dict(d=None), INV),
     (dict(y=None), INV), (dict(x=ODD), INV), (dict(gu=ODD), INV), (dict(d=ODD), INV), (dict(y=ODD), INV),
     (dict(ws=None), WSP), (dict(ws=ctypes.c_void_p(0x100010)), WSP), (dict(wsb=512), WSP),
     (dict(T=0, x=None, y=None, ws=None), M.MOE_OK),
