@@ -453,21 +453,24 @@ def _on_stream(fn):
     caller gave a ``stream``, with that stream current: what ``fn`` allocates
     then belongs to the stream its kernels run on, so the memory cannot be
     handed to them while another stream still uses it."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         torch = _torch()
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            return fn(first, *args, **kw)  # refused by fn's checks
+            return fn(*args, **kw)  # refused by fn's checks
         index = first.get_device()
         if stream is not None:
             if stream.device.index != index:
                 raise ValueError(f"stream is on {stream.device}, the call's tensors on {first.device}")
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if index != torch._C._cuda_getDevice():
             with torch.cuda.device(index):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
+                return fn(*args, **kw)
+        return fn(*args, **kw)
     return call
 
 

@@ -66,6 +66,26 @@ def test_norm_post_rejects(kw, want):
     assert got == want
 
 
+def test_every_argument_may_be_named():
+    """A call that names its first tensor too reaches its operator's checks."""
+    z, w, f = torch.zeros(4, 64, dtype=BF), torch.zeros(64), torch.zeros(8, 64)
+    gu, dn = torch.zeros(8, 64, 64, dtype=BF), torch.zeros(8, 32, 64, dtype=BF)
+    q, s4 = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    layer = dict(w_router=f, bias=None, k=2)
+    i8 = dict(w_gate_up=gu.to(torch.int8), s_gate_up=torch.zeros(8, 64), w_down=torch.zeros(8, 64, 32, dtype=torch.int8),
+              s_down=torch.zeros(8, 64))
+    for call in (lambda: M.moe_norm_pre(r=z, w=w), lambda: M.moe_norm_post(y=z, residual=z),
+                 lambda: M.moe_forward_few(x=z, w_gate_up=gu, w_down=dn, e0=0, **layer),
+                 lambda: M.moe_forward_few_f32(x=z, w_gate_up=gu, w_down=dn, e0=0, **layer),
+                 lambda: M.moe_quantize_rows(x=z), lambda: M.moe_quantize_weights(w=gu),
+                 lambda: M.moe_gemm_i8(a=q, a_scale=s4, w=q[None], w_scale=s4[None]),
+                 lambda: M.moe_expert_ffn_i8(x_perm=z, offsets=torch.zeros(9, dtype=torch.int32), **i8),
+                 lambda: M.moe_forward_i8(x=z, e0=0, **layer, **i8),
+                 lambda: M.moe_block_forward(residual=z, w_pre=w, w_gate_up=gu, w_down=dn, **layer)):
+        with pytest.raises(ValueError, match="must live on a GPU"):
+            call()
+
+
 def test_norms_reject_mismatched_tensors():
     y, w = torch.zeros(4, 64, dtype=BF), torch.zeros(64)
     for bad, exc, match in ((dict(r=y.double()), TypeError, "r must be"), (dict(w=w.double()), TypeError, "w must be"),
@@ -209,6 +229,17 @@ def test_norm_post_keeps_infinities_and_nans_in_their_row(T, H):
     assert torch.equal(o2[3], r[3]) and torch.isfinite(n2[3]).all()  # a row of zeros has the norm zero
     keep = [0, *range(4, T)]
     assert torch.equal(o2[keep], out[keep]) and torch.equal(n2[keep], normed[keep])
+
+
+@gpu
+def test_norm_arguments_by_name_on_a_stream():
+    x, w = torch.randn(5, 96, device="cuda"), torch.randn(96, device="cuda")
+    want = M.moe_norm_pre(x, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = M.moe_norm_pre(r=x, w=w, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(M.moe_norm_pre(w=w, r=x), want)
 
 
 @gpu
