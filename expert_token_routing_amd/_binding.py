@@ -512,6 +512,13 @@ def _fits(*specs):
     return True
 
 
+def _ints(*sizes):
+    """Sizes that the library takes as int: ctypes would pass on a larger one's
+    low 32 bits."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes are at most 2^31 - 1, got {max(sizes)}")
+
+
 def _dims(t, n):
     """The shape of an n-dimensional tensor, None for anything else."""
     shape = getattr(t, "shape", None)
@@ -553,6 +560,7 @@ def moe_norm_pre(r, w, eps=1e-6, *, out=None):
             _need(out, torch.bfloat16, "out", shape)
         _placed(r.device, r=r, w=w, out=out)
     T, H = shape
+    _ints(T, H)
     rt = TYPE_BF16 if r.dtype == torch.bfloat16 else TYPE_F32
     dev = r.device
     if out is None:
@@ -596,6 +604,7 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
             _need(normed, torch.bfloat16, "normed", shape)
         _placed(y.device, y=y, residual=residual, w_post=w_post, gate=gate, w_next=w_next, out=out, normed=normed)
     T, H = shape
+    _ints(T, H)
     kind = _gate_kind(gate, T, H)
     yt = TYPE_BF16 if y.dtype == torch.bfloat16 else TYPE_F32
     rt = TYPE_BF16 if residual.dtype == torch.bfloat16 else TYPE_F32
@@ -632,6 +641,7 @@ def _few(name, out_dtype, x, w_router, bias, w_gate_up, w_down, k, e0, renormali
             _need(y, out_dtype, "y", mx)
         _placed(x.device, x=x, w_router=w_router, bias=bias, w_gate_up=w_gate_up, w_down=w_down, y=y)
     (T, H), E, E_local, I = mx, mr[0], mg[0], mg[2] // 2
+    _ints(T, H, E, I)
     dev = x.device
     if y is None:
         y = torch.empty(mx, dtype=out_dtype, device=dev)
@@ -676,6 +686,7 @@ def moe_quantize_rows(x, *, q=None, scale=None):
             _need(scale, torch.float32, "scale", shape[:1])
         _placed(x.device, x=x, q=q, scale=scale)
     M, K = shape
+    _ints(M, K)
     dev = x.device
     if q is None:
         q = torch.empty(shape, dtype=torch.int8, device=dev)
@@ -693,6 +704,7 @@ def moe_quantize_weights(w, *, q=None, scale=None):
     torch = _torch()
     _need(w, torch.bfloat16, "w", (None, None, None))
     E_local, K, N = w.shape
+    _ints(E_local, K, N)
     if q is not None:
         _need(q, torch.int8, "q", (E_local, N, K))
     if scale is not None:
@@ -732,6 +744,7 @@ def moe_gemm_i8(a, a_scale, w, w_scale, offsets=None, *, out=None):
             _need(out, torch.bfloat16, "out", (ma[0], mw[1]))
         _placed(a.device, a=a, a_scale=a_scale, w=w, w_scale=w_scale, offsets=offsets, out=out)
     (M, K), (E_local, N, _) = ma, mw
+    _ints(M, K, E_local, N)
     dev = a.device
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
@@ -779,6 +792,7 @@ def moe_expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, *, 
         _placed(x_perm.device, x_perm=x_perm, offsets=offsets, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
                 s_down=s_down, out=out)
     (cap, H), E_local, I = mx, mg[0], mg[1] // 2
+    _ints(cap, H, E_local, I)
     dev = x_perm.device
     if out is None:
         out = torch.empty_like(x_perm)
@@ -807,6 +821,7 @@ def moe_forward_i8(x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, k, e
     if bias is not None:
         _need(bias, torch.float32, "bias", (E,))
     E_local, I = _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down)
+    _ints(T, H, E, E_local, I)
     _check_k(k, E)
     if not (0 <= e0 and e0 + E_local <= E):
         raise ValueError(f"local experts [e0, e0 + E_local) = [{e0}, {e0 + E_local}) must lie in [0, E = {E})")
@@ -839,6 +854,7 @@ def moe_block_forward(residual, w_pre, w_router, bias, w_gate_up, w_down, k, w_p
     torch = _torch()
     rt = _need_either(residual, "residual", (None, None))
     T, H = residual.shape
+    _ints(T, H)
     _need(w_pre, torch.float32, "w_pre", (H,))
     _need(w_router, torch.float32, "w_router", (None, H))
     E = w_router.shape[0]
@@ -849,6 +865,7 @@ def moe_block_forward(residual, w_pre, w_router, bias, w_gate_up, w_down, k, w_p
     if I2 % 2:
         raise ValueError(f"w_gate_up's last dimension 2I must be even, got {I2}")
     I = I2 // 2
+    _ints(E, I)
     _need(w_down, torch.bfloat16, "w_down", (E, I, H))
     _check_k(k, E)
     if w_post is not None:

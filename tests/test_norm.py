@@ -112,6 +112,32 @@ def test_norms_reject_mismatched_tensors():
             M.moe_norm_post(a.pop("y"), a.pop("residual"), **a)
 
 
+def test_sizes_past_31_bits_are_refused(monkeypatch):
+    """Before they reach an int argument, which would take their low 32 bits
+    (meta tensors: shapes without memory, let past the device check)."""
+    big, small = 2 ** 32 + 16, 16
+
+    def t(*shape, dtype=BF):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    I8 = torch.int8
+    monkeypatch.setattr(M._binding, "_fits", lambda *specs: True)
+    for call in (lambda: M.moe_norm_pre(t(big, 8), t(8, dtype=F32)), lambda: M.moe_norm_pre(t(1, big), t(big, dtype=F32)),
+                 lambda: M.moe_norm_post(t(big, 8), t(big, 8)),
+                 lambda: M.moe_forward_few(t(big, 8), t(4, 8, dtype=F32), None, t(4, 8, 16), t(4, 8, 8), 1, 0),
+                 lambda: M.moe_forward_few_f32(t(1, 8), t(big, 8, dtype=F32), None, t(4, 8, 16), t(4, 8, 8), 1, 0),
+                 lambda: M.moe_quantize_rows(t(1, big)), lambda: M.moe_quantize_weights(t(1, big, 8)),
+                 lambda: M.moe_quantize_weights(t(1, 16, big)), lambda: M.moe_quantize_weights(t(big, 16, 8)),
+                 lambda: M.moe_gemm_i8(t(1, small, dtype=I8), t(1, dtype=F32), t(1, big, small, dtype=I8), t(1, big, dtype=F32)),
+                 lambda: M.moe_expert_ffn_i8(t(big, small), t(2, dtype=torch.int32), t(1, 32, small, dtype=I8),
+                                             t(1, 32, dtype=F32), t(1, small, small, dtype=I8), t(1, small, dtype=F32)),
+                 lambda: M.moe_forward_i8(t(big, small), t(4, small, dtype=F32), None, t(1, 32, small, dtype=I8),
+                                          t(1, 32, dtype=F32), t(1, small, small, dtype=I8), t(1, small, dtype=F32), 1, 0),
+                 lambda: M.moe_block_forward(t(big, 8), t(8, dtype=F32), t(4, 8, dtype=F32), None, t(4, 8, 16), t(4, 8, 8),
+                                             1)):
+        with pytest.raises(ValueError, match="at most 2.31 - 1, got 42949"):
+            call()
+
+
 # --------------------------------------------------------------------------- #
 # The kernels (GPU)                                                            #
 # --------------------------------------------------------------------------- #
