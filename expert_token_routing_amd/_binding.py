@@ -1,4 +1,5 @@
-"""ctypes binding of ``libmoe.so`` (the C-ABI declared in include/moe.h).
+"""ctypes binding of ``libmoe.so`` (the C-ABI declared in include/moe.h); the
+small calls go through the extension module ``_calls.so`` (csrc/calls.cpp).
 
 Argument marshalling only: every step of the MoE share runs in the library's
 HIP kernels. PyTorch provides device memory and the current stream. There is
@@ -6,6 +7,7 @@ no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import numbers
@@ -94,6 +96,27 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = h
     return _lib
+
+
+_calls_module = None
+
+
+def _calls():
+    """The extension module behind the small calls (csrc/calls.cpp), which
+    calls the library loaded here."""
+    global _calls_module
+    if _calls_module is None:
+        L = lib()
+        _torch()  # its libraries first
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or was built for another torch: build it with "
+                               "`python -m expert_token_routing_amd.build_lib`; there is no fallback path") from e
+        module.bind(*(ctypes.cast(getattr(L, n), c_void_p).value
+                      for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8")))
+        _calls_module = module
+    return _calls_module
 
 
 def status_string(status: int) -> str:
@@ -448,11 +471,22 @@ def moe_forward_noalloc(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize
     return y
 
 
+@contextlib.contextmanager
+def _current(first, stream):
+    """``first``'s device, and ``stream`` where the caller gave one, as the
+    current ones: what the call allocates then belongs to the stream its kernels
+    run on, so the memory cannot be handed to them while another stream still
+    uses it."""
+    torch = _torch()
+    if stream is not None and stream.device.index != first.get_device():
+        raise ValueError(f"stream is on {stream.device}, the call's tensors on {first.device}")
+    with torch.cuda.device(first.get_device()) if stream is None else torch.cuda.stream(stream):
+        yield
+
+
 def _on_stream(fn):
     """Runs ``fn`` with the device of its first tensor current and, where the
-    caller gave a ``stream``, with that stream current: what ``fn`` allocates
-    then belongs to the stream its kernels run on, so the memory cannot be
-    handed to them while another stream still uses it."""
+    caller gave a ``stream``, with that stream current."""
     name = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
@@ -461,17 +495,28 @@ def _on_stream(fn):
         first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             return fn(*args, **kw)  # refused by fn's checks
-        index = first.get_device()
-        if stream is not None:
-            if stream.device.index != index:
-                raise ValueError(f"stream is on {stream.device}, the call's tensors on {first.device}")
-            with torch.cuda.stream(stream):
-                return fn(*args, **kw)
-        if index != torch._C._cuda_getDevice():
-            with torch.cuda.device(index):
+        if stream is not None or first.get_device() != torch._C._cuda_getDevice():
+            with _current(first, stream):
                 return fn(*args, **kw)
         return fn(*args, **kw)
     return call
+
+
+def _small_call(name, args, stream, refuse):
+    """The call ``name`` of the extension module. Where it does not take the
+    arguments as they are, ``refuse`` says what is wrong with them, or their
+    device or stream is made current first."""
+    fn = getattr(_calls(), name)
+    done = fn(*args) if stream is None else None
+    if done is None:
+        refuse()
+        with _current(args[0], stream):
+            done = fn(*args)
+        if done is None:
+            raise TypeError(f"moe_{name} does not take these tensors")
+    if done.__class__ is int:
+        check(done, "moe_" + name)
+    return done
 
 
 # --------------------------------------------------------------------------- #
@@ -545,33 +590,23 @@ def _gate_kind(gate, T, H):
     return kind
 
 
-@_on_stream
-def moe_norm_pre(r, w, eps=1e-6, *, out=None):
+def moe_norm_pre(r, w, eps=1e-6, *, out=None, stream=None):
     """The norm before the block: out [T, H] bf16 = r / sqrt(mean(r^2) + eps) * w.
-    ``r`` [T, H] is bf16 or float32, ``w`` [H] float32. Takes ``stream``."""
-    torch = _torch()
-    shape = _dims(r, 2)
-    if not (shape and r.dtype in (torch.bfloat16, torch.float32)
-            and _fits((r, r.dtype, shape), (w, torch.float32, shape[1:]), (out, torch.bfloat16, shape))):
+    ``r`` [T, H] is bf16 or float32, ``w`` [H] float32."""
+    def refuse():
+        torch = _torch()
         _need_either(r, "r", (None, None))
-        shape = r.shape
-        _need(w, torch.float32, "w", shape[1:])
+        T, H = r.shape
+        _need(w, torch.float32, "w", (H,))
         if out is not None:
-            _need(out, torch.bfloat16, "out", shape)
+            _need(out, torch.bfloat16, "out", (T, H))
+        _ints(T, H)
         _placed(r.device, r=r, w=w, out=out)
-    T, H = shape
-    _ints(T, H)
-    rt = TYPE_BF16 if r.dtype == torch.bfloat16 else TYPE_F32
-    dev = r.device
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    check(lib().moe_norm_pre(_ptr(r), rt, _ptr(w), eps, T, H, _ptr(out), _stream(None, dev)), "moe_norm_pre")
-    return out
+    return _small_call("norm_pre", (r, w, eps, out), stream, refuse)
 
 
-@_on_stream
 def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_next=None, eps=1e-6, out=None,
-                  normed=None):
+                  normed=None, stream=None):
     """out = residual_scale * residual + gate * norm(y; w_post), of the
     residual's type, and with ``w_next`` also normed [T, H] bf16 =
     norm(out before its rounding; w_next). Returns (out, normed or None).
@@ -579,44 +614,26 @@ def moe_norm_post(y, residual, w_post=None, *, gate=None, residual_scale=1.0, w_
     ``y`` and ``residual`` [T, H] are bf16 or float32; ``w_post`` and
     ``w_next`` [H] float32 (``w_post`` None: y as it is). ``gate`` float32 is
     [H] (per channel), [T, 1] (per token) or [T, H]. ``out`` may be
-    ``residual``. Takes ``stream``."""
-    torch = _torch()
-    shape, f32 = _dims(y, 2), torch.float32
-    types = (torch.bfloat16, f32)
-    if not (shape and y.dtype in types and getattr(residual, "dtype", None) in types
-            and (gate is None or isinstance(gate, torch.Tensor)) and (normed is None or w_next is not None)
-            and _fits((y, y.dtype, shape), (residual, residual.dtype, shape), (w_post, f32, shape[1:]),
-                      (w_next, f32, shape[1:]), (gate, f32, getattr(gate, "shape", None)),
-                      (out, residual.dtype, shape), (normed, torch.bfloat16, shape))):
+    ``residual``."""
+    def refuse():
+        torch = _torch()
         _need_either(y, "y", (None, None))
-        shape = y.shape
-        _need_either(residual, "residual", shape)
+        T, H = y.shape
+        _need_either(residual, "residual", (T, H))
         if w_post is not None:
-            _need(w_post, f32, "w_post", shape[1:])
-        _gate_kind(gate, *shape)
+            _need(w_post, torch.float32, "w_post", (H,))
+        _gate_kind(gate, T, H)
         if w_next is not None:
-            _need(w_next, f32, "w_next", shape[1:])
+            _need(w_next, torch.float32, "w_next", (H,))
         elif normed is not None:
             raise ValueError("normed is given without w_next")
         if out is not None:
-            _need(out, residual.dtype, "out", shape)
+            _need(out, residual.dtype, "out", (T, H))
         if normed is not None:
-            _need(normed, torch.bfloat16, "normed", shape)
+            _need(normed, torch.bfloat16, "normed", (T, H))
+        _ints(T, H)
         _placed(y.device, y=y, residual=residual, w_post=w_post, gate=gate, w_next=w_next, out=out, normed=normed)
-    T, H = shape
-    _ints(T, H)
-    kind = _gate_kind(gate, T, H)
-    yt = TYPE_BF16 if y.dtype == torch.bfloat16 else TYPE_F32
-    rt = TYPE_BF16 if residual.dtype == torch.bfloat16 else TYPE_F32
-    dev = y.device
-    if out is None:
-        out = torch.empty_like(residual)
-    if w_next is not None and normed is None:
-        normed = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    st = lib().moe_norm_post(_ptr(y), yt, _ptr(residual), rt, _ptr(w_post), _ptr(gate), kind, residual_scale,
-                             _ptr(w_next), eps, T, H, _ptr(out), _ptr(normed), _stream(None, dev))
-    check(st, "moe_norm_post")
-    return out, normed
+    return _small_call("norm_post", (y, residual, w_post, gate, residual_scale, w_next, eps, out, normed), stream, refuse)
 
 
 # --------------------------------------------------------------------------- #
@@ -671,29 +688,20 @@ def moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize
 # --------------------------------------------------------------------------- #
 # 8-bit integer products                                                       #
 # --------------------------------------------------------------------------- #
-@_on_stream
-def moe_quantize_rows(x, *, q=None, scale=None):
+def moe_quantize_rows(x, *, q=None, scale=None, stream=None):
     """q [M, K] int8 and scale [M] float32 of x [M, K] bf16: scale = max|x| / 127
-    per row, q = x / scale to the nearest integer. Takes ``stream``."""
-    torch = _torch()
-    shape = _dims(x, 2)
-    if not (shape and _fits((x, torch.bfloat16, shape), (q, torch.int8, shape), (scale, torch.float32, shape[:1]))):
+    per row, q = x / scale to the nearest integer."""
+    def refuse():
+        torch = _torch()
         _need(x, torch.bfloat16, "x", (None, None))
-        shape = x.shape
+        M, K = x.shape
         if q is not None:
-            _need(q, torch.int8, "q", shape)
+            _need(q, torch.int8, "q", (M, K))
         if scale is not None:
-            _need(scale, torch.float32, "scale", shape[:1])
+            _need(scale, torch.float32, "scale", (M,))
+        _ints(M, K)
         _placed(x.device, x=x, q=q, scale=scale)
-    M, K = shape
-    _ints(M, K)
-    dev = x.device
-    if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=dev)
-    if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
-    check(lib().moe_quantize_rows(_ptr(x), M, K, _ptr(q), _ptr(scale), _stream(None, dev)), "moe_quantize_rows")
-    return q, scale
+    return _small_call("quantize_rows", (x, q, scale), stream, refuse)
 
 
 @_on_stream
@@ -718,40 +726,28 @@ def moe_quantize_weights(w, *, q=None, scale=None):
     return q, scale
 
 
-@_on_stream
-def moe_gemm_i8(a, a_scale, w, w_scale, offsets=None, *, out=None):
+def moe_gemm_i8(a, a_scale, w, w_scale, offsets=None, *, out=None, stream=None):
     """out [M, N] bf16 = (a @ w[e].T) * a_scale[:, None] * w_scale[e] for the
     rows of segment e of ``offsets`` [E_local + 1] int32 (None: one weight
     matrix for all rows). a [M, K] and w [E_local, N, K] are int8, the scales
-    [M] and [E_local, N] float32. Takes ``stream``."""
-    torch = _torch()
-    ma, mw = _dims(a, 2), _dims(w, 3)
-    if not (ma and mw and mw[2] == ma[1] and (offsets is not None or mw[0] == 1)
-            and _fits((a, torch.int8, ma), (a_scale, torch.float32, ma[:1]), (w, torch.int8, mw),
-                      (w_scale, torch.float32, mw[:2]), (offsets, torch.int32, (mw[0] + 1,)),
-                      (out, torch.bfloat16, (ma[0], mw[1])))):
+    [M] and [E_local, N] float32."""
+    def refuse():
+        torch = _torch()
         _need(a, torch.int8, "a", (None, None))
-        ma = a.shape
-        _need(a_scale, torch.float32, "a_scale", ma[:1])
-        _need(w, torch.int8, "w", (None, None, ma[1]))
-        mw = w.shape
-        _need(w_scale, torch.float32, "w_scale", mw[:2])
+        M, K = a.shape
+        _need(a_scale, torch.float32, "a_scale", (M,))
+        _need(w, torch.int8, "w", (None, None, K))
+        E_local, N, _ = w.shape
+        _need(w_scale, torch.float32, "w_scale", (E_local, N))
         if offsets is not None:
-            _need(offsets, torch.int32, "offsets", (mw[0] + 1,))
-        elif mw[0] != 1:
-            raise ValueError(f"w holds {mw[0]} matrices: offsets is required")
+            _need(offsets, torch.int32, "offsets", (E_local + 1,))
+        elif E_local != 1:
+            raise ValueError(f"w holds {E_local} matrices: offsets is required")
         if out is not None:
-            _need(out, torch.bfloat16, "out", (ma[0], mw[1]))
+            _need(out, torch.bfloat16, "out", (M, N))
+        _ints(M, K, E_local, N)
         _placed(a.device, a=a, a_scale=a_scale, w=w, w_scale=w_scale, offsets=offsets, out=out)
-    (M, K), (E_local, N, _) = ma, mw
-    _ints(M, K, E_local, N)
-    dev = a.device
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    st = lib().moe_gemm_i8(_ptr(a), _ptr(a_scale), _ptr(offsets), _ptr(w), _ptr(w_scale), M, N, K, E_local, _ptr(out),
-                           _stream(None, dev))
-    check(st, "moe_gemm_i8")
-    return out
+    return _small_call("gemm_i8", (a, a_scale, w, w_scale, offsets, out), stream, refuse)
 
 
 def _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down):

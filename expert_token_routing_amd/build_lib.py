@@ -3,7 +3,9 @@
 Usage: ``python -m expert_token_routing_amd.build_lib`` (or ``build()``).
 Compiles every ``csrc/*.hip`` with hipcc in parallel and links one shared
 library next to this file; ``calib/*.hip`` (counter calibration,
-include/moe_calib.h) becomes ``libmoe_calib.so`` beside it. Always recompiles.
+include/moe_calib.h) becomes ``libmoe_calib.so`` beside it, and
+``csrc/calls.cpp``, the Python side of the small calls, the extension module
+``_calls.so`` (host compiler, against the installed torch). Always recompiles.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = pathlib.Path(__file__).resolve().parent
@@ -21,6 +24,7 @@ CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libmoe.so"
 CALIB_LIB = PKG / "libmoe_calib.so"
+CALLS = PKG / "_calls.so"
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 COMMON_FLAGS = [
@@ -49,6 +53,26 @@ def _run(cmd):
     if r.returncode != 0:
         raise RuntimeError("command failed:\n" + " ".join(map(str, cmd)) + "\n" + r.stdout)
     return r.stdout
+
+
+def build_calls() -> str:
+    """csrc/calls.cpp -> _calls.so; torch's own libraries are in the process
+    before it is loaded."""
+    import torch
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found (needed to build _calls.so)")
+    torch_dir = pathlib.Path(torch.__file__).resolve().parent
+    tmp = CALLS.with_suffix(".so.tmp")
+    out = _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{ROOT / 'include'}",
+                f"-I{sysconfig.get_paths()['include']}", "-isystem", torch_dir / "include",
+                "-isystem", torch_dir / "include/torch/csrc/api/include",
+                "-isystem", pathlib.Path(hipcc()).resolve().parent.parent / "include",
+                str(CSRC / "calls.cpp"), "-o", str(tmp), f"-L{torch_dir / 'lib'}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+                "-ltorch_python"])
+    os.replace(tmp, CALLS)
+    return out
 
 
 _SGPR = re.compile(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b")
@@ -114,7 +138,11 @@ def build(verbose: bool = False, jobs: int | None = None) -> pathlib.Path:
 
     jobs = jobs or min(len(sources) + len(calib), max(1, min(16, os.cpu_count() or 1)))
     with ThreadPoolExecutor(jobs) as ex:
+        calls = ex.submit(build_calls)
         list(ex.map(compile_one, zip(sources + calib, objs + calib_objs)))
+        if verbose and calls.result().strip():
+            print(calls.result())
+        calls.result()
     problems = []
     for src in sources + calib:
         for asm_file in BUILD.glob(src.stem + "-hip-amdgcn-amd-amdhsa-*.s"):

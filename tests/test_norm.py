@@ -11,6 +11,7 @@ root, the three products and the final addition add at most 6 steps more. So
 """
 import ctypes
 import math
+import sys
 
 import pytest
 import torch
@@ -266,6 +267,41 @@ def test_norm_arguments_by_name_on_a_stream():
     got = M.moe_norm_pre(r=x, w=w, stream=s)
     s.synchronize()
     assert torch.equal(got, want) and torch.equal(M.moe_norm_pre(w=w, r=x), want)
+
+
+@gpu
+def test_small_calls_report_and_keep_what_they_are_given():
+    """The calls of the extension module: the library's status as MoEError, a
+    wrong number as TypeError, the caller's outputs returned as they are and
+    with no reference kept."""
+    x, w = torch.randn(6, 64, device="cuda", dtype=BF), torch.randn(64, device="cuda")
+    flat = torch.zeros(6 * 64 + 1, device="cuda", dtype=BF)[1:].view(6, 64)  # 2 bytes past an aligned address
+    i8, s = torch.zeros(6, 64, device="cuda", dtype=torch.int8), torch.ones(6, device="cuda")
+    for call in (lambda: M.moe_norm_pre(x, w, -1.0), lambda: M.moe_norm_pre(flat, w), lambda: M.moe_norm_post(flat, x),
+                 lambda: M.moe_norm_pre(x[:, :12].contiguous(), w[:12].contiguous()), lambda: M.moe_quantize_rows(flat),
+                 lambda: M.moe_quantize_rows(x[:, :24].contiguous()),
+                 lambda: M.moe_gemm_i8(i8, s, i8[None], s[None], out=torch.empty(37, device="cuda", dtype=BF)[1:].view(6, 6))):
+        with pytest.raises(M.MoEError):
+            call()
+    for call in (lambda: M.moe_norm_pre(x, w, "1"), lambda: M.moe_norm_post(x, x, residual_scale=None)):
+        with pytest.raises(TypeError):
+            call()
+    for call, exc in ((lambda: M.moe_norm_pre(x.t(), w), ValueError), (lambda: M.moe_norm_pre(x, w.cpu()), ValueError),
+                      (lambda: M.moe_norm_pre(x, w, stream=0), AttributeError), (lambda: M.moe_norm_post(x, x.float()[:5]), ValueError),
+                      (lambda: M.moe_gemm_i8(i8, s, i8.view(2, 3, 64), s.view(2, 3)), ValueError)):
+        with pytest.raises(exc):
+            call()
+    out, normed, q = torch.empty_like(x), torch.empty_like(x), torch.empty_like(i8)
+    held = [sys.getrefcount(t) for t in (x, w, out, normed, q, s)]
+    for _ in range(3):
+        assert M.moe_norm_pre(x, w, out=out) is out
+        got = M.moe_norm_post(x, x, w, w_next=w, out=out, normed=normed)
+        assert got[0] is out and got[1] is normed
+        got = M.moe_quantize_rows(x, q=q, scale=s)
+        assert got[0] is q and got[1] is s
+    assert M.moe_norm_post(x, x)[1] is None
+    del got
+    assert [sys.getrefcount(t) for t in (x, w, out, normed, q, s)] == held
 
 
 @gpu
