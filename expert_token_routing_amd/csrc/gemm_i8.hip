@@ -16,7 +16,7 @@
 // The weights are always the first operand, so a lane ends with 4 consecutive
 // channels of one token and stores them as one vector.
 //
-// One kernel in six tile shapes, from 16 x 32 (few rows: the weight stream is the
+// One kernel in seven tile shapes, from 16 x 32 (few rows: the weight stream is the
 // whole cost) to 288 x 256. The operands come through LDS by direct-to-LDS loads
 // of whole 128-byte lines. (Weight fragments loaded straight into registers, 16
 // rows x 64 bytes an instruction, streamed a DeepSeek-R1-shaped rank's 1.41 GB at
@@ -376,8 +376,11 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
 // Largest tile: 2 x 4 waves, 256 channels, blocks of up to 288 rows.
 typedef Shape<2, 4, 4, 2, 1> Big;
 constexpr int kBigFM = 9;
-// 128 rows x 128 channels, 8 waves, four stages.
+// 128 rows x 128 channels, 8 waves: four stages for up to one tile per CU, two
+// stages and two workgroups per CU for more (one streams while the other starts
+// or ends a tile).
 typedef Shape<2, 4, 2, 4, 1> Mid;
+typedef Shape<2, 4, 2, 2, 1> Mid2;
 constexpr int kMidFM = 4;
 // 64 x 64, four groups of 4 waves with two stages each: for few tiles, whose
 // time is the number of stages one after another.
@@ -601,8 +604,17 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   }
   if (rows <= 64 && streams && tiles(64, 64 / d) > cus)
     return go(Stream64{}, std::integral_constant<int, 4>{}, StreamE{}, 64, 2);
-  if (tiles(256, 256 / d) >= cus)
+  // The largest tiles read the fewest operand bytes, but one at a time per CU:
+  // they need rows to fill them and a long k, or very many tiles. (us, Mid2 / Big,
+  // 32 experts, K x N: 96 rows 7168 x 4096 192 / 214, 128 rows 273 / 221, 512 rows
+  // 595 / 447; 2880 x 2880 68 / 88, 99 / 91, 227 / 167; 1408 x 2048 22 / 33,
+  // 32 / 34, 66 / 70; 64 experts 1408 x 2048, 512 rows: 156 / 142.)
+  const int64_t tall = p.offsets ? rows_hint + rows_hint / 4 : rows_hint;
+  const int64_t mid = ceil_div(tall, 128) * p.E_local * ceil_div(p.N, 128 / d);
+  if (rows_hint >= 128 && mid > 2 * cus && (p.K >= 2048 || mid * p.K >= (int64_t(5) << 20)))
     return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
+  // (2048 x 7168 x 4096: Mid 75 us, Mid2 56, Big 58; 1024 x 7168 x 4096: Mid 38, Mid2 40)
+  if (mid > cus) return go(Mid2{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 2);
   if (tiles(128, 128 / d) >= cus / 2) return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
   return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
 }

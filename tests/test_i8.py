@@ -229,7 +229,8 @@ def test_gemm_i8_small(M_, K, N):
 
 @gpu
 @pytest.mark.parametrize("M_,K,N", [(2049, 272, 4096), (4096, 128, 4104), (1000, 1024, 4096), (8192, 400, 2048),
-                                    (600, 7168, 1024), (1, 7168, 4096), (64, 131056, 8)])
+                                    (600, 7168, 1024), (1, 7168, 4096), (64, 131056, 8), (4096, 2064, 4104),
+                                    (3000, 2048, 4096), (12800, 1920, 4096), (1000, 7168, 8)])
 def test_gemm_i8_large(M_, K, N):
     _check_gemm(M_, K, N)
 
@@ -239,13 +240,16 @@ def test_gemm_i8_large(M_, K, N):
     ([3, 0, 1, 16, 17, 33, 0], 208, 72, 9),           # few rows: one skinny pass, several for the longest
     ([90, 0, 1, 300, 64, 65, 5, 0], 272, 264, 0),     # small tiles
     ([200, 0, 129, 1, 500, 128], 400, 2056, 70),      # middle tiles
-    ([600, 0, 17, 289, 1000, 576, 1, 2000], 272, 4096, 11),  # the largest tiles, every block height
+    ([600, 0, 17, 289, 1000, 576, 1, 2000], 272, 4096, 11),  # two of them per CU
+    ([600, 0, 17, 289, 1000, 576, 1, 2000], 2064, 4096, 11),  # the largest tiles, every block height
+    ([520, 130, 0, 257, 700, 33, 161, 225], 2048, 4104, 0),
+    ([100, 80, 120, 90], 272, 4104, 5),               # middle tiles, one round of them
     ([0, 0, 0], 64, 64, 40),                          # no rows at all
     ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 4104, 2),        # streams: 16 rows a block
     ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 400, 4096, 1),  # 32 rows
     ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 4096, 3),  # 64 rows
     ([i % 4 for i in range(300)], 144, 1032, 5),      # more experts than the streams' tables hold
-], ids=["narrow", "small", "mid", "big", "none", "stream16", "stream32", "stream64", "many"])
+], ids=["narrow", "small", "mid", "mid2", "big", "big_whole", "mid_round", "none", "stream16", "stream32", "stream64", "many"])
 def test_gemm_i8_segments(segs, K, N, behind):
     _check_gemm(sum(segs) + behind, K, N, segs)
 
@@ -279,10 +283,11 @@ def _weights(g, E, H, I):
     ([100, 1, 0, 240], 144, 208, 5),
     ([700, 300, 0, 33, 600], 208, 400, 2),
     ([520, 480, 0, 700, 511, 512, 513, 1], 256, 2048, 0),
+    ([520, 480, 0, 700, 511, 512, 513, 1], 2064, 2048, 4),
     ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 1040, 1),
     ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 272, 1040, 0),
     ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 1040, 0),
-], ids=["one", "few", "decode", "small", "mid", "big", "stream16", "stream32", "stream64"])
+], ids=["one", "few", "decode", "small", "mid", "mid2", "big", "stream16", "stream32", "stream64"])
 def test_expert_ffn_i8(segs, H, I, behind):
     g = _gen(4)
     E, cap = len(segs), sum(segs) + behind
