@@ -16,7 +16,7 @@
 // The weights are always the first operand, so a lane ends with 4 consecutive
 // channels of one token and stores them as one vector.
 //
-// One kernel in seven tile shapes, from 16 x 32 (few rows: the weight stream is the
+// One kernel in ten tile shapes, from 16 x 32 (few rows: the weight stream is the
 // whole cost) to 288 x 256. The operands come through LDS by direct-to-LDS loads
 // of whole 128-byte lines. (Weight fragments loaded straight into registers, 16
 // rows x 64 bytes an instruction, streamed a DeepSeek-R1-shaped rank's 1.41 GB at
@@ -376,14 +376,17 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmArgs& p, c
 // Largest tile: 2 x 4 waves, 256 channels, blocks of up to 288 rows.
 typedef Shape<2, 4, 4, 2, 1> Big;
 constexpr int kBigFM = 9;
-// 128 rows x 128 channels, 8 waves: four stages for up to one tile per CU, two
-// stages and two workgroups per CU for more (one streams while the other starts
-// or ends a tile).
+// 128 rows x 128 channels, 8 waves for a group of k. Up to one tile per CU: four
+// stages (Mid), or for a long k two groups with two stages each (MidK). More
+// tiles: two stages and two workgroups per CU, so that one streams while the
+// other starts or ends a tile (Mid2).
 typedef Shape<2, 4, 2, 4, 1> Mid;
+typedef Shape<2, 4, 2, 2, 2> MidK;
 typedef Shape<2, 4, 2, 2, 1> Mid2;
 constexpr int kMidFM = 4;
-// 64 x 64, four groups of 4 waves with two stages each: for few tiles, whose
-// time is the number of stages one after another.
+// Fewer tiles, whose time is the number of stages one after another: 64 x 128 in
+// two groups of 4 waves, 64 x 64 in four.
+typedef Shape<2, 2, 4, 3, 2> Mid64;
 typedef Shape<2, 2, 2, 2, 4> Small;
 constexpr int kSmallFM = 2;
 
@@ -585,8 +588,12 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   typedef std::integral_constant<int, kMaxLocal> AnyE;
   typedef std::integral_constant<int, kStreamLocal> StreamE;
   // Ragged segments spread around the expected length: twice as many rows as
-  // expected still make one block.
-  const int64_t rows = p.offsets ? 2 * rows_hint : rows_hint;
+  // expected still make one block, and a block in two is a segment's last.
+  const int64_t rows = std::min(p.offsets ? 2 * rows_hint : rows_hint, p.capacity);
+  auto blocks = [&](int bm) {
+    const int64_t tall = std::min(p.offsets ? rows_hint + rows_hint / 4 : rows_hint, p.capacity);
+    return std::min(ceil_div(tall, bm) * p.E_local, ceil_div(rows_hint * p.E_local, bm) + p.E_local / 2);
+  };
   // Streams from the first tile beyond one per CU: a second round of narrow
   // tiles costs more (16 experts of 2880 x 768, 61 rows: 34.4 us narrow, 31.2 us).
   const bool streams = p.E_local <= kStreamLocal;
@@ -609,14 +616,21 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   // 32 experts, K x N: 96 rows 7168 x 4096 192 / 214, 128 rows 273 / 221, 512 rows
   // 595 / 447; 2880 x 2880 68 / 88, 99 / 91, 227 / 167; 1408 x 2048 22 / 33,
   // 32 / 34, 66 / 70; 64 experts 1408 x 2048, 512 rows: 156 / 142.)
-  const int64_t tall = p.offsets ? rows_hint + rows_hint / 4 : rows_hint;
-  const int64_t mid = ceil_div(tall, 128) * p.E_local * ceil_div(p.N, 128 / d);
+  const int64_t mid = blocks(128) * ceil_div(p.N, 128 / d);
   if (rows_hint >= 128 && mid > 2 * cus && (p.K >= 2048 || mid * p.K >= (int64_t(5) << 20)))
     return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
   // (2048 x 7168 x 4096: Mid 75 us, Mid2 56, Big 58; 1024 x 7168 x 4096: Mid 38, Mid2 40)
   if (mid > cus) return go(Mid2{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 2);
-  if (tiles(128, 128 / d) >= cus / 2) return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
-  return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
+  // The smallest tiles of which each CU gets one at most. (us: 512 rows 1408 x 2048
+  // Small 7.7, Mid64 9.4; 640 rows Small 11.6, Mid64 9.5; 512 rows 7168 x 4096
+  // Small 34, Mid64 28, Mid 35; 1024 rows MidK 37; 1280 rows 768 x 2048 Mid 8.7,
+  // MidK 9.8.)
+  if (blocks(64) * ceil_div(p.N, 64 / d) <= cus)
+    return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
+  if (blocks(64) * ceil_div(p.N, 128 / d) <= cus)
+    return go(Mid64{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
+  if (p.K > 2048) return go(MidK{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
+  return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
 }
 
 // ---------------------------------------------------------------------------

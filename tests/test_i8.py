@@ -230,7 +230,8 @@ def test_gemm_i8_small(M_, K, N):
 @gpu
 @pytest.mark.parametrize("M_,K,N", [(2049, 272, 4096), (4096, 128, 4104), (1000, 1024, 4096), (8192, 400, 2048),
                                     (600, 7168, 1024), (1, 7168, 4096), (64, 131056, 8), (4096, 2064, 4104),
-                                    (3000, 2048, 4096), (12800, 1920, 4096), (1000, 7168, 8)])
+                                    (3000, 2048, 4096), (12800, 1920, 4096), (1000, 7168, 8), (1000, 2064, 4096), (1000, 2304, 4104),
+                                    (500, 2064, 4096), (512, 256, 4096)])
 def test_gemm_i8_large(M_, K, N):
     _check_gemm(M_, K, N)
 
@@ -284,10 +285,13 @@ def _weights(g, E, H, I):
     ([700, 300, 0, 33, 600], 208, 400, 2),
     ([520, 480, 0, 700, 511, 512, 513, 1], 256, 2048, 0),
     ([520, 480, 0, 700, 511, 512, 513, 1], 2064, 2048, 4),
+    ([100, 60, 0, 64], 144, 2048, 1),                      # 64 x 128 tiles
+    ([110, 90, 100, 70, 100, 0, 100], 2064, 2048, 0),      # one round of 128 x 128, long k
+    ([110, 90, 100, 70, 100, 0, 129], 528, 2048, 0),       # and short
     ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 1040, 1),
     ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 272, 1040, 0),
     ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 1040, 0),
-], ids=["one", "few", "decode", "small", "mid", "mid2", "big", "stream16", "stream32", "stream64"])
+], ids=["one", "few", "decode", "small", "mid", "mid2", "big", "mid64", "mid_long", "mid_round", "stream16", "stream32", "stream64"])
 def test_expert_ffn_i8(segs, H, I, behind):
     g = _gen(4)
     E, cap = len(segs), sum(segs) + behind
