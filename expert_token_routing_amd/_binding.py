@@ -114,7 +114,9 @@ def _calls():
             raise RuntimeError("_calls.so is missing or was built for another torch: build it with "
                                "`python -m expert_token_routing_amd.build_lib`; there is no fallback path") from e
         module.bind(*(ctypes.cast(getattr(L, n), c_void_p).value
-                      for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8")))
+                      for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8",
+                                "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8", "moe_few_workspace_size",
+                                "moe_forward_few", "moe_forward_few_f32")))
         _calls_module = module
     return _calls_module
 
@@ -540,23 +542,6 @@ def _need_either(t, name, shape):
     return kind
 
 
-def _fits(*specs):
-    """Whether every (tensor or None, dtype, shape) is a contiguous tensor of
-    that type and shape on the GPU of the first one. Quick, and silent: where it
-    says no, the checks that follow say what is wrong."""
-    try:
-        index = specs[0][0].get_device()
-        if index < 0:
-            return False
-        for t, dtype, shape in specs:
-            if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
-                                  or not t.is_contiguous()):
-                return False
-    except AttributeError:  # not a tensor
-        return False
-    return True
-
-
 def _ints(*sizes):
     """Sizes that the library takes as int: ctypes would pass on a larger one's
     low 32 bits."""
@@ -564,10 +549,9 @@ def _ints(*sizes):
         raise ValueError(f"sizes are at most 2^31 - 1, got {max(sizes)}")
 
 
-def _dims(t, n):
-    """The shape of an n-dimensional tensor, None for anything else."""
-    shape = getattr(t, "shape", None)
-    return shape if shape is not None and len(shape) == n else None
+def _plain_int(n):
+    """An integer of another type (numpy's) as int; anything else as it is."""
+    return n if type(n) is int else int(n) if isinstance(n, numbers.Integral) else n
 
 
 def _gate_kind(gate, T, H):
@@ -644,45 +628,32 @@ def few_workspace_size(T, H, I, E, k, E_local) -> int:
     return int(lib().moe_few_workspace_size(T, H, I, E, k, E_local))
 
 
-def _few(name, out_dtype, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y, workspace):
-    torch = _torch()
-    mx, mr, mg = _dims(x, 2), _dims(w_router, 2), _dims(w_gate_up, 3)
-    if not (mx and mr and mg and mr[1] == mg[1] == mx[1] and mg[2] % 2 == 0 and type(k) is int and 1 <= k <= mr[0]
-            and 0 <= e0 <= mr[0] - mg[0]
-            and _fits((x, torch.bfloat16, mx), (w_router, torch.float32, mr), (bias, torch.float32, mr[:1]),
-                      (w_gate_up, torch.bfloat16, mg), (w_down, torch.bfloat16, (mg[0], mg[2] // 2, mx[1])),
-                      (y, out_dtype, mx))):
-        _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
-        mx, mr, mg = x.shape, w_router.shape, w_gate_up.shape
+def _few(name, out_dtype, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y, workspace, stream):
+    def refuse():
+        T, H, I, E, E_local, dev = _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
         if y is not None:
-            _need(y, out_dtype, "y", mx)
-        _placed(x.device, x=x, w_router=w_router, bias=bias, w_gate_up=w_gate_up, w_down=w_down, y=y)
-    (T, H), E, E_local, I = mx, mr[0], mg[0], mg[2] // 2
-    _ints(T, H, E, I)
-    dev = x.device
-    if y is None:
-        y = torch.empty(mx, dtype=out_dtype, device=dev)
-    L = lib()
-    ws = _workspace(L.moe_few_workspace_size(T, H, I, E, k, E_local), dev, workspace)
-    st = getattr(L, name)(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate_up), _ptr(w_down), T, H, I, E, k, e0,
-                          E_local, int(bool(renormalize)), _ptr(y), _ptr(ws), _nbytes(ws), _stream(None, dev))
-    check(st, name)
-    return y, ws
+            _need(y, out_dtype, "y", (T, H))
+        _ints(T, H, E, I)
+        _placed(dev, x=x, w_router=w_router, bias=bias, w_gate_up=w_gate_up, w_down=w_down, y=y)
+        if workspace is not None:
+            _workspace(lib().moe_few_workspace_size(T, H, I, E, k, E_local), dev, workspace)
+    return _small_call(name, (x, w_router, bias, w_gate_up, w_down, _plain_int(k), _plain_int(e0), renormalize, y,
+                              workspace), stream, refuse)
 
 
-@_on_stream
-def moe_forward_few(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None):
+def moe_forward_few(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None,
+                    stream=None):
     """moe_forward for at most FEW_TOKENS tokens in two kernels: y [T, H] bf16,
-    rounded once. Returns (y, workspace). Takes ``stream``."""
-    return _few("moe_forward_few", _torch().bfloat16, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
-                workspace)
+    rounded once. Returns (y, workspace)."""
+    return _few("forward_few", _torch().bfloat16, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
+                workspace, stream)
 
 
-@_on_stream
-def moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None):
+def moe_forward_few_f32(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize=True, *, y=None, workspace=None,
+                        stream=None):
     """moe_forward_few with the share kept in float32 (y [T, H] float32)."""
-    return _few("moe_forward_few_f32", _torch().float32, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
-                workspace)
+    return _few("forward_few_f32", _torch().float32, x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y,
+                workspace, stream)
 
 
 # --------------------------------------------------------------------------- #
@@ -767,37 +738,25 @@ def expert_ffn_i8_workspace_size(H, I, capacity) -> int:
     return int(lib().moe_expert_ffn_i8_workspace_size(H, I, capacity))
 
 
-@_on_stream
-def moe_expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, *, out=None, workspace=None):
+def moe_expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, *, out=None, workspace=None, stream=None):
     """moe_expert_ffn with 8-bit weights (moe_quantize_weights) and activations
     quantised per row: expert outputs [cap, H] bf16 for the segments in
-    ``offsets``. Returns (out, workspace). Takes ``stream``."""
-    torch = _torch()
-    mx, mg = _dims(x_perm, 2), _dims(w_gate_up, 3)
-    if not (mx and mg and mg[2] == mx[1] and mg[1] % 2 == 0
-            and _fits((x_perm, torch.bfloat16, mx), (offsets, torch.int32, (mg[0] + 1,)), (w_gate_up, torch.int8, mg),
-                      (s_gate_up, torch.float32, mg[:2]), (w_down, torch.int8, (mg[0], mx[1], mg[1] // 2)),
-                      (s_down, torch.float32, (mg[0], mx[1])), (out, torch.bfloat16, mx))):
+    ``offsets``. Returns (out, workspace)."""
+    def refuse():
+        torch = _torch()
         _need(x_perm, torch.bfloat16, "x_perm", (None, None))
-        mx = x_perm.shape
-        _need_ffn_i8(mx[1], w_gate_up, s_gate_up, w_down, s_down)
-        mg = w_gate_up.shape
-        _need(offsets, torch.int32, "offsets", (mg[0] + 1,))
+        cap, H = x_perm.shape
+        E_local, I = _need_ffn_i8(H, w_gate_up, s_gate_up, w_down, s_down)
+        _need(offsets, torch.int32, "offsets", (E_local + 1,))
         if out is not None:
-            _need(out, torch.bfloat16, "out", mx)
+            _need(out, torch.bfloat16, "out", (cap, H))
+        _ints(cap, H, E_local, I)
         _placed(x_perm.device, x_perm=x_perm, offsets=offsets, w_gate_up=w_gate_up, s_gate_up=s_gate_up, w_down=w_down,
                 s_down=s_down, out=out)
-    (cap, H), E_local, I = mx, mg[0], mg[1] // 2
-    _ints(cap, H, E_local, I)
-    dev = x_perm.device
-    if out is None:
-        out = torch.empty_like(x_perm)
-    L = lib()
-    ws = _workspace(L.moe_expert_ffn_i8_workspace_size(H, I, cap), dev, workspace)
-    st = L.moe_expert_ffn_i8(_ptr(x_perm), _ptr(offsets), _ptr(w_gate_up), _ptr(s_gate_up), _ptr(w_down), _ptr(s_down),
-                             H, I, E_local, cap, _ptr(out), _ptr(ws), _nbytes(ws), _stream(None, dev))
-    check(st, "moe_expert_ffn_i8")
-    return out, ws
+        if workspace is not None:
+            _workspace(lib().moe_expert_ffn_i8_workspace_size(H, I, cap), x_perm.device, workspace)
+    return _small_call("expert_ffn_i8", (x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, out, workspace), stream,
+                       refuse)
 
 
 def forward_i8_workspace_size(T, H, I, E, k, E_local) -> int:

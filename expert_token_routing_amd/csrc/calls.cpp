@@ -1,15 +1,21 @@
-// The Python side of the small calls (norms, row quantiser, 8-bit product),
-// whose kernels take 4 to 10 us, less than the checks and allocations around
-// them in Python: the same checks on the tensors themselves, the outputs, and
-// the call of the C entry point. Calling thread per call, ctypes -> here (a
-// launch alone is 3.2 us): norm before the block 8.4 -> 4.5 us, after it with
-// two outputs 11.9 -> 5.4, quantiser 9 -> 5.3, product 8.6 -> 4.6.
+// The Python side of the small calls (norms, row quantiser, 8-bit products, the
+// share for a few tokens), whose kernels take 4 to 20 us, less than the checks
+// and allocations around them in Python: the same checks on the tensors
+// themselves, the outputs, and the call of the C entry point. Calling thread per
+// call, ctypes -> here (a launch alone is 3.2 us): norm before the block
+// 8.4 -> 4.5 us, after it with two outputs 11.9 -> 5.4, quantiser 9 -> 5.3,
+// product 8.6 -> 4.6, few tokens 14.5 -> 8.3 (two launches), 8-bit MLPs 22 ->
+// 16.7 (four).
 //
 // Each function returns None where its arguments do not fit (or the tensors
 // are not on the current device): the caller's checks then say why. A status
 // other than 0 is returned as an int, else the outputs.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstring>
 
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
@@ -31,6 +37,11 @@ struct {
   decltype(&moe_norm_post) norm_post;
   decltype(&moe_quantize_rows) quantize_rows;
   decltype(&moe_gemm_i8) gemm_i8;
+  decltype(&moe_expert_ffn_i8_workspace_size) expert_ffn_i8_workspace_size;
+  decltype(&moe_expert_ffn_i8) expert_ffn_i8;
+  decltype(&moe_few_workspace_size) few_workspace_size;
+  decltype(&moe_forward_few) forward_few;
+  decltype(&moe_forward_few_f32) forward_few_f32;
 } entry;
 
 // One call's tensors, all on the current device.
@@ -66,6 +77,15 @@ struct Call {
   void may(const Tensor* t, ScalarType type, IntArrayRef shape) { ok = ok && (t == nullptr || is(t, type, shape)); }
   Tensor out(const Tensor* t, ScalarType type, IntArrayRef shape) const {
     return t ? *t : at::empty(shape, at::TensorOptions(type).device(at::kCUDA, c10::DeviceIndex(index)));
+  }
+  // The caller's workspace where it is large enough, or a new one.
+  Tensor workspace(const Tensor* t, size_t bytes) {
+    if (t) {
+      ok = ok && t->is_cuda() && t->get_device() == index && t->is_contiguous() && t->nbytes() >= bytes;
+      return *t;
+    }
+    return at::empty({std::max<int64_t>(int64_t(bytes), 1)},
+                     at::TensorOptions(at::kByte).device(at::kCUDA, c10::DeviceIndex(index)));
   }
   hipStream_t stream() const { return c10::hip::getCurrentHIPStream(c10::DeviceIndex(index)).stream(); }
 };
@@ -219,21 +239,90 @@ PyObject* gemm_i8(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of moe_norm_pre, moe_norm_post, moe_quantize_rows, moe_gemm_i8)
+// expert_ffn_i8(x_perm, offsets, w_gate_up, s_gate_up, w_down, s_down, out, workspace)
+PyObject* expert_ffn_i8(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 8)) return nullptr;
+  Call c;
+  const Tensor* x = c.first(p[0], 2);
+  if (!c.ok || x->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
+  const Tensor *offsets = c.arg(p[1]), *gu = c.arg(p[2]), *sg = c.arg(p[3]), *dn = c.arg(p[4]), *sd = c.arg(p[5]),
+               *o = c.arg(p[6]), *w = c.arg(p[7]);
+  if (!c.ok || !gu || gu->dim() != 3 || gu->size(1) % 2 != 0) Py_RETURN_NONE;
+  const int64_t cap = x->size(0), H = x->size(1), E = gu->size(0), I = gu->size(1) / 2;
+  c.need(offsets, at::kInt, {E + 1});
+  c.need(gu, at::kChar, {E, 2 * I, H});
+  c.need(sg, at::kFloat, {E, 2 * I});
+  c.need(dn, at::kChar, {E, H, I});
+  c.need(sd, at::kFloat, {E, H});
+  c.may(o, at::kBFloat16, {cap, H});
+  if (!c.ok || E > INT_MAX || I > INT_MAX) Py_RETURN_NONE;
+  const Tensor ws = c.workspace(w, entry.expert_ffn_i8_workspace_size(int(H), int(I), cap));
+  if (!c.ok) Py_RETURN_NONE;
+  const Tensor out = c.out(o, at::kBFloat16, {cap, H});
+  const int st = unlocked([&] {
+    return entry.expert_ffn_i8(in<moe_bf16>(x), in<int32_t>(offsets), in<int8_t>(gu), in<float>(sg), in<int8_t>(dn),
+                               in<float>(sd), int(H), int(I), int(E), cap, to<moe_bf16>(out), to<void>(ws), ws.nbytes(),
+                               c.stream());
+  });
+  return st == MOE_OK ? pair(out, ws) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// forward_few(x, w_router, bias, w_gate_up, w_down, k, e0, renormalize, y, workspace)
+template <bool F32>
+PyObject* forward_few(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 10)) return nullptr;
+  Call c;
+  const Tensor* x = c.first(p[0], 2);
+  if (!c.ok || x->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
+  const Tensor *wr = c.arg(p[1]), *bias = c.arg(p[2]), *gu = c.arg(p[3]), *dn = c.arg(p[4]), *o = c.arg(p[8]),
+               *w = c.arg(p[9]);
+  if (!c.ok || !wr || wr->dim() != 2 || !gu || gu->dim() != 3 || gu->size(2) % 2 != 0) Py_RETURN_NONE;
+  const int64_t T = x->size(0), H = x->size(1), E = wr->size(0), El = gu->size(0), I = gu->size(2) / 2;
+  const ScalarType type = F32 ? at::kFloat : at::kBFloat16;
+  c.need(wr, at::kFloat, {E, H});
+  c.may(bias, at::kFloat, {E});
+  c.need(gu, at::kBFloat16, {El, H, 2 * I});
+  c.need(dn, at::kBFloat16, {El, I, H});
+  c.may(o, type, {T, H});
+  if (!c.ok || E > INT_MAX || I > INT_MAX || !PyLong_Check(p[5]) || !PyLong_Check(p[6])) Py_RETURN_NONE;
+  int over_k, over_e;
+  const int64_t k = PyLong_AsLongLongAndOverflow(p[5], &over_k), e0 = PyLong_AsLongLongAndOverflow(p[6], &over_e);
+  if (over_k || over_e || k < 1 || k > E || e0 < 0 || e0 > E - El) Py_RETURN_NONE;
+  const int renormalize = PyObject_IsTrue(p[7]);
+  if (renormalize < 0) return nullptr;
+  const Tensor ws = c.workspace(w, entry.few_workspace_size(int(T), int(H), int(I), int(E), int(k), int(El)));
+  if (!c.ok) Py_RETURN_NONE;
+  const Tensor y = c.out(o, type, {T, H});
+  const int st = unlocked([&] {
+    if constexpr (F32)
+      return entry.forward_few_f32(in<moe_bf16>(x), in<float>(wr), in<float>(bias), in<moe_bf16>(gu), in<moe_bf16>(dn),
+                                   int(T), int(H), int(I), int(E), int(k), int(e0), int(El), renormalize, to<float>(y),
+                                   to<void>(ws), ws.nbytes(), c.stream());
+    else
+      return entry.forward_few(in<moe_bf16>(x), in<float>(wr), in<float>(bias), in<moe_bf16>(gu), in<moe_bf16>(dn),
+                               int(T), int(H), int(I), int(E), int(k), int(e0), int(El), renormalize, to<moe_bf16>(y),
+                               to<void>(ws), ws.nbytes(), c.stream());
+  });
+  return st == MOE_OK ? pair(y, ws) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(addresses of the entry points, in the order of `entry`)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 4)) return nullptr;
-  void* at[4];
-  for (int i = 0; i < 4; ++i) {
+  void* at[sizeof(entry) / sizeof(void*)];
+  static_assert(sizeof(at) == sizeof(entry), "an address each");
+  if (!count(n, sizeof(at) / sizeof(void*))) return nullptr;
+  for (Py_ssize_t i = 0; i < n; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i]);
     if (!at[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
       return nullptr;
     }
   }
-  entry.norm_pre = reinterpret_cast<decltype(entry.norm_pre)>(at[0]);
-  entry.norm_post = reinterpret_cast<decltype(entry.norm_post)>(at[1]);
-  entry.quantize_rows = reinterpret_cast<decltype(entry.quantize_rows)>(at[2]);
-  entry.gemm_i8 = reinterpret_cast<decltype(entry.gemm_i8)>(at[3]);
+  memcpy(&entry, at, sizeof(entry));
   Py_RETURN_NONE;
 }
 
@@ -245,6 +334,9 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"norm_post", fast(norm_post), METH_FASTCALL, nullptr},
                          {"quantize_rows", fast(quantize_rows), METH_FASTCALL, nullptr},
                          {"gemm_i8", fast(gemm_i8), METH_FASTCALL, nullptr},
+                         {"expert_ffn_i8", fast(expert_ffn_i8), METH_FASTCALL, nullptr},
+                         {"forward_few", fast(forward_few<false>), METH_FASTCALL, nullptr},
+                         {"forward_few_f32", fast(forward_few<true>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
