@@ -4,7 +4,7 @@
 // themselves, the outputs, and the call of the C entry point. Calling thread per
 // call, ctypes -> here (a launch alone is 3.2 us): norm before the block
 // 8.4 -> 4.5 us, after it with two outputs 11.9 -> 5.4, quantiser 9 -> 5.3,
-// product 8.6 -> 4.6, few tokens 14.5 -> 8.3 (two launches), 8-bit MLPs 22 ->
+// product 8.6 -> 4.6, few tokens 14.6 -> 8.3 (two launches), 8-bit MLPs 20.5 ->
 // 16.7 (four).
 //
 // Each function returns None where its arguments do not fit (or the tensors
