@@ -115,13 +115,15 @@ bool count(Py_ssize_t got, Py_ssize_t want) {
   return false;
 }
 
-// f() without the interpreter's lock
+// f() without the interpreter's lock, which is held again where f throws (a
+// tensor without storage has no data pointer)
 template <typename F>
 int unlocked(F f) {
-  PyThreadState* state = PyEval_SaveThread();
-  const int status = f();
-  PyEval_RestoreThread(state);
-  return status;
+  struct Unlock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+  } unlock;
+  return f();
 }
 PyObject* wrap(const Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;

@@ -304,6 +304,21 @@ def test_small_calls_report_and_keep_what_they_are_given():
 
 
 @gpu
+def test_small_calls_refuse_tensors_without_storage():
+    """A tensor that only pretends to be on the GPU has no data pointer: an
+    exception, and the calls after it work."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    x, w = torch.randn(6, 64, device="cuda", dtype=BF), torch.randn(64, device="cuda")
+    mode = FakeTensorMode()
+    fx, fw = mode.from_tensor(x), mode.from_tensor(w)
+    for call in (lambda: M.moe_norm_pre(fx, fw), lambda: M.moe_norm_pre(fx, fw, out=fx),
+                 lambda: M.moe_norm_post(fx, fx, fw), lambda: M.moe_quantize_rows(fx)):
+        with pytest.raises((RuntimeError, TypeError, ValueError)):
+            call()
+        assert torch.equal(M.moe_norm_pre(x, w), M.moe_norm_pre(x, w))
+
+
+@gpu
 def test_norm_replays_and_other_stream():
     y, r, wp, ga, wn = _inputs(700, 7168, F32, BF, "channel", True)
     ref, nref = M.moe_norm_post(y, r, wp, gate=ga, w_next=wn)
