@@ -16,7 +16,7 @@
 // The weights are always the first operand, so a lane ends with 4 consecutive
 // channels of one token and stores them as one vector.
 //
-// One kernel in ten tile shapes, from 16 x 32 (few rows: the weight stream is the
+// One kernel in a dozen tile shapes, from 16 x 32 (few rows: the weight stream is the
 // whole cost) to 288 x 256. The operands come through LDS by direct-to-LDS loads
 // of whole 128-byte lines. (Weight fragments loaded straight into registers, 16
 // rows x 64 bytes an instruction, streamed a DeepSeek-R1-shaped rank's 1.41 GB at
@@ -398,7 +398,9 @@ typedef Shape<1, 2, 2, 3, 2> Stream;
 typedef Shape<1, 2, 2, 2, 2> Stream64;  // 64 rows
 constexpr int kStreamLocal = 256;  // local experts (two workgroups fill the LDS)
 typedef Shape<1, 2, 1, 3, 8> Narrow;
-typedef Shape<1, 2, 2, 3, 4> NarrowGU;
+typedef Shape<1, 2, 2, 3, 4> NarrowGU;    // 16 or 32 rows
+typedef Shape<1, 2, 1, 2, 8> Narrow32;    // 32 rows x 32 channels
+typedef Shape<2, 2, 1, 3, 4> Narrow64;    // 64 rows x 32 channels
 
 // Row caps of the largest tile (the fewest rounds of the grid win, weighted by
 // the tallest block, as in the bf16 grouped GEMM); the others have one.
@@ -611,6 +613,25 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   }
   if (rows <= 64 && streams && tiles(64, 64 / d) > cus)
     return go(Stream64{}, std::integral_constant<int, 4>{}, StreamE{}, 64, 2);
+  // The smallest tiles of which each CU gets one at most. (us: 64 x 7168 x 4096
+  // Narrow 14.1, Narrow32 11.0, Narrow64 13.6, Small 17.8; 128 x 7168 x 4096 25.3,
+  // 18.5, 14.3, 17.7; 128 x 7168 x 1024 8.4, 10.2, 13.8, 16.8; 512 rows 1408 x 2048
+  // Small 7.7, Mid64 9.4; 640 rows Small 11.6, Mid64 9.5; 512 rows 7168 x 4096
+  // Small 34, Mid64 28, Mid 35; 1024 rows MidK 37; 1280 rows 768 x 2048 Mid 8.7,
+  // MidK 9.8.)
+  typedef std::integral_constant<int, 1> One;
+  typedef std::integral_constant<int, 2> Two;
+  auto once = [&](int bm, int outputs) { return blocks(bm) * ceil_div(p.N, outputs) <= cus; };
+  if constexpr (SWIGLU) {
+    if (once(16, 32)) return go(NarrowGU{}, One{}, AnyE{}, 16, 1);
+    if (once(32, 32)) return go(NarrowGU{}, Two{}, AnyE{}, 32, 1);
+  } else {
+    if (once(16, 32)) return go(Narrow{}, One{}, AnyE{}, 16, 1);
+    if (once(32, 32)) return go(Narrow32{}, Two{}, AnyE{}, 32, 1);
+    if (once(64, 32)) return go(Narrow64{}, Two{}, AnyE{}, 64, 1);
+  }
+  if (once(64, 64 / d)) return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
+  if (once(64, 128 / d)) return go(Mid64{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
   // The largest tiles read the fewest operand bytes, but one at a time per CU:
   // they need rows to fill them and a long k, or very many tiles. (us, Mid2 / Big,
   // 32 experts, K x N: 96 rows 7168 x 4096 192 / 214, 128 rows 273 / 221, 512 rows
@@ -621,14 +642,6 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
     return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
   // (2048 x 7168 x 4096: Mid 75 us, Mid2 56, Big 58; 1024 x 7168 x 4096: Mid 38, Mid2 40)
   if (mid > cus) return go(Mid2{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 2);
-  // The smallest tiles of which each CU gets one at most. (us: 512 rows 1408 x 2048
-  // Small 7.7, Mid64 9.4; 640 rows Small 11.6, Mid64 9.5; 512 rows 7168 x 4096
-  // Small 34, Mid64 28, Mid 35; 1024 rows MidK 37; 1280 rows 768 x 2048 Mid 8.7,
-  // MidK 9.8.)
-  if (blocks(64) * ceil_div(p.N, 64 / d) <= cus)
-    return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
-  if (blocks(64) * ceil_div(p.N, 128 / d) <= cus)
-    return go(Mid64{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
   if (p.K > 2048) return go(MidK{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
   return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
 }

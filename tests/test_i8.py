@@ -231,7 +231,8 @@ def test_gemm_i8_small(M_, K, N):
 @pytest.mark.parametrize("M_,K,N", [(2049, 272, 4096), (4096, 128, 4104), (1000, 1024, 4096), (8192, 400, 2048),
                                     (600, 7168, 1024), (1, 7168, 4096), (64, 131056, 8), (4096, 2064, 4104),
                                     (3000, 2048, 4096), (12800, 1920, 4096), (1000, 7168, 8), (1000, 2064, 4096), (1000, 2304, 4104),
-                                    (500, 2064, 4096), (512, 256, 4096)])
+                                    (500, 2064, 4096), (512, 256, 4096), (128, 2064, 4096), (100, 7168, 4096),
+                                    (64, 2048, 4096), (64, 16, 4096), (128, 16, 4096), (127, 640, 4088), (33, 144, 4096)])
 def test_gemm_i8_large(M_, K, N):
     _check_gemm(M_, K, N)
 
@@ -244,13 +245,16 @@ def test_gemm_i8_large(M_, K, N):
     ([600, 0, 17, 289, 1000, 576, 1, 2000], 272, 4096, 11),  # two of them per CU
     ([600, 0, 17, 289, 1000, 576, 1, 2000], 2064, 4096, 11),  # the largest tiles, every block height
     ([520, 130, 0, 257, 700, 33, 161, 225], 2048, 4104, 0),
+    ([33, 0, 40, 20, 1, 50], 272, 1032, 7),           # 32 x 32 tiles
+    ([33, 64, 40, 20, 1, 50], 256, 2056, 0),          # 64 x 32
+    ([90, 0, 1, 300, 64, 65, 5, 0], 272, 1032, 0),    # 64 x 64
     ([100, 80, 120, 90], 272, 4104, 5),               # middle tiles, one round of them
     ([0, 0, 0], 64, 64, 40),                          # no rows at all
     ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 4104, 2),        # streams: 16 rows a block
     ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 400, 4096, 1),  # 32 rows
     ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 4096, 3),  # 64 rows
     ([i % 4 for i in range(300)], 144, 1032, 5),      # more experts than the streams' tables hold
-], ids=["narrow", "small", "mid", "mid2", "big", "big_whole", "mid_round", "none", "stream16", "stream32", "stream64", "many"])
+], ids=["narrow", "small", "mid", "mid2", "big", "big_whole", "narrow32", "narrow64", "small64", "mid_round", "none", "stream16", "stream32", "stream64", "many"])
 def test_gemm_i8_segments(segs, K, N, behind):
     _check_gemm(sum(segs) + behind, K, N, segs)
 
@@ -285,13 +289,16 @@ def _weights(g, E, H, I):
     ([700, 300, 0, 33, 600], 208, 400, 2),
     ([520, 480, 0, 700, 511, 512, 513, 1], 256, 2048, 0),
     ([520, 480, 0, 700, 511, 512, 513, 1], 2064, 2048, 4),
+    ([33, 0, 40, 20, 1, 50], 272, 1040, 3),                # 32 rows x 32 outputs
+    ([33, 0, 40, 20, 1, 50], 256, 1040, 0),
+    ([100, 1, 0, 240], 144, 688, 0),                       # 64 rows x 32 outputs
     ([100, 60, 0, 64], 144, 2048, 1),                      # 64 x 128 tiles
     ([110, 90, 100, 70, 100, 0, 100], 2064, 2048, 0),      # one round of 128 x 128, long k
     ([110, 90, 100, 70, 100, 0, 129], 528, 2048, 0),       # and short
     ([5, 0, 8, 3, 1, 2, 17, 9, 0, 4, 6, 7, 33, 0, 1, 2], 272, 1040, 1),
     ([15, 0, 8, 13, 11, 32, 17, 9, 0, 14, 6, 7, 33, 0, 1, 20], 272, 1040, 0),
     ([25, 0, 48, 13, 31, 64, 17, 9, 0, 34, 65, 27, 33, 0, 1, 20], 272, 1040, 0),
-], ids=["one", "few", "decode", "small", "mid", "mid2", "big", "mid64", "mid_long", "mid_round", "stream16", "stream32", "stream64"])
+], ids=["one", "few", "decode", "small", "mid", "mid2", "big", "rows32", "rows32_whole", "rows64", "mid64", "mid_long", "mid_round", "stream16", "stream32", "stream64"])
 def test_expert_ffn_i8(segs, H, I, behind):
     g = _gen(4)
     E, cap = len(segs), sum(segs) + behind
