@@ -649,12 +649,18 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
 // ---------------------------------------------------------------------------
 // Quantisation
 // ---------------------------------------------------------------------------
-// q = 127 v / top rounded to the nearest integer, halves to even. v and top
-// have at most 24 significant bits and 127 v is formed first: the quotient of
-// the reciprocal estimate is corrected once by its exact remainder (fma), so
-// exact halves of bf16 values stay exact. A row whose top is below 2^-64 (or
-// above 2^64) is multiplied by 2^64 (2^-64) first, which keeps the reciprocal
-// and 127 v finite and normal.
+// q = 127 v / top rounded to the nearest integer, halves to even. A row whose
+// top is below 2^-64 (or above 2^64) is multiplied by 2^64 (2^-64) first, which
+// keeps the reciprocal and 127 v finite and normal.
+//
+// bf16 values: 127 v is exact, and the quotient of the reciprocal estimate is
+// corrected once by its exact remainder (fma); it is a half or at least 2^-9
+// away from one, so its rounding decides right.
+// float32 values: 127 v has 31 bits and the quotient can lie closer to a half
+// than its own last bit, so the half is compared exactly: m = floor(127 v / top)
+// to within one, and 254 v (as hi + lo) against (2 m + 1) top. hi - (2 m + 1)
+// top is exact where it is small, and where it is not, lo does not change its
+// sign.
 struct RowScale {
   float lift, top, rcp, scale;
   bool zero;  // q = 0 throughout: top is 0, infinite or NaN
@@ -666,11 +672,20 @@ struct RowScale {
     scale = t / 127.f;
     zero = !(t > 0.f) || top_bits >= 0x7F800000u;
   }
+  template <bool F32 = false>
   __device__ __forceinline__ int q(float v) const {
-    const float n = v * lift * 127.f;
-    const float t = n * rcp;
-    const float r = fmaf(-t, top, n);
-    return zero ? 0 : int(rintf(fmaf(r, rcp, t)));
+    if constexpr (F32) {
+      const float vl = v * lift, hi = vl * 254.f, lo = fmaf(vl, 254.f, -hi);
+      const float m = floorf(0.5f * hi * rcp);
+      const float over = fmaf(-fmaf(2.f, m, 1.f), top, hi) + lo;
+      const int f = int(m);
+      return zero ? 0 : f + (over > 0.f || (over == 0.f && (f & 1)) ? 1 : 0);
+    } else {
+      const float n = v * lift * 127.f;
+      const float t = n * rcp;
+      const float r = fmaf(-t, top, n);
+      return zero ? 0 : int(rintf(fmaf(r, rcp, t)));
+    }
   }
 };
 
@@ -746,8 +761,8 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const void* x, cons
     if (threadIdx.x == 0) scale[m] = rs.scale;
     auto put = [&](const float (&f)[8], int c) {
       reinterpret_cast<uint2*>(q)[m * nvec + c] =
-          make_uint2(pack4(rs.q(f[0]), rs.q(f[1]), rs.q(f[2]), rs.q(f[3])),
-                     pack4(rs.q(f[4]), rs.q(f[5]), rs.q(f[6]), rs.q(f[7])));
+          make_uint2(pack4(rs.template q<F32>(f[0]), rs.template q<F32>(f[1]), rs.template q<F32>(f[2]), rs.template q<F32>(f[3])),
+                     pack4(rs.template q<F32>(f[4]), rs.template q<F32>(f[5]), rs.template q<F32>(f[6]), rs.template q<F32>(f[7])));
     };
     if constexpr (NV > 0) {
 #pragma unroll

@@ -341,6 +341,26 @@ def test_expert_ffn_i8(segs, H, I, behind):
 
 
 @gpu
+def test_expert_ffn_i8_h_to_the_nearest():
+    """Every one of 33.5 million float32 h's next to its row's largest: 127 h / top
+    in 64 bits is on the same side of each half as the quotient of the two
+    24-bit values itself (254 h and an odd multiple of top differ by 2^-33 of
+    them at least, or not at all), so q is equal, not near."""
+    R, H, I = 16384, 64, 2048
+    g = _gen(7)
+    x = torch.randn((R, H), generator=g, device="cuda").to(BF)
+    w = _weights(g, 1, H, I)
+    off = torch.tensor([0, R], device="cuda", dtype=torch.int32)
+    print(f"[gpu] expert_ffn_i8 rows={R} H={H} I={I}", flush=True)
+    _, ws = M.moe_expert_ffn_i8(x, off, *w)
+    torch.cuda.synchronize()
+    lay = _layout(R, R, H, I)
+    h, hq = (ws[a:a + b].view(t).reshape(R, I) for (a, b), t in ((lay["h"], F32), (lay["hq"], I8)))
+    off_by = int(_quantized(h)[0].ne(hq.to(F64)).sum())
+    assert off_by == 0, f"{off_by} of {R * I} values of h are not the nearest"
+
+
+@gpu
 @pytest.mark.parametrize("T,H,I,E,k,e0,El", [(1, 128, 32, 8, 2, 0, 8), (50, 272, 48, 12, 3, 4, 5), (900, 256, 400, 16, 4, 3, 6),
                                              (3000, 1024, 2048, 8, 2, 0, 8)])
 def test_forward_i8_equals_its_steps(T, H, I, E, k, e0, El):
