@@ -451,6 +451,13 @@ route_logits_w32_kernel(const uint16_t* __restrict__ x, const float* __restrict_
 
 }  // namespace routedma
 
+// What the selection and the softmax make of a logit: NaN counts as -infinity.
+// A maximum skips NaN and NaN equals nothing, so a round over NaN alone would
+// find no expert, and the ids after it would be none either: dispatch and the
+// expert MLPs index with them. (A token whose logits are all NaN still gets NaN
+// weights, from -infinity less itself.)
+__device__ __forceinline__ float rankable(float l) { return l == l ? l : -INFINITY; }
+
 // One wave per token: top-k by (logit descending, expert id ascending), then
 // softmax weights. Lane l holds experts l, l+64, ... (EPL per lane). Each of
 // the k rounds takes the wave maximum of the experts not yet taken (DPP, no
@@ -505,7 +512,7 @@ route_topk_kernel(float* __restrict__ logits, const float* __restrict__ part, in
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
     if (part == nullptr) v[i] = e < E ? row[e] : -INFINITY;
-    if (e >= E) v[i] = -INFINITY;
+    v[i] = e < E ? rankable(v[i]) : -INFINITY;
     if (e < E) {
       live |= 1u << i;
       lm = fmaxf(lm, v[i]);
@@ -633,6 +640,8 @@ route_topk_vec_kernel(float* __restrict__ logits, const float* __restrict__ part
       for (int i = 0; i < Q; ++i) v[i] += bias[Q * lane + i];
     store_q<Q>(row, v);
   }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) v[i] = rankable(v[i]);
   float lm = v[0];
 #pragma unroll
   for (int i = 1; i < Q; ++i) lm = fmaxf(lm, v[i]);
@@ -763,6 +772,8 @@ route_topk_row_kernel(float* __restrict__ logits, const float* __restrict__ part
     }
     store_q<Q>(row, v);
   }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) v[i] = rankable(v[i]);
   float lm = v[0];
 #pragma unroll
   for (int i = 1; i < Q; ++i) lm = fmaxf(lm, v[i]);
@@ -776,9 +787,9 @@ route_topk_row_kernel(float* __restrict__ logits, const float* __restrict__ part
     den_all = row_sum16(s);
   }
 
-  // A taken expert's value becomes NaN: the maximum ignores NaN and no NaN
-  // equals the row maximum, so it is never chosen again (a logit of -inf
-  // stays selectable).
+  // A taken expert's value becomes NaN (none is left by rankable): the maximum
+  // ignores NaN and no NaN equals the row maximum, so it is never chosen again
+  // (a logit of -inf stays selectable).
   const uint32_t base = uint32_t(Q * l16);
   int my_e = 0;
   float my_v = 0.f;

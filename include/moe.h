@@ -89,7 +89,11 @@ size_t moe_route_workspace_size(int T, int H, int E, int k);
  *                     selection and the softmax use. Computed with float32
  *                     accuracy (exact bf16 products, float32 accumulation).
  *   topk_idx  [T, k]  i32    OUT: expert ids by descending logit; equal
- *                     logits put the lower expert id first
+ *                     logits put the lower expert id first. A NaN logit (it
+ *                     is stored as NaN) counts as -infinity here and in
+ *                     topk_w: the ids are distinct and in [0, E) whatever x
+ *                     holds. A token whose logits are all NaN gets experts
+ *                     0 .. k-1 and NaN weights.
  *   topk_w    [T, k]  f32    OUT: combine weight of each selected expert
  *   workspace, workspace_bytes: at least moe_route_workspace_size bytes,
  *                     256-byte aligned
