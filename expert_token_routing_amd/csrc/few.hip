@@ -364,7 +364,8 @@ __device__ __forceinline__ bool stream(const Args& a, const Tables& s, int e, in
             const int j = 2 * i + b;
             const float f = __uint_as_float(qx[d][gi][j >> 2][j & 3]);
             hi[b] = __float_as_uint(f) & 0xFFFF0000u;
-            const float r1 = f - __uint_as_float(hi[b]);
+            // (nothing is left of an infinity: inf - inf would make its products NaN)
+            const float r1 = hi[b] == __float_as_uint(f) ? 0.f : f - __uint_as_float(hi[b]);
             mid[b] = __float_as_uint(r1) & 0xFFFF0000u;
             lo[b] = __float_as_uint(r1 - __uint_as_float(mid[b]));
           }

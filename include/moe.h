@@ -336,7 +336,9 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
  *     a selection can differ from moe_forward's where two logits are equal to
  *     within float32 rounding;
  *   - h and the expert outputs stay float32 (moe_forward rounds both to bf16),
- *     so y is rounded once;
+ *     so y is rounded once; an infinite h counts as one, while an infinite
+ *     weight of w_down can give NaN where moe_forward gives an infinity (h is
+ *     multiplied in three parts, and a part may be 0);
  *   - two calls with the same arguments give the same bits.
  */
 size_t moe_few_workspace_size(int T, int H, int I, int E, int k, int E_local);

@@ -129,3 +129,29 @@ def test_block_keeps_nonfinite_tokens_to_themselves(T, rdtype):
         assert torch.isnan(a[1]).all() and torch.isnan(a[T - 1]).all()
         a, b = a[others].float(), b[others].float()
         assert torch.isfinite(a).all() and float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
+
+
+@gpu
+@pytest.mark.parametrize("fn", ["moe_forward_few", "moe_forward_few_f32", "moe_forward"])
+@pytest.mark.parametrize("T,H,I,k", [(3, 72, 40, 2), (24, 256, 136, 4)])
+def test_few_infinite_h(fn, T, H, I, k):
+    """silu(g) u past the largest float32: every h of two tokens is an infinity,
+    and so is their y (all selections weighted by the bias alone, all products
+    of one sign: no 0 inf and no inf - inf). The experts in use stay the same,
+    and with them the order of the other tokens' sums."""
+    E = 4
+    g = _gen(4)
+    x = torch.rand((T, H), generator=g, device="cuda").to(BF)
+    wr, bias = torch.zeros((E, H), device="cuda"), torch.randn(E, generator=g, device="cuda")
+    gu, dn = (w.abs() for w in _bf16_weights(g, E, H, I))
+    print(f"[gpu] {fn} with infinite h T={T}", flush=True)
+    clean = [getattr(M, fn)(x, wr, bias, gu, d, k, 0)[0].clone() for d in (dn, -dn)]
+    x[1] *= 2.0 ** 70
+    x[2] *= 2.0 ** 100
+    up = getattr(M, fn)(x, wr, bias, gu, dn, k, 0)[0]
+    down = getattr(M, fn)(x, wr, bias, gu, -dn, k, 0)[0]
+    torch.cuda.synchronize()
+    assert torch.isposinf(up[1:3]).all() and torch.isneginf(down[1:3]).all()
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[1:3] = False
+    assert _same_bits(up[others], clean[0][others]) and _same_bits(down[others], clean[1][others])
