@@ -31,9 +31,10 @@
 // takes its own queue's gate/up items, then its down items, then its return
 // items. Waiting is safe however many workgroups run at a time and whatever
 // else the GPU runs: a gate/up item waits for nothing; a workgroup that has
-// waited for kSpins polls puts its item aside and takes what the other queues
-// still hold of the kinds before it, gate/up items first, so all items that
-// anybody waits for are with workgroups that are running.
+// waited for Args::polls polls (kFewPolls, some 2 ms) puts its item aside and
+// takes what the other queues still hold of the kinds before it, gate/up items
+// first, so all items that anybody waits for are with workgroups that are
+// running.
 //
 // Bound: HBM from some eight tokens on (DeepSeek-R1-shaped EP=8 share, 16
 // tokens, 1.13 GB of used experts: 198 us, the stream itself at 6 TB/s and
@@ -71,7 +72,6 @@ constexpr int kTokens = 8;      // tokens of a return item
 constexpr int kItems = 1024;    // items an operand is cut into where k allows (two per workgroup)
 constexpr int kQueues = 8;      // of each kind of item, one per XCD (workgroup b runs on XCD b % 8)
 constexpr int kPitch = 32;      // ints between counters: a 128-byte line each
-constexpr int kSpins = 4096;    // polls before a waiting workgroup looks for items (some 2 ms)
 constexpr int kCoherent = 16;   // buffer cache policy sc1: agent scope
 constexpr int kStream = 2;      // nt: each weight byte is read once
 constexpr uint32_t kOutside = 0x80000000u;  // offset past every buffer: reads zero
@@ -82,6 +82,7 @@ struct Args {
   const uint16_t* w_gate_up;
   const uint16_t* w_down;
   int T, H, I, E, k, e0, E_local, renormalize, y_f32;
+  int polls;  // before a waiting workgroup looks for items
   void* y;
   // counters, kPitch apart
   int* queue;     // [kind][queue]: items handed out
@@ -567,9 +568,9 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       }
     return make_int2(3, 0);
   };
-  // Polls until *c reaches n, at most kSpins times.
+  // Polls until *c reaches n, at most a.polls times.
   auto poll = [&](const int* c, int n) {
-    for (int i = 0; i < kSpins; ++i) {
+    for (int i = 0; i < a.polls; ++i) {
       if (peek(c) >= n) return true;
       __builtin_amdgcn_s_sleep(1);
     }
@@ -889,7 +890,7 @@ size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {
 
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                      void* y, bool y_f32, char* ws, hipStream_t stream) {
+                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream) {
   using namespace few;
   const Layout L = layout(T, H, I, E, k, E_local);
   float* logits = reinterpret_cast<float*>(ws + L.logits);
@@ -906,10 +907,13 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
     score(std::integral_constant<int, 8>{});
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), y, ctr, ctr + L.cnt_a,
-               ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
+  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), polls, y, ctr,
+               ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
                reinterpret_cast<float*>(ws + L.part_b), reinterpret_cast<float*>(ws + L.h)};
-  hipLaunchKernelGGL(T > 16 ? few_experts_kernel<true> : few_experts_kernel<false>, dim3(unsigned(2 * device_cu_count())), dim3(few::kThreads), 0, stream, a);
+  // (at least one workgroup per queue: return items are not taken from another's)
+  const int grid = std::max(kQueues, workgroups > 0 ? workgroups : 2 * device_cu_count());
+  hipLaunchKernelGGL(T > 16 ? few_experts_kernel<true> : few_experts_kernel<false>, dim3(unsigned(grid)),
+                     dim3(few::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

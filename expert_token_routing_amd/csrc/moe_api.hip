@@ -357,11 +357,12 @@ size_t moe_few_workspace_size(int T, int H, int I, int E, int k, int E_local) {
 
 static int few_impl(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
                     const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                    void* y, bool y_f32, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                    void* y, bool y_f32, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                    int workgroups = 0, int polls = kFewPolls) {
   int st = check_route_dims(T, H, E, k);
   if (st != MOE_OK) return st;
   if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
-  if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (I <= 0 || (I % 8) != 0 || workgroups < 0 || polls < 1) return MOE_ERR_INVALID_ARG;
   if (T > MOE_FEW_TOKENS || !expert_weights_fit(H, I) || !few_supported(T, H, I, k, E_local))
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -372,7 +373,7 @@ static int few_impl(const moe_bf16* x, const float* w_router, const float* bias,
       workspace_bytes < few_workspace_bytes(T, H, I, E, k, E_local))
     return MOE_ERR_WORKSPACE;
   return hip_status(launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, y_f32,
-                               static_cast<char*>(workspace), stream));
+                               workgroups, polls, static_cast<char*>(workspace), stream));
 }
 
 int moe_forward_few(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
@@ -387,6 +388,20 @@ int moe_forward_few_f32(const moe_bf16* x, const float* w_router, const float* b
                         int renormalize, float* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   return few_impl(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, true, workspace,
                   workspace_bytes, stream);
+}
+
+// moe_forward_few_f32 with another number of workgroups (at least 8; 0: two per
+// CU) and of polls before a waiting workgroup puts its item aside for others'
+// work. That work is there only where workgroups wait while queues still hold
+// earlier items, which two per CU hardly leave (at most 5 items of a call even
+// with one poll): the tests call this one with few workgroups, where up to 700
+// items of a call are taken that way. Not part of moe.h.
+int moe_internal_forward_few(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                             const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
+                             int renormalize, float* y, void* workspace, size_t workspace_bytes, int workgroups,
+                             int polls, hipStream_t stream) {
+  return few_impl(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, y, true, workspace,
+                  workspace_bytes, stream, workgroups, polls);
 }
 
 // Sizes of the 8-bit products: an exact int32 sum needs K < 2^17; 32-bit

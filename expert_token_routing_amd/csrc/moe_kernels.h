@@ -106,12 +106,15 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
                              const float* gate, int gate_kind, float scale, const float* w_next, float eps, int T,
                              int H, void* out, uint16_t* normed, hipStream_t stream);
 
-// The whole share for T <= 32 tokens in two kernels (few.hip).
+// The whole share for T <= 32 tokens in two kernels (few.hip). workgroups of the
+// second (0: two per CU), and polls: how often a waiting one looks before it
+// turns to other work. The results depend on neither.
+constexpr int kFewPolls = 4096;
 bool few_supported(int T, int H, int I, int k, int E_local);
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local);
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                      void* y, bool y_f32, char* ws, hipStream_t stream);
+                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream);
 
 // 8-bit integer products (gemm_i8.hip). Rows of x quantised with a scale each;
 // rows at and past *end (device memory; NULL: none) are left alone.

@@ -254,3 +254,55 @@ def test_few_two_calls_at_once():
     torch.cuda.synchronize()
     for y, r in ys:
         assert torch.equal(y.view(torch.int16), r.view(torch.int16))
+
+
+def _internal():
+    """moe_forward_few_f32 with its number of workgroups and of polls before a
+    waiting one turns to other work as arguments (an entry point for tests)."""
+    f = M.lib().moe_internal_forward_few
+    f.restype = ctypes.c_int
+    f.argtypes = M.SIGNATURES["moe_forward_few_f32"][1][:16] + [ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
+    return f
+
+
+def _few_with(workgroups, polls, a, k, e0, y, ws):
+    x, wr, _, _, dn = a
+    st = _internal()(*(t.data_ptr() if t is not None else None for t in a), x.shape[0], x.shape[1], dn.shape[1],
+                     wr.shape[0], k, e0, dn.shape[0], 1, y.data_ptr(), ws.data_ptr(), ws.numel(), workgroups, polls,
+                     torch.cuda.current_stream().cuda_stream)
+    M.check(st, "moe_internal_forward_few")
+
+
+@pytest.mark.parametrize("workgroups,polls", [(0, 0), (0, -1), (-1, 1)])
+def test_few_internal_rejects(workgroups, polls):
+    assert _internal()(FAKE, FAKE, None, FAKE, FAKE, 8, 8, 8, 4, 2, 0, 4, 1, FAKE, ctypes.c_void_p(0x100000), 1 << 30,
+                       workgroups, polls, None) == INV
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,E,k,e0,El", CASES + [(1, 7168, 256, 256, 8, 0, 256), (16, 2048, 1024, 64, 8, 16, 32)])
+@pytest.mark.parametrize("workgroups,polls", [(8, 1), (11, 2), (40, 1), (0, 1)])
+def test_few_items_put_aside(T, H, I, E, k, e0, El, workgroups, polls):
+    """Workgroups that find their own queues empty while others still hold items
+    put theirs aside and take those: with 11 workgroups on eight queues, up to
+    700 items of a call. The same bits, from a workspace of any contents, one call
+    after another and two side by side."""
+    a = _inputs(T, H, I, E, El, bias=True)
+    ref, ws = M.moe_forward_few_f32(*a, k, e0)
+    ws2 = torch.empty_like(ws)
+    ys = [torch.empty_like(ref) for _ in range(3)]
+    side = torch.cuda.Stream()
+    for i in range(2):
+        print(f"[gpu] few put aside {i} workgroups={workgroups} polls={polls} T={T} H={H} I={I} E={E}", flush=True)
+        ws.fill_(85 * i)
+        ws2.fill_(255 - 85 * i)
+        for y in ys:
+            y.fill_(float("nan"))
+        side.wait_stream(torch.cuda.current_stream())
+        _few_with(workgroups, polls, a, k, e0, ys[0], ws)
+        _few_with(workgroups, polls, a, k, e0, ys[1], ws)
+        with torch.cuda.stream(side):
+            _few_with(workgroups, polls, a, k, e0, ys[2], ws2)
+        torch.cuda.synchronize()
+        for y in ys:
+            assert torch.equal(y.view(torch.int32), ref.view(torch.int32))
