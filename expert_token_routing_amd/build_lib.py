@@ -5,7 +5,8 @@ Compiles every ``csrc/*.hip`` with hipcc in parallel and links one shared
 library next to this file; ``calib/*.hip`` (counter calibration,
 include/moe_calib.h) becomes ``libmoe_calib.so`` beside it, and
 ``csrc/calls.cpp``, the Python side of the small calls, the extension module
-``_calls.so`` (host compiler, against the installed torch). Always recompiles.
+``_calls.so`` (host compiler, against the installed torch; the two libraries are
+built whether or not that works). Always recompiles.
 """
 from __future__ import annotations
 
@@ -140,9 +141,6 @@ def build(verbose: bool = False, jobs: int | None = None) -> pathlib.Path:
     with ThreadPoolExecutor(jobs) as ex:
         calls = ex.submit(build_calls)
         list(ex.map(compile_one, zip(sources + calib, objs + calib_objs)))
-        if verbose and calls.result().strip():
-            print(calls.result())
-        calls.result()
     problems = []
     for src in sources + calib:
         for asm_file in BUILD.glob(src.stem + "-hip-amdgcn-amd-amdhsa-*.s"):
@@ -158,6 +156,18 @@ def build(verbose: bool = False, jobs: int | None = None) -> pathlib.Path:
         tmp = lib.with_suffix(".so.tmp")
         _run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), *map(str, lib_objs)])
         os.replace(tmp, lib)
+    # the C library needs neither torch nor a host compiler and is there by now
+    try:
+        out = calls.result()
+    except Exception as e:
+        CALLS.unlink(missing_ok=True)  # one of an earlier build may not fit this library
+        if isinstance(e, ModuleNotFoundError):
+            print(f"{CALLS.name} is not built: {e} (nothing can load it without torch)", file=sys.stderr)
+        else:
+            raise RuntimeError(f"{LIB} is built, {CALLS.name} is not (the Python binding's small calls need it)") from e
+    else:
+        if verbose and out.strip():
+            print(out)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -1,6 +1,8 @@
 """Host-side logic of the tests themselves (CPU only): the replica of the
 panel GEMM's row-block split that the full-size parity tests use to place
-their sampled rows on block edges."""
+their sampled rows on block edges; and of the build."""
+import pytest
+
 from tests.gpu_helpers import PANEL_ROW_CAPS, panel_blocks
 
 
@@ -52,3 +54,41 @@ def test_sgpr_hazard_scan():
     assert vmem_sgpr_hazards(five) == []
     four = "\n\t".join(["v_readlane_b32 s1, v253, 2"] + ["s_add_i32 s2, s2, 1"] * 4 + [load])
     assert len(vmem_sgpr_hazards(four)) == 1
+
+
+def _build_in(tmp_path, monkeypatch, calls):
+    """build() into tmp_path, every compiler run replaced by an empty output
+    file and the extension module's build by ``calls``."""
+    from expert_token_routing_amd import build_lib as B
+
+    def run(cmd):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return ""
+    for name in ("LIB", "CALIB_LIB", "CALLS"):
+        monkeypatch.setattr(B, name, tmp_path / getattr(B, name).name)
+    monkeypatch.setattr(B, "BUILD", tmp_path / "build")
+    monkeypatch.setattr(B, "_run", run)
+    monkeypatch.setattr(B, "build_calls", calls)
+    return B
+
+
+def test_build_links_the_library_without_the_extension_module(tmp_path, monkeypatch, capsys):
+    """The C library needs no torch and no host compiler: it is linked where the
+    Python extension cannot be built, which is then reported, and no extension
+    of an earlier build is left beside the new library."""
+    def failing(error):
+        def calls():
+            raise error
+        return calls
+    B = _build_in(tmp_path, monkeypatch, failing(RuntimeError("no C++ compiler found")))
+    B.CALLS.write_text("old")
+    with pytest.raises(RuntimeError, match="_calls.so is not"):
+        B.build()
+    assert B.LIB.exists() and B.CALIB_LIB.exists() and not B.CALLS.exists()
+    for f in (B.LIB, B.CALIB_LIB):
+        f.unlink()
+    monkeypatch.setattr(B, "build_calls", failing(ModuleNotFoundError("No module named 'torch'")))
+    assert B.build() == B.LIB
+    assert B.LIB.exists() and "without torch" in capsys.readouterr().err
+    monkeypatch.setattr(B, "build_calls", lambda: "")
+    assert B.build() == B.LIB
