@@ -12,6 +12,7 @@ import ctypes
 import functools
 import numbers
 import pathlib
+import sys
 from ctypes import c_float, c_int, c_int64, c_size_t, c_void_p
 
 LIB_PATH = pathlib.Path(__file__).resolve().parent / "libmoe.so"
@@ -101,6 +102,13 @@ def lib() -> ctypes.CDLL:
 _calls_module = None
 
 
+def torch_identity() -> str:
+    """The torch and the interpreter that _calls.so has to be built for: it uses
+    torch's C++ ABI and both's object layouts."""
+    torch = _torch()
+    return f"torch {torch.__version__} {torch.version.git_version} {sys.implementation.cache_tag}"
+
+
 def _calls():
     """The extension module behind the small calls (csrc/calls.cpp), which
     calls the library loaded here."""
@@ -108,11 +116,14 @@ def _calls():
     if _calls_module is None:
         L = lib()
         _torch()  # its libraries first
+        how = "build it with `python -m expert_token_routing_amd.build_lib`; there is no fallback path"
         try:
             from . import _calls as module
         except ImportError as e:
-            raise RuntimeError("_calls.so is missing or was built for another torch: build it with "
-                               "`python -m expert_token_routing_amd.build_lib`; there is no fallback path") from e
+            raise RuntimeError(f"_calls.so is missing or was built for another torch: {how}") from e
+        built_for = getattr(module, "built_for", "an unnamed torch")
+        if built_for != torch_identity():
+            raise RuntimeError(f"_calls.so was built for {built_for}, this is {torch_identity()}: {how}")
         module.bind(*(ctypes.cast(getattr(L, n), c_void_p).value
                       for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8",
                                 "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8", "moe_few_workspace_size",

@@ -60,12 +60,14 @@ def build_calls() -> str:
     """csrc/calls.cpp -> _calls.so; torch's own libraries are in the process
     before it is loaded."""
     import torch
+    from ._binding import torch_identity
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("no C++ compiler found (needed to build _calls.so)")
     torch_dir = pathlib.Path(torch.__file__).resolve().parent
     tmp = CALLS.with_suffix(".so.tmp")
     out = _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+                f'-DMOE_BUILT_FOR="{torch_identity()}"',
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{ROOT / 'include'}",
                 f"-I{sysconfig.get_paths()['include']}", "-isystem", torch_dir / "include",
                 "-isystem", torch_dir / "include/torch/csrc/api/include",

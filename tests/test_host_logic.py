@@ -92,3 +92,23 @@ def test_build_links_the_library_without_the_extension_module(tmp_path, monkeypa
     assert B.LIB.exists() and "without torch" in capsys.readouterr().err
     monkeypatch.setattr(B, "build_calls", lambda: "")
     assert B.build() == B.LIB
+
+
+def test_extension_module_of_another_torch_is_refused(monkeypatch):
+    """It would load where its symbols happen to resolve, and then read torch's
+    objects by another layout."""
+    import types
+
+    import expert_token_routing_amd as M
+    from expert_token_routing_amd import _binding as B
+    B._calls()
+    from expert_token_routing_amd import _calls as module
+    assert module.built_for == B.torch_identity()
+    bound = []
+    for fake in (types.SimpleNamespace(bind=lambda *a: bound.append(a)),
+                 types.SimpleNamespace(bind=lambda *a: bound.append(a), built_for="torch 2.9.1 0123abc cpython-310")):
+        monkeypatch.setattr(M, "_calls", fake)
+        monkeypatch.setattr(B, "_calls_module", None)
+        with pytest.raises(RuntimeError, match="was built for .*build_lib"):
+            B._calls()
+    assert not bound
