@@ -51,6 +51,7 @@
 #include "gemm_dma.h"
 #include "gemm_tile.h"
 #include "moe_kernels.h"
+#include "moe_row.h"
 
 #include <utility>
 

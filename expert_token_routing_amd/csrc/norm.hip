@@ -17,7 +17,7 @@
 // them again from L2) and the next row's loads are issued before the current
 // row's reductions. 16384 x 7168 with a float32 y: 200 us, 5.9 TB/s.
 #include "moe_kernels.h"
-#include "moe_device.h"
+#include "moe_row.h"
 
 namespace moe {
 namespace norm {

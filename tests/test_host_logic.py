@@ -112,3 +112,13 @@ def test_extension_module_of_another_torch_is_refused(monkeypatch):
         with pytest.raises(RuntimeError, match="was built for .*build_lib"):
             B._calls()
     assert not bound
+
+
+def test_recorded_gemm_traffic_belongs_to_the_sources():
+    """The benchmark reports the gate/up GEMM's measured HBM bytes only while the
+    GEMM's sources are those that were profiled. A change to one of them needs
+    its counters retaken with it; helpers that the GEMM does not use belong in
+    another header."""
+    import bench
+    nbytes, note = bench.recorded_gemm1_traffic()
+    assert nbytes is not None and nbytes > 0, note
