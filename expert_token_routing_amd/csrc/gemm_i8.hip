@@ -726,10 +726,12 @@ __device__ __forceinline__ void load8(float (&o)[8], const void* base, int64_t v
 
 // One workgroup per row: its NV vectors of 8 per thread are read once and kept
 // (NV = 0: a row wider than 4 vectors of 1024 threads is read twice). Rows at
-// and past *end (device memory; NULL: none) are left alone.
+// and past *end (device memory; NULL: none) are left alone, and not read either,
+// but for `ahead`, a call of few rows, where the first row is asked for before
+// *end arrives.
 template <bool F32, int NV>
 __global__ void __launch_bounds__(1024) quantize_rows_kernel(const void* x, const int32_t* end, int M, int nvec,
-                                                             int8_t* q, float* scale) {
+                                                             bool ahead, int8_t* q, float* scale) {
   __shared__ uint32_t s_red[16];
   constexpr int kKeep = NV ? NV : 1;
   float v[kKeep][8];
@@ -741,8 +743,9 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const void* x, cons
     }
   };
   int64_t m = blockIdx.x;
-  load_row(m);  // (m < M: in the array even if it lies past *end, which is still on its way)
+  if (ahead) load_row(m);  // (m < M: in the array even if it lies past *end)
   const int64_t rows = end != nullptr ? min(M, *end) : M;
+  if (!ahead && m < rows) load_row(m);
   while (m < rows) {
     uint32_t top = 0;
     if constexpr (NV > 0) {
@@ -790,17 +793,24 @@ hipError_t launch_quantize(const void* x, const int32_t* end, int64_t M, int K, 
   // one vector per thread for few rows (the shortest chain), two up to 1024
   // vectors for many, so that several rows share a CU
   const bool many = M > 2 * device_cu_count();
+  // Of a large capacity's rows most can lie past *end, so none is asked for ahead
+  // and the workgroups are 16 per CU, not one per row (MLPs, us, with both / with
+  // a workgroup per row / with its row asked for ahead too: 16 rows of 65536, 32
+  // experts of 4096 x 4096: 225 / 249 / 464; 16384 rows of 131072, 7168 x 2048:
+  // 800 / 854 / 1187; all 16384 rows there: 802 / 804 / 805).
+  const bool bounded = end != nullptr && many, ahead = !bounded;
   const int nv = nvec <= (many ? 256 : 1024) ? 1 : nvec <= 1024 ? 2 : nvec <= 4096 ? 4 : 0;
   const int nt = nv ? int(ceil_div(ceil_div(nvec, nv), 64) * 64) : 1024;
-  const dim3 grid(unsigned(std::min<int64_t>(M, kMaxGrid))), block(static_cast<unsigned>(nt));
+  const dim3 grid(unsigned(std::min<int64_t>(M, bounded ? 16 * device_cu_count() : kMaxGrid)));
+  const dim3 block(static_cast<unsigned>(nt));
   if (nv == 1)
-    hipLaunchKernelGGL((quantize_rows_kernel<F32, 1>), grid, block, 0, stream, x, end, int(M), nvec, q, scale);
+    hipLaunchKernelGGL((quantize_rows_kernel<F32, 1>), grid, block, 0, stream, x, end, int(M), nvec, ahead, q, scale);
   else if (nv == 2)
-    hipLaunchKernelGGL((quantize_rows_kernel<F32, 2>), grid, block, 0, stream, x, end, int(M), nvec, q, scale);
+    hipLaunchKernelGGL((quantize_rows_kernel<F32, 2>), grid, block, 0, stream, x, end, int(M), nvec, ahead, q, scale);
   else if (nv == 4)
-    hipLaunchKernelGGL((quantize_rows_kernel<F32, 4>), grid, block, 0, stream, x, end, int(M), nvec, q, scale);
+    hipLaunchKernelGGL((quantize_rows_kernel<F32, 4>), grid, block, 0, stream, x, end, int(M), nvec, ahead, q, scale);
   else
-    hipLaunchKernelGGL((quantize_rows_kernel<F32, 0>), grid, block, 0, stream, x, end, int(M), nvec, q, scale);
+    hipLaunchKernelGGL((quantize_rows_kernel<F32, 0>), grid, block, 0, stream, x, end, int(M), nvec, ahead, q, scale);
   return hipGetLastError();
 }
 

@@ -341,6 +341,34 @@ def test_expert_ffn_i8(segs, H, I, behind):
 
 
 @gpu
+def test_expert_ffn_i8_does_not_read_the_rows_that_are_not_there():
+    """16 rows in buffers for 98304, as dispatch leaves them: a call takes less
+    time than reading the other rows of x_perm and h (2.4 GB) at HBM's peak of
+    8 TB/s would take."""
+    cap, rows, H, I = 98304, 16, 4096, 4096
+    x = torch.zeros((cap, H), dtype=BF, device="cuda")
+    x[:rows] = torch.randn((rows, H), generator=_gen(8), device="cuda").to(BF)
+    w = _weights(_gen(9), 1, H, I)
+    off = torch.tensor([0, rows], device="cuda", dtype=torch.int32)
+    print(f"[gpu] expert_ffn_i8 rows={rows} capacity={cap}", flush=True)
+    out, ws = M.moe_expert_ffn_i8(x, off, *w)
+    few, _ = M.moe_expert_ffn_i8(x[:rows], off, *w)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:rows].view(torch.int16), few.view(torch.int16))
+    best = float("inf")
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(10):
+            M.moe_expert_ffn_i8(x, off, *w, out=out, workspace=ws)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / 10)
+    limit = (cap - rows) * (2 * H + 4 * I) / 8e12 * 1e3
+    assert best < limit, f"{best * 1e3:.0f} us, reading the other rows alone takes {limit * 1e3:.0f}"
+
+
+@gpu
 def test_expert_ffn_i8_h_to_the_nearest():
     """Every one of 33.5 million float32 h's next to its row's largest: 127 h / top
     in 64 bits is on the same side of each half as the quotient of the two
