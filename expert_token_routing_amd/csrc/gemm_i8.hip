@@ -571,11 +571,62 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
   }
 }
 
+// Which tiles a launch takes (names as the shapes above; 16, 32, 64: rows of a
+// block), by its sizes and the rows a segment is expected to hold.
+enum Tile { kStream16, kStream32, kStream64, kNarrow, kNarrow32, kNarrow64, kSmall, kMid64, kMid, kMidK, kMid2, kBig };
+
+Tile pick_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int64_t rows_hint, int64_t cus) {
+  const int d = swiglu ? 2 : 1;  // channels of an output
+  // segments that can have rows
+  const int64_t active = std::min<int64_t>(E_local, capacity);
+  auto tiles = [&](int bm, int outputs) { return ceil_div(rows_hint, bm) * active * ceil_div(N, outputs); };
+  // Ragged segments spread around the expected length: twice as many rows as
+  // expected still make one block, and a block in two is a segment's last.
+  const int64_t rows = std::min(ragged ? 2 * rows_hint : rows_hint, capacity);
+  auto blocks = [&](int bm) {
+    const int64_t tall = std::min(ragged ? rows_hint + rows_hint / 4 : rows_hint, capacity);
+    return std::min(ceil_div(tall, bm) * active, ceil_div(rows_hint * active, bm) + active / 2);
+  };
+  // Streams from the first narrow tile (32 outputs) beyond one per CU: a second
+  // round of those costs more (us, narrow / stream: 16 experts of 2880 x 768, 61
+  // rows 34.4 / 31.2; 5 rows 8.1 / 5.3; 1 x 7168 x 10240 16.7 / 14.3; 17 x 2048 x
+  // 16384 14.0 / 8.5).
+  const bool streams = E_local <= kStreamLocal;
+  if (rows <= 16 && streams && tiles(16, 32) > cus) return kStream16;
+  if (rows <= 32 && streams && tiles(32, 32) > cus) return kStream32;
+  // blocks of 16 rows also for 17 to 32: twice the tiles, and both blocks of a
+  // weight tile read it at the same time (32 x 7168 x 4096: 10.7 -> 8.6 us; two
+  // rounds of them, 17 x 7168 x 8192: 14.2, streams 17.1)
+  if (rows <= 32) return kNarrow;
+  if (rows <= 64 && streams && tiles(64, 64 / d) > cus) return kStream64;
+  // The smallest tiles of which each CU gets one at most. (us: 64 x 7168 x 4096
+  // Narrow 14.1, Narrow32 11.0, Narrow64 13.6, Small 17.8; 128 x 7168 x 4096 25.3,
+  // 18.5, 14.3, 17.7; 128 x 7168 x 1024 8.4, 10.2, 13.8, 16.8; 512 rows 1408 x 2048
+  // Small 7.7, Mid64 9.4; 640 rows Small 11.6, Mid64 9.5; 512 rows 7168 x 4096
+  // Small 34, Mid64 28, Mid 35; 1024 rows MidK 37; 1280 rows 768 x 2048 Mid 8.7,
+  // MidK 9.8.)
+  auto once = [&](int bm, int outputs) { return blocks(bm) * ceil_div(N, outputs) <= cus; };
+  if (once(16, 32)) return kNarrow;
+  if (once(32, 32)) return kNarrow32;
+  if (!swiglu && once(64, 32)) return kNarrow64;
+  if (once(64, 64 / d)) return kSmall;
+  if (once(64, 128 / d)) return kMid64;
+  // The largest tiles read the fewest operand bytes, but one at a time per CU:
+  // they need rows to fill them and a long k, or very many tiles. (us, Mid2 / Big,
+  // 32 experts, K x N: 96 rows 7168 x 4096 192 / 214, 128 rows 273 / 221, 512 rows
+  // 595 / 447; 2880 x 2880 68 / 88, 99 / 91, 227 / 167; 1408 x 2048 22 / 33,
+  // 32 / 34, 66 / 70; 64 experts 1408 x 2048, 512 rows: 156 / 142.)
+  const int64_t mid = blocks(128) * ceil_div(N, 128 / d);
+  if (rows_hint >= 128 && mid > 2 * cus && (K >= 2048 || mid * K >= (int64_t(5) << 20))) return kBig;
+  // (2048 x 7168 x 4096: Mid 75 us, Mid2 56, Big 58; 1024 x 7168 x 4096: Mid 38, Mid2 40)
+  if (mid > cus) return kMid2;
+  return K > 2048 ? kMidK : kMid;
+}
+
 template <bool SWIGLU>
 hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream) {
   const bool tail = p.K % kRowB != 0;
   const int64_t cus = device_cu_count() / 8 * 8;
-  auto tiles = [&](int bm, int cols) { return ceil_div(rows_hint, bm) * p.E_local * ceil_div(p.N, cols); };
   constexpr int d = SWIGLU ? 2 : 1;
   auto go = [&](auto shape, auto fm_t, auto maxe_t, int bm, int per_cu) {
     typedef decltype(shape) T;
@@ -590,61 +641,29 @@ hipError_t launch_gemm(const GemmArgs& p, int64_t rows_hint, hipStream_t stream)
   };
   typedef std::integral_constant<int, kMaxLocal> AnyE;
   typedef std::integral_constant<int, kStreamLocal> StreamE;
-  // Ragged segments spread around the expected length: twice as many rows as
-  // expected still make one block, and a block in two is a segment's last.
-  const int64_t rows = std::min(p.offsets ? 2 * rows_hint : rows_hint, p.capacity);
-  auto blocks = [&](int bm) {
-    const int64_t tall = std::min(p.offsets ? rows_hint + rows_hint / 4 : rows_hint, p.capacity);
-    return std::min(ceil_div(tall, bm) * p.E_local, ceil_div(rows_hint * p.E_local, bm) + p.E_local / 2);
-  };
-  // Streams from the first tile beyond one per CU: a second round of narrow
-  // tiles costs more (16 experts of 2880 x 768, 61 rows: 34.4 us narrow, 31.2 us).
-  const bool streams = p.E_local <= kStreamLocal;
-  if (rows <= 16 && streams && tiles(16, 64 / d) > cus)
-    return go(Stream{}, std::integral_constant<int, 1>{}, StreamE{}, 16, 2);
-  if (rows <= 32 && streams && tiles(32, 64 / d) > cus)
-    return go(Stream{}, std::integral_constant<int, 2>{}, StreamE{}, 32, 2);
-  if (rows <= 32) {
-    // blocks of 16 rows also for 17 to 32: twice the tiles, and both blocks of a
-    // weight tile read it at the same time (32 x 7168 x 4096: 10.7 -> 8.6 us)
-    if constexpr (SWIGLU)
-      return go(NarrowGU{}, std::integral_constant<int, 1>{}, AnyE{}, 16, 1);
-    else
-      return go(Narrow{}, std::integral_constant<int, 1>{}, AnyE{}, 16, 1);
-  }
-  if (rows <= 64 && streams && tiles(64, 64 / d) > cus)
-    return go(Stream64{}, std::integral_constant<int, 4>{}, StreamE{}, 64, 2);
-  // The smallest tiles of which each CU gets one at most. (us: 64 x 7168 x 4096
-  // Narrow 14.1, Narrow32 11.0, Narrow64 13.6, Small 17.8; 128 x 7168 x 4096 25.3,
-  // 18.5, 14.3, 17.7; 128 x 7168 x 1024 8.4, 10.2, 13.8, 16.8; 512 rows 1408 x 2048
-  // Small 7.7, Mid64 9.4; 640 rows Small 11.6, Mid64 9.5; 512 rows 7168 x 4096
-  // Small 34, Mid64 28, Mid 35; 1024 rows MidK 37; 1280 rows 768 x 2048 Mid 8.7,
-  // MidK 9.8.)
   typedef std::integral_constant<int, 1> One;
   typedef std::integral_constant<int, 2> Two;
-  auto once = [&](int bm, int outputs) { return blocks(bm) * ceil_div(p.N, outputs) <= cus; };
-  if constexpr (SWIGLU) {
-    if (once(16, 32)) return go(NarrowGU{}, One{}, AnyE{}, 16, 1);
-    if (once(32, 32)) return go(NarrowGU{}, Two{}, AnyE{}, 32, 1);
-  } else {
-    if (once(16, 32)) return go(Narrow{}, One{}, AnyE{}, 16, 1);
-    if (once(32, 32)) return go(Narrow32{}, Two{}, AnyE{}, 32, 1);
-    if (once(64, 32)) return go(Narrow64{}, Two{}, AnyE{}, 64, 1);
+  typedef std::integral_constant<int, 4> Four;
+  typedef std::integral_constant<int, kSmallFM> SmallFM;
+  typedef std::integral_constant<int, kMidFM> MidFM;
+  typedef std::conditional_t<SWIGLU, NarrowGU, Narrow> Narrow16;
+  switch (pick_tile(SWIGLU, p.offsets != nullptr, p.E_local, p.capacity, p.N, p.K, rows_hint, cus)) {
+    case kStream16: return go(Stream{}, One{}, StreamE{}, 16, 2);
+    case kStream32: return go(Stream{}, Two{}, StreamE{}, 32, 2);
+    case kStream64: return go(Stream64{}, Four{}, StreamE{}, 64, 2);
+    case kNarrow: return go(Narrow16{}, One{}, AnyE{}, 16, 1);
+    case kNarrow32: return go(std::conditional_t<SWIGLU, NarrowGU, Narrow32>{}, Two{}, AnyE{}, 32, 1);
+    case kNarrow64:
+      if constexpr (!SWIGLU) return go(Narrow64{}, Two{}, AnyE{}, 64, 1);
+      return hipErrorInvalidValue;
+    case kSmall: return go(Small{}, SmallFM{}, AnyE{}, 64, 1);
+    case kMid64: return go(Mid64{}, SmallFM{}, AnyE{}, 64, 1);
+    case kMid: return go(Mid{}, MidFM{}, AnyE{}, 128, 1);
+    case kMidK: return go(MidK{}, MidFM{}, AnyE{}, 128, 1);
+    case kMid2: return go(Mid2{}, MidFM{}, AnyE{}, 128, 2);
+    case kBig: return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
   }
-  if (once(64, 64 / d)) return go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
-  if (once(64, 128 / d)) return go(Mid64{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1);
-  // The largest tiles read the fewest operand bytes, but one at a time per CU:
-  // they need rows to fill them and a long k, or very many tiles. (us, Mid2 / Big,
-  // 32 experts, K x N: 96 rows 7168 x 4096 192 / 214, 128 rows 273 / 221, 512 rows
-  // 595 / 447; 2880 x 2880 68 / 88, 99 / 91, 227 / 167; 1408 x 2048 22 / 33,
-  // 32 / 34, 66 / 70; 64 experts 1408 x 2048, 512 rows: 156 / 142.)
-  const int64_t mid = blocks(128) * ceil_div(p.N, 128 / d);
-  if (rows_hint >= 128 && mid > 2 * cus && (p.K >= 2048 || mid * p.K >= (int64_t(5) << 20)))
-    return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
-  // (2048 x 7168 x 4096: Mid 75 us, Mid2 56, Big 58; 1024 x 7168 x 4096: Mid 38, Mid2 40)
-  if (mid > cus) return go(Mid2{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 2);
-  if (p.K > 2048) return go(MidK{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
-  return go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1);
+  return hipErrorInvalidValue;
 }
 
 // ---------------------------------------------------------------------------
@@ -871,6 +890,10 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const uint16_t* w
 }
 
 }  // namespace i8
+
+int i8_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int64_t rows_hint, int cus) {
+  return int(i8::pick_tile(swiglu, ragged, E_local, capacity, N, K, rows_hint, cus));
+}
 
 hipError_t launch_quantize_rows(const void* x, bool x_f32, const int32_t* end, int64_t M, int K, int8_t* q,
                                 float* scale, hipStream_t stream) {

@@ -532,6 +532,12 @@ static ForwardI8Layout forward_i8_layout(int T, int H, int I, int E, int k, int 
 
 extern "C" {
 
+// The tiles of a product, for the tests of the rule. Not part of moe.h.
+int moe_internal_i8_tile(int swiglu, int ragged, int E_local, int64_t capacity, int N, int K, int64_t rows_hint,
+                         int cus) {
+  return i8_tile(swiglu != 0, ragged != 0, E_local, capacity, N, K, rows_hint, cus);
+}
+
 size_t moe_expert_ffn_i8_workspace_size(int H, int I, int64_t capacity) {
   if (H <= 0 || I <= 0 || capacity < 0) return 0;
   return ffn_i8_layout(0, capacity, capacity, H, I).total;

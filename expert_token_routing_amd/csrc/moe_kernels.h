@@ -129,6 +129,9 @@ hipError_t launch_quantize_weights(const uint16_t* w, int E_local, int K, int N,
 hipError_t launch_gemm_i8(const int8_t* A, const float* sa, const int32_t* offsets, int E_local, int64_t capacity,
                           const int8_t* W, const float* sw, int K, int N, uint16_t* C, int64_t rows_hint,
                           hipStream_t stream);
+// The tiles that a product takes on a device of `cus` CUs (an i8::Tile); ragged:
+// segments by offsets.
+int i8_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int64_t rows_hint, int cus);
 // h [capacity, I] float32 = silu(gate) * up, W [E_local, 2 I, H]; row n of a
 // segment is row gather_src[n] / gather_k of A when gather_src is given.
 hipError_t launch_gate_up_i8(const int8_t* A, const float* sa, const int32_t* gather_src, int gather_k,

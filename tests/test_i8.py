@@ -117,6 +117,36 @@ def test_i8_reject_mismatched_tensors():
         M.moe_forward_i8(x, torch.zeros(4, 32), None, w, sw, dn, sd, 2, 3)
 
 
+STREAM16, STREAM32, STREAM64, NARROW, NARROW32, NARROW64, SMALL, MID64, MID, MIDK, MID2, BIG = range(12)
+
+
+def _tile(swiglu, ragged, E, cap, N, K, hint, cus=256):
+    f = M.lib().moe_internal_i8_tile
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                  ctypes.c_int]
+    return f(swiglu, ragged, E, cap, N, K, hint, cus)
+
+
+@pytest.mark.parametrize("swiglu,N,K", [(1, 2048, 7168), (0, 7168, 2048), (1, 768, 2880), (0, 2880, 768), (1, 256, 7168)])
+@pytest.mark.parametrize("E,rows", [(32, 1), (256, 1), (256, 3), (1024, 8), (32, 16)])
+def test_i8_tiles_count_segments_that_can_have_rows(swiglu, N, K, E, rows):
+    """Experts beyond the number of rows are empty: they do not change the tiles."""
+    if E <= 256:
+        assert _tile(swiglu, 1, E, rows, N, K, 1) == _tile(swiglu, 1, rows, rows, N, K, 1)
+    want = STREAM16 if rows * -(-N // 32) > 256 and E <= 256 else NARROW
+    assert _tile(swiglu, 1, E, rows, N, K, 1) == want
+
+
+@pytest.mark.parametrize("rows,N,want", [
+    (1, 8192, NARROW), (1, 8200, STREAM16), (16, 16384, STREAM16), (1, 16392, STREAM16),
+    (17, 8192, NARROW), (17, 8200, STREAM32), (32, 16384, STREAM32), (33, 1024, NARROW), (64, 4096, NARROW32)])
+def test_i8_narrow_tiles_make_one_round(rows, N, want):
+    """Narrow tiles hold 32 channels: up to one per CU, streams beyond (blocks
+    of 32 rows for 17 rows and more)."""
+    assert _tile(0, 0, 1, rows, N, 2048, rows) == want
+
+
 # --------------------------------------------------------------------------- #
 # The kernels (GPU)                                                            #
 # --------------------------------------------------------------------------- #
@@ -338,6 +368,21 @@ def test_expert_ffn_i8(segs, H, I, behind):
         _close(out[s], (hq[s].to(F64) @ dnq[e].to(F64).T) * hs[s, None].to(F64) * dns[e].to(F64), REL, f"out {e}")
         at += m
     assert out[n:].eq(7.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("segs", [[0] * 7 + [1] + [0] * 24, [1] + [0] * 31, [0] * 31 + [1], [0, 2] + [0] * 10 + [1] * 3 + [0] * 17,
+                                  [0] * 250 + [1] + [0] * 4 + [1]], ids=["one", "first", "last", "five", "two_of_256"])
+@pytest.mark.parametrize("H,I,behind", [(272, 1040, 0), (2880, 768, 0), (1024, 2048, 3)])
+def test_expert_ffn_i8_more_experts_than_rows(segs, H, I, behind):
+    test_expert_ffn_i8(segs, H, I, behind)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 16, 17, 32])
+@pytest.mark.parametrize("N", [8192, 8200, 16384])
+def test_gemm_i8_many_channels(rows, N):
+    _check_gemm(rows, 528, N)
 
 
 @gpu
