@@ -121,8 +121,12 @@ extern "C" {
 const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "MOE_OK";
-    case MOE_ERR_INVALID_ARG: return "MOE_ERR_INVALID_ARG: invalid size, index range or null pointer";
-    case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED: outside the supported sizes (E <= 1024, k <= 32, T*k < 2^31, H*I < 2^29)";
+    case MOE_ERR_INVALID_ARG:
+      return "MOE_ERR_INVALID_ARG: invalid size, value or index range, or a null or misaligned pointer";
+    case MOE_ERR_UNSUPPORTED:
+      return "MOE_ERR_UNSUPPORTED: outside the supported sizes (E <= 1024, k <= 32, T*k < 2^31, H*I < 2^29; "
+             "moe_forward_few: T <= 32; 8-bit products: K < 131072, N*K < 2^31; norms: H <= 32768; "
+             "the others stand at the entry point's declaration in moe.h)";
     case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace missing, misaligned or too small";
     case MOE_ERR_HIP: return "MOE_ERR_HIP: a HIP launch failed";
     default: return "unknown moe_status";

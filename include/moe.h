@@ -55,7 +55,8 @@ extern "C" {
 typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = -1, /* a size, index range or required pointer is wrong */
-  MOE_ERR_UNSUPPORTED = -2, /* valid problem outside the supported envelope (E > 1024, k > 32, ...) */
+  MOE_ERR_UNSUPPORTED = -2, /* valid problem outside the supported envelope (E > 1024, k > 32, ...; each
+                               entry point's declaration states its own) */
   MOE_ERR_WORKSPACE = -3,   /* workspace missing or smaller than the *_workspace_size result */
   MOE_ERR_HIP = -4          /* a HIP runtime call or kernel launch failed */
 } moe_status;

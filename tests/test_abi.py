@@ -61,6 +61,18 @@ def test_status_strings():
     assert "unknown" in M.status_string(12345)
 
 
+def test_unsupported_sizes_are_named():
+    """The message of a refusal states the limit that the call broke."""
+    L, ws = M.lib(), ctypes.c_void_p(0x100000)
+    for st, limit in (
+            (L.moe_forward_few(FAKE, FAKE, None, FAKE, FAKE, 33, 8, 8, 4, 2, 0, 4, 1, FAKE, ws, 1 << 30, None), "T <= 32"),
+            (L.moe_norm_pre(FAKE, 1, FAKE, 1e-6, 4, 40000, FAKE, None), "H <= 32768"),
+            (L.moe_quantize_weights(FAKE, 1, 131072, 8, FAKE, FAKE, None), "K < 131072"),
+            (L.moe_gemm_i8(FAKE, FAKE, None, FAKE, FAKE, 4, 32768, 65536, 1, FAKE, None), r"N*K < 2^31"),
+            (L.moe_route(FAKE, FAKE, None, 4, 8, 2000, 2, 1, FAKE, FAKE, FAKE, ws, 1 << 30, None), "E <= 1024")):
+        assert st == M.MOE_ERR_UNSUPPORTED and limit in M.status_string(st)
+
+
 def test_workspace_sizes():
     L = M.lib()
     assert L.moe_route_workspace_size(16384, 7168, 256, 8) >= 3 * 256 * 7168 * 2
