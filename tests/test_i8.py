@@ -289,6 +289,45 @@ def test_gemm_i8_segments(segs, K, N, behind):
     _check_gemm(sum(segs) + behind, K, N, segs)
 
 
+OFFSETS_SHAPES = [(9, 272, 264, NARROW), (16, 272, 16392, STREAM16), (30, 272, 16392, STREAM32),
+                  (60, 272, 16392, STREAM64), (64, 272, 2056, NARROW32), (100, 272, 2056, NARROW64),
+                  (300, 272, 2056, SMALL), (300, 272, 4104, MID64), (700, 272, 4104, MID), (700, 2064, 4104, MIDK),
+                  (2049, 272, 4096, MID2), (4000, 2064, 4104, BIG)]
+
+
+@gpu
+@pytest.mark.parametrize("cap,K,N,tile", OFFSETS_SHAPES)
+@pytest.mark.parametrize("E", [1, 3])
+def test_gemm_i8_offsets(cap, K, N, tile, E):
+    """Device offsets of one matrix (no segment tables) and of three: shorter
+    than the capacity, starting past 0, ending past the capacity and before 0
+    (both clamped), descending (an empty segment). The host picks the tiles from
+    the capacity; rows outside the segments stay as they are."""
+    if E == 1:
+        assert _tile(0, 1, E, cap, N, K, cap) == tile
+    g = _gen(10)
+    a, w = _rand_i8(g, cap, K), _rand_i8(g, E, N, K)
+    sa, sw = torch.rand(cap, generator=g, device="cuda") + 0.01, torch.rand((E, N), generator=g, device="cuda") + 0.01
+    third, most = cap // 3, cap - 1
+    lists = ([[0, most], [third, cap], [most, cap + 1000], [-5, third], [cap, cap], [cap + 3, cap + 9], [third, 0], [0, 1]]
+             if E == 1 else
+             [[0, 1, 1, most], [third, third + 1, most, cap], [0, third, cap + 9, cap + 70], [-3, 0, third, third + 1],
+              [third, third, 1, 1]])
+    refs = [(a.to(F64) @ w[e].to(F64).T) * sa[:, None].to(F64) * sw[e].to(F64) for e in range(E)]
+    for off in lists:
+        out = torch.full((cap, N), 7.0, dtype=BF, device="cuda")
+        print(f"[gpu] gemm_i8 capacity={cap} K={K} N={N} offsets={off}", flush=True)
+        M.moe_gemm_i8(a, sa, w, sw, torch.tensor(off, dtype=torch.int32, device="cuda"), out=out)
+        torch.cuda.synchronize()
+        inside = torch.zeros(cap, dtype=torch.bool, device="cuda")
+        for e in range(E):
+            lo, hi = (min(max(v, 0), cap) for v in off[e:e + 2])
+            if lo < hi:
+                _close(out[lo:hi], refs[e][lo:hi], REL, f"offsets {off} segment {e}")
+            inside[lo:hi] = True
+        assert out[~inside].eq(7.0).all(), f"offsets {off}: rows outside were written"
+
+
 @gpu
 @pytest.mark.parametrize("M_", [3, 100])
 def test_gemm_i8_largest_sum(M_):
