@@ -155,3 +155,54 @@ def test_few_infinite_h(fn, T, H, I, k):
     others = torch.ones(T, dtype=torch.bool, device="cuda")
     others[1:3] = False
     assert _same_bits(up[others], clean[0][others]) and _same_bits(down[others], clean[1][others])
+
+
+@gpu
+@pytest.mark.parametrize("segs,H,I,behind", [([3, 0, 5], 272, 48, 2), ([9], 2880, 768, 0), ([100, 0, 240], 144, 208, 5),
+                                             ([600, 300, 0, 33], 256, 400, 0)])
+def test_expert_ffn_i8_keeps_nonfinite_rows_to_themselves(segs, H, I, behind):
+    """A row that holds an infinity or NaN gets an infinite or NaN scale and
+    quantised zeros: its output is NaN, also where only its h is not finite."""
+    g = _gen(5)
+    n, E = sum(segs), len(segs)
+    x = torch.randn((n + behind, H), generator=g, device="cuda").to(BF)
+    w = [t for p in _bf16_weights(g, E, H, I) for t in M.moe_quantize_weights(p)]
+    off = torch.tensor([0, *segs], device="cuda").cumsum(0).to(torch.int32)
+    print(f"[gpu] expert_ffn_i8 with NaN segs={segs} H={H} I={I}", flush=True)
+    clean = M.moe_expert_ffn_i8(x, off, *w)[0][:n].clone()
+    rows = [0, n // 2, n - 2, n - 1]
+    x[rows[0], 3], x[rows[1], H - 1], x[rows[2], 0] = NAN, INF, -INF
+    x[rows[3]] *= 2.0 ** 70  # finite, but its h is past float32
+    x[n:] = NAN
+    out = M.moe_expert_ffn_i8(x, off, *w)[0][:n]
+    torch.cuda.synchronize()
+    assert torch.isnan(out[rows]).all()
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[rows] = False
+    assert torch.isfinite(clean).all() and _same_bits(out[others], clean[others])
+
+
+@gpu
+@pytest.mark.parametrize("fn", ["moe_forward_few", "moe_forward_few_f32"])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 72, 40, 8, 2), (4, 128, 64, 100, 7), (9, 72, 136, 40, 3), (24, 256, 136, 8, 2),
+                                       (32, 64, 40, 300, 5)])
+def test_few_keeps_nonfinite_tokens_to_themselves(fn, T, H, I, E, k):
+    """Every selection kernel; the other tokens' sums are added in another order
+    where other experts are in use: compared to a step of bf16 of the largest."""
+    g = _gen(6)
+    x = (torch.randn((T, H), generator=g, device="cuda") / H ** 0.5).to(BF)
+    wr = torch.randn((E, H), generator=g, device="cuda")
+    gu, dn = _bf16_weights(g, E, H, I)
+    print(f"[gpu] {fn} with NaN T={T} H={H} I={I} E={E}", flush=True)
+    clean = getattr(M, fn)(x, wr, None, gu, dn, k, 0)[0].float()
+    rows = sorted({0, T // 2, T - 1})
+    for t, v in zip(rows, (NAN, INF, -INF)):
+        x[t, (3 * t + 1) % H] = v
+    y = getattr(M, fn)(x, wr, None, gu, dn, k, 0)[0].float()
+    torch.cuda.synchronize()
+    assert torch.isnan(y[rows]).all()
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[rows] = False
+    if T > 3:
+        a, b = y[others], clean[others]
+        assert torch.isfinite(a).all() and float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
