@@ -418,6 +418,15 @@ def test_expert_ffn_i8_more_experts_than_rows(segs, H, I, behind):
 
 
 @gpu
+@pytest.mark.parametrize("segs,H,I,behind", [([5000, 0, 3001], 48, 64, 6000), ([4097], 64, 320, 0), ([3], 16, 40000, 2),
+                                             ([600, 1], 16, 33600, 9)],
+                         ids=["rows_dealt", "one_more", "wide", "wide_many"])
+def test_expert_ffn_i8_quantiser_forms(segs, H, I, behind):
+    """Rows dealt to 16 workgroups per CU, and rows of h that are read twice."""
+    test_expert_ffn_i8(segs, H, I, behind)
+
+
+@gpu
 @pytest.mark.parametrize("rows", [1, 16, 17, 32])
 @pytest.mark.parametrize("N", [8192, 8200, 16384])
 def test_gemm_i8_many_channels(rows, N):
