@@ -5,8 +5,9 @@
 //
 // The sum is exact: int8 x int8 products in int32 accumulators, |sum| <=
 // 2^14 K < 2^31 for K < 2^17. It does not depend on tiling, k order or split,
-// so every kernel here gives the same bits. The two scales are multiplied in
-// float32 and the result is rounded once.
+// so every kernel here gives the same bits. The sum is converted to float32 and
+// multiplied there by the product of the two scales; then comes the rounding to
+// bf16.
 //
 // Both operands are k-contiguous (W is stored [N, K], a channel per row), so
 // both feed v_mfma_i32_16x16x64_i8 without a transpose:

@@ -15,7 +15,7 @@
 // and walks the rows with a stride of the grid, so that the norm weights and a
 // channel gate stay in registers for all of its rows (NV <= 2; wider rows read
 // them again from L2) and the next row's loads are issued before the current
-// row's reductions. 16384 x 7168 with a float32 y: 200 us, 5.9 TB/s.
+// row's reductions. 16384 x 7168 with a float32 y: 200-207 us, 5.7-5.9 TB/s.
 #include "moe_kernels.h"
 #include "moe_row.h"
 
@@ -223,7 +223,10 @@ hipError_t launch_as(const Args& a, hipStream_t stream) {
   const int cus = device_cu_count();
   // Few rows: one vector per thread, the shortest chain of a row. Many rows:
   // two vectors per thread from 513 vectors on, so that two or more rows are
-  // in flight per CU beside the prefetched ones.
+  // in flight per CU beside the prefetched ones. (Not so with float32 on both
+  // sides: 136 registers leave room for one row of more than 6 waves, 16384 x
+  // 7168 332 us, 5.0 TB/s, and the kernels of four vectors with a float32 residual
+  // keep 12 to 20 bytes a lane in scratch, 2048 x 16384 100 us, 4.7 TB/s.)
   const bool many = a.T > 2 * cus;
   const int nv = a.nvec <= (many ? 512 : 1024) ? 1 : a.nvec <= 1024 ? 2 : 4;
   const int nt = int(ceil_div(ceil_div(a.nvec, nv), 64) * 64);

@@ -340,7 +340,9 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
  *     so y is rounded once; an infinite h counts as one, while an infinite
  *     weight of w_down can give NaN where moe_forward gives an infinity (h is
  *     multiplied in three parts, and a part may be 0);
- *   - two calls with the same arguments give the same bits.
+ *   - two calls with the same arguments give the same bits (the order of the
+ *     sums goes by T and by how many local experts are in use, so a token's last
+ *     bits can change with the others in its batch).
  */
 size_t moe_few_workspace_size(int T, int H, int I, int E, int k, int E_local);
 int moe_forward_few(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
@@ -375,8 +377,9 @@ int moe_quantize_rows(const moe_bf16* x, int64_t M, int K, int8_t* q, float* sca
 int moe_quantize_weights(const moe_bf16* w, int E_local, int K, int N, int8_t* q, float* scale, hipStream_t stream);
 
 /*
- * out[m, n] = (sum_k a[m, k] w[e, n, k]) a_scale[m] w_scale[e, n], rounded once
- * to bf16, for the rows m of segment e; the integer sum is exact.
+ * out[m, n] = (sum_k a[m, k] w[e, n, k]) a_scale[m] w_scale[e, n] for the rows m
+ * of segment e; the integer sum is exact, its conversion and the products are
+ * float32, and the result is rounded to bf16.
  *   a       [capacity, K] int8, a_scale [capacity] f32
  *   offsets [E_local+1] i32 DEVICE memory as for moe_expert_ffn, or NULL with
  *           E_local = 1: all capacity rows
@@ -442,7 +445,10 @@ int moe_forward_i8(const moe_bf16* x, const float* w_router, const float* bias, 
 
 /*
  * The norm before the block: out[t] = rms(r[t]) * w, with
- * rms(v) = v / sqrt(mean(v^2) + eps); float32 arithmetic, one rounding.
+ * rms(v) = v / sqrt(mean(v^2) + eps); float32 arithmetic (the squares too: they
+ * overflow above 1.8e19), then the rounding to bf16. The order in which a row's
+ * squares are added depends on H and on whether T is small, not on the other
+ * rows: two calls with the same T give the same bits.
  *
  *   r    [T, H] bf16 or f32 (r_type: MOE_TYPE_BF16 or MOE_TYPE_F32)
  *   w    [H]    f32
