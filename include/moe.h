@@ -446,7 +446,7 @@ int moe_forward_i8(const moe_bf16* x, const float* w_router, const float* bias, 
 /*
  * The norm before the block: out[t] = rms(r[t]) * w, with
  * rms(v) = v / sqrt(mean(v^2) + eps); float32 arithmetic (the squares too: they
- * overflow above 1.8e19), then the rounding to bf16. The order in which a row's
+ * overflow above 1.8e19 and vanish below 1e-23), then the rounding to bf16. The order in which a row's
  * squares are added depends on H and on whether T is small, not on the other
  * rows: two calls with the same T give the same bits.
  *
