@@ -117,7 +117,7 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
                       void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream);
 
 // 8-bit integer products (gemm_i8.hip). Rows of x quantised with a scale each;
-// rows at and past *end (device memory; NULL: none) are left alone.
+// rows at and past *end (device memory; NULL, for bf16 rows: none) are left alone.
 hipError_t launch_quantize_rows(const void* x, bool x_f32, const int32_t* end, int64_t M, int K, int8_t* q,
                                 float* scale, hipStream_t stream);
 // w [E_local, K, N] bf16 -> q [E_local, N, K] and a scale per channel.
