@@ -65,6 +65,13 @@ SIGNATURES = {
     "moe_block_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "moe_block_forward": (c_int, [_P, c_int, _P, _P, _P, _P, _P, _P, _P, c_int, c_float, _P, c_float, c_int, c_int,
                                   c_int, c_int, c_int, c_int, _P, _P, _P, c_size_t, _P]),
+    "moe_select": (c_int, [_P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float, _P, _P, _P]),
+    "moe_route_scored": (c_int, [_P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+                                 _P, _P, _P, _P, c_size_t, _P]),
+    "moe_gemm": (c_int, [_P, _P, _P, _P, c_int, _P, c_int64, c_int, c_int, c_int, c_int, _P, c_int, _P]),
+    "moe_layer_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+    "moe_layer_forward": (c_int, [_P, _P, _P, _P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                  c_int, c_int, c_int, c_int, c_int, c_float, _P, c_int, _P, c_size_t, _P]),
     "moe_norm_pre": (c_int, [_P, c_int, _P, c_float, c_int, c_int, _P, _P]),
     "moe_norm_post": (c_int, [_P, c_int, _P, c_int, _P, _P, c_int, c_float, _P, c_float, c_int, c_int, _P, _P, _P]),
 }
@@ -127,7 +134,7 @@ def _calls():
         module.bind(*(ctypes.cast(getattr(L, n), c_void_p).value
                       for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8",
                                 "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8", "moe_few_workspace_size",
-                                "moe_forward_few", "moe_forward_few_f32")))
+                                "moe_forward_few", "moe_forward_few_f32", "moe_select", "moe_gemm")))
         _calls_module = module
     return _calls_module
 
@@ -859,3 +866,196 @@ def moe_block_forward(residual, w_pre, w_router, bias, w_gate_up, w_down, k, w_p
                              _stream(None, dev))
     check(st, "moe_block_forward")
     return out, normed, ws
+
+
+# --------------------------------------------------------------------------- #
+# Routing by scores                                                            #
+# --------------------------------------------------------------------------- #
+# MOE_SCORE_*, MOE_GROUP_*, MOE_ACT_* by the names that the calls take
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
+# most groups of experts (MOE_MAX_GROUPS)
+MAX_GROUPS = 64
+
+
+def _named(names, value, what):
+    try:
+        return names[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(map(repr, names))}, got {value!r}") from None
+
+
+def _check_groups(E, k, n_group, topk_group):
+    for name, v in (("n_group", n_group), ("topk_group", topk_group)):
+        if not isinstance(v, numbers.Integral) or v < 1:
+            raise ValueError(f"{name} must be an int >= 1, got {v!r}")
+    if E % n_group:
+        raise ValueError(f"the {E} experts do not divide into n_group = {n_group} groups")
+    if topk_group > n_group:
+        raise ValueError(f"topk_group = {topk_group} exceeds n_group = {n_group}")
+    if k > topk_group * (E // n_group):
+        raise ValueError(f"k = {k} exceeds the {topk_group * (E // n_group)} experts of topk_group = {topk_group} groups")
+
+
+def moe_select(logits, k, bias=None, *, score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True,
+               scale=1.0, topk_idx=None, topk_w=None, stream=None):
+    """Experts of each token from its router logits [T, E] float32: topk_idx
+    [T, k] int32 and topk_w [T, k] float32.
+
+    ``score`` "softmax" or "sigmoid" of the logits; ``bias`` [E] float32 is added
+    to the scores for the choice alone. The experts are ``n_group`` groups of
+    consecutive ones, of which the ``topk_group`` with the largest
+    ``group_score`` stay ("max": their best expert, "top2": the sum of their two
+    best). The k best of these are taken in descending order, equal ones by
+    lower id; their weights are the scores, with ``renormalize`` divided by
+    their sum, times ``scale``."""
+    rule, kind = _named(GROUP_SCORES, group_score, "group_score"), _named(SCORES, score, "score")
+
+    def refuse():
+        torch = _torch()
+        _need(logits, torch.float32, "logits", (None, None))
+        T, E = logits.shape
+        if bias is not None:
+            _need(bias, torch.float32, "bias", (E,))
+        _check_k(k, E)
+        _check_groups(E, k, n_group, topk_group)
+        if topk_idx is not None:
+            _need(topk_idx, torch.int32, "topk_idx", (T, k))
+        if topk_w is not None:
+            _need(topk_w, torch.float32, "topk_w", (T, k))
+        _ints(T, E)
+        _placed(logits.device, logits=logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
+    return _small_call("select", (logits, bias, _plain_int(k), kind, _plain_int(n_group), _plain_int(topk_group), rule,
+                                  renormalize, scale, topk_idx, topk_w), stream, refuse)
+
+
+@_on_stream
+def moe_route_scored(x, w_router, bias, choice_bias, k, *, score="softmax", n_group=1, topk_group=1, group_score="max",
+                     renormalize=True, scale=1.0, logits=None, topk_idx=None, topk_w=None, workspace=None):
+    """moe_route with moe_select's choice: logits [T, E] float32 (with ``bias``,
+    as moe_route computes them), topk_idx [T, k] and topk_w [T, k], chosen with
+    ``choice_bias`` added to the scores. Takes ``stream``."""
+    torch = _torch()
+    rule, kind = _named(GROUP_SCORES, group_score, "group_score"), _named(SCORES, score, "score")
+    _need(x, torch.bfloat16, "x", (None, None))
+    T, H = x.shape
+    _need(w_router, torch.float32, "w_router", (None, H))
+    E = w_router.shape[0]
+    for name, t in (("bias", bias), ("choice_bias", choice_bias)):
+        if t is not None:
+            _need(t, torch.float32, name, (E,))
+    _ints(T, H, E)
+    _check_k(k, E)
+    _check_groups(E, k, n_group, topk_group)
+    for name, t, shp, dt in (("logits", logits, (T, E), torch.float32), ("topk_idx", topk_idx, (T, k), torch.int32),
+                             ("topk_w", topk_w, (T, k), torch.float32)):
+        if t is not None:
+            _need(t, dt, name, shp)
+    dev = x.device
+    _placed(dev, x=x, w_router=w_router, bias=bias, choice_bias=choice_bias)
+    logits = _out(logits, (T, E), torch.float32, dev, "logits")
+    topk_idx = _out(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+    topk_w = _out(topk_w, (T, k), torch.float32, dev, "topk_w")
+    L = lib()
+    ws = _workspace(L.moe_route_workspace_size(T, H, E, k), dev, workspace)
+    st = L.moe_route_scored(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(choice_bias), T, H, E, k, kind, n_group,
+                            topk_group, rule, int(bool(renormalize)), scale, _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+                            _ptr(ws), _nbytes(ws), _stream(None, dev))
+    check(st, "moe_route_scored")
+    return logits, topk_idx, topk_w
+
+
+# --------------------------------------------------------------------------- #
+# bf16 products with an epilogue, and the layer with a shared expert           #
+# --------------------------------------------------------------------------- #
+def moe_gemm(a, w, bias=None, offsets=None, *, activation="none", residual=None, out_dtype=None, out=None, stream=None):
+    """out [M, N] = act(a @ w[e] + bias[e]) + residual for the rows of segment e
+    of ``offsets`` [E_local + 1] int32 (None: one weight matrix for all rows).
+
+    a [M, K] and w [E_local, K, N] are bf16, ``bias`` [E_local, N] float32,
+    ``residual`` [M, N] bf16 or float32. ``activation``: "none", "relu", "silu",
+    "gelu", "gelu_tanh" or "swiglu" (w and bias then have 2 N columns, gate before
+    up, as w_gate_up). ``out_dtype`` bf16 (the default, or that of ``out``) or
+    float32; ``out`` may be ``residual``. Rows past the last segment are left as
+    they are."""
+    kind = _named(ACTIVATIONS, activation, "activation")
+    torch = _torch()
+    if out_dtype is None:
+        out_dtype = out.dtype if isinstance(out, torch.Tensor) else torch.bfloat16
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+
+    def refuse():
+        _need(a, torch.bfloat16, "a", (None, None))
+        M, K = a.shape
+        _need(w, torch.bfloat16, "w", (None, K, None))
+        E_local, _, C = w.shape
+        if kind == ACTIVATIONS["swiglu"] and C % 2:
+            raise ValueError(f"w's last dimension 2 N must be even, got {C}")
+        N = C // 2 if kind == ACTIVATIONS["swiglu"] else C
+        if bias is not None:
+            _need(bias, torch.float32, "bias", (E_local, C))
+        if offsets is not None:
+            _need(offsets, torch.int32, "offsets", (E_local + 1,))
+        elif E_local != 1:
+            raise ValueError(f"w holds {E_local} matrices: offsets is required")
+        if residual is not None:
+            _need_either(residual, "residual", (M, N))
+        if out is not None:
+            _need(out, out_dtype, "out", (M, N))
+        _ints(M, K, E_local, C)
+        _placed(a.device, a=a, w=w, bias=bias, offsets=offsets, residual=residual, out=out)
+    return _small_call("gemm", (a, w, bias, offsets, kind, residual,
+                                TYPE_F32 if out_dtype is torch.float32 else TYPE_BF16, out), stream, refuse)
+
+
+def layer_workspace_size(T, H, I, I_shared, E, k, E_local) -> int:
+    return int(lib().moe_layer_workspace_size(T, H, I, I_shared, E, k, E_local))
+
+
+@_on_stream
+def moe_layer_forward(x, w_router, bias, choice_bias, w_gate_up, w_down, k, e0, shared_gate_up=None, shared_down=None, *,
+                      score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True, scale=1.0,
+                      out_dtype=None, y=None, workspace=None):
+    """The rank's share of an MoE layer routed as by moe_route_scored, plus the
+    expert that every token shares: swiglu(x @ shared_gate_up) @ shared_down
+    ([H, 2 I_shared] and [I_shared, H] bf16; None: no shared expert). Under
+    expert parallelism one of a token's ranks adds it. Returns (y [T, H] bf16 or
+    float32, workspace). Takes ``stream``."""
+    torch = _torch()
+    rule, kind = _named(GROUP_SCORES, group_score, "group_score"), _named(SCORES, score, "score")
+    T, H, I, E, E_local, dev = _forward_args(x, w_router, bias, w_gate_up, w_down, k, e0)
+    if choice_bias is not None:
+        _need(choice_bias, torch.float32, "choice_bias", (E,))
+    _check_groups(E, k, n_group, topk_group)
+    if (shared_gate_up is None) != (shared_down is None):
+        raise ValueError("shared_gate_up and shared_down are given together")
+    Is = 0
+    if shared_gate_up is not None:
+        _need(shared_gate_up, torch.bfloat16, "shared_gate_up", (H, None))
+        if shared_gate_up.shape[1] % 2:
+            raise ValueError(f"shared_gate_up's last dimension 2 I_shared must be even, got {shared_gate_up.shape[1]}")
+        Is = shared_gate_up.shape[1] // 2
+        if Is == 0:
+            raise ValueError("shared_gate_up has no columns")
+        _need(shared_down, torch.bfloat16, "shared_down", (Is, H))
+    _ints(T, H, I, E, E_local, Is)
+    if out_dtype is None:
+        out_dtype = y.dtype if isinstance(y, torch.Tensor) else torch.bfloat16
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    if y is not None:
+        _need(y, out_dtype, "y", (T, H))
+    _placed(dev, x=x, w_router=w_router, bias=bias, choice_bias=choice_bias, w_gate_up=w_gate_up, w_down=w_down,
+            shared_gate_up=shared_gate_up, shared_down=shared_down)
+    y = _out(y, (T, H), out_dtype, dev, "y")
+    L = lib()
+    ws = _workspace(L.moe_layer_workspace_size(T, H, I, Is, E, k, E_local), dev, workspace)
+    st = L.moe_layer_forward(_ptr(x), _ptr(w_router), _ptr(bias), _ptr(choice_bias), _ptr(w_gate_up), _ptr(w_down),
+                             _ptr(shared_gate_up), _ptr(shared_down), T, H, I, Is, E, k, e0, E_local, kind, n_group,
+                             topk_group, rule, int(bool(renormalize)), scale, _ptr(y),
+                             TYPE_F32 if out_dtype is torch.float32 else TYPE_BF16, _ptr(ws), _nbytes(ws),
+                             _stream(None, dev))
+    check(st, "moe_layer_forward")
+    return y, ws

@@ -1,5 +1,5 @@
-// The Python side of the small calls (norms, row quantiser, 8-bit products, the
-// share for a few tokens), whose kernels take 4 to 20 us, less than the checks
+// The Python side of the small calls (norms, row quantiser, 8-bit and bf16
+// products, choice of experts, the share for a few tokens), whose kernels take 4 to 20 us, less than the checks
 // and allocations around them in Python: the same checks on the tensors
 // themselves, the outputs, and the call of the C entry point. Calling thread per
 // call, ctypes -> here (a launch alone is 3.2 us): norm before the block
@@ -42,6 +42,8 @@ struct {
   decltype(&moe_few_workspace_size) few_workspace_size;
   decltype(&moe_forward_few) forward_few;
   decltype(&moe_forward_few_f32) forward_few_f32;
+  decltype(&moe_select) select;
+  decltype(&moe_gemm) gemm;
 } entry;
 
 // One call's tensors, all on the current device.
@@ -108,6 +110,13 @@ bool number(PyObject* o, float& v) {
   const double d = PyFloat_AsDouble(o);
   v = float(d);
   return !(d == -1.0 && PyErr_Occurred());
+}
+// o as an int; false where it is none (no error is set)
+bool whole(PyObject* o, int& v) {
+  int over;
+  const int64_t n = PyLong_Check(o) ? PyLong_AsLongLongAndOverflow(o, &over) : (over = 1);
+  v = int(n);
+  return !over && n >= INT_MIN && n <= INT_MAX;
 }
 bool count(Py_ssize_t got, Py_ssize_t want) {
   if (got == want) return true;
@@ -312,6 +321,65 @@ PyObject* forward_few(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// select(logits, bias, k, score, n_group, topk_group, group_rule, renormalize, scale, topk_idx, topk_w)
+PyObject* select(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 11)) return nullptr;
+  Call c;
+  const Tensor* l = c.first(p[0], 2);
+  if (!c.ok || l->scalar_type() != at::kFloat) Py_RETURN_NONE;
+  const Tensor *bias = c.arg(p[1]), *io = c.arg(p[9]), *wo = c.arg(p[10]);
+  const int64_t T = l->size(0), E = l->size(1);
+  int k, score, n_group, topk_group, rule;
+  if (!whole(p[2], k) || !whole(p[3], score) || !whole(p[4], n_group) || !whole(p[5], topk_group) ||
+      !whole(p[6], rule) || k < 1 || k > E)
+    Py_RETURN_NONE;
+  c.may(bias, at::kFloat, {E});
+  c.may(io, at::kInt, {T, k});
+  c.may(wo, at::kFloat, {T, k});
+  if (!c.ok) Py_RETURN_NONE;
+  const int renormalize = PyObject_IsTrue(p[7]);
+  float scale;
+  if (renormalize < 0 || !number(p[8], scale)) return nullptr;
+  const Tensor idx = c.out(io, at::kInt, {T, k}), w = c.out(wo, at::kFloat, {T, k});
+  const int st = unlocked([&] {
+    return entry.select(in<float>(l), in<float>(bias), int(T), int(E), k, score, n_group, topk_group, rule, renormalize,
+                        scale, to<int32_t>(idx), to<float>(w), c.stream());
+  });
+  return st == MOE_OK ? pair(idx, w) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// gemm(a, w, bias, offsets, activation, residual, out_type, out)
+PyObject* gemm(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 8)) return nullptr;
+  Call c;
+  const Tensor* a = c.first(p[0], 2);
+  if (!c.ok || a->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
+  const Tensor *w = c.arg(p[1]), *bias = c.arg(p[2]), *offsets = c.arg(p[3]), *res = c.arg(p[5]), *o = c.arg(p[7]);
+  int act, out_type;
+  if (!c.ok || !w || w->dim() != 3 || !whole(p[4], act) || !whole(p[6], out_type)) Py_RETURN_NONE;
+  const int64_t M = a->size(0), K = a->size(1), E = w->size(0), C = w->size(2);
+  if (act == MOE_ACT_SWIGLU && C % 2 != 0) Py_RETURN_NONE;
+  const int64_t N = act == MOE_ACT_SWIGLU ? C / 2 : C;
+  const ScalarType type = out_type == MOE_TYPE_F32 ? at::kFloat : at::kBFloat16;
+  c.need(w, at::kBFloat16, {E, K, C});
+  c.may(bias, at::kFloat, {E, C});
+  c.may(offsets, at::kInt, {E + 1});
+  if (res && !either(res)) Py_RETURN_NONE;
+  if (res) c.need(res, res->scalar_type(), {M, N});
+  c.may(o, type, {M, N});
+  if (!c.ok || N > INT_MAX || E > INT_MAX || (!offsets && E != 1)) Py_RETURN_NONE;
+  const Tensor out = c.out(o, type, {M, N});
+  const int st = unlocked([&] {
+    return entry.gemm(in<moe_bf16>(a), in<moe_bf16>(w), in<float>(bias), in<void>(res), res ? type_of(*res) : 0,
+                      in<int32_t>(offsets), M, int(N), int(K), int(E), act, to<void>(out), out_type, c.stream());
+  });
+  return st == MOE_OK ? wrap(out) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the entry points, in the order of `entry`)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* at[sizeof(entry) / sizeof(void*)];
@@ -339,6 +407,8 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"expert_ffn_i8", fast(expert_ffn_i8), METH_FASTCALL, nullptr},
                          {"forward_few", fast(forward_few<false>), METH_FASTCALL, nullptr},
                          {"forward_few_f32", fast(forward_few<true>), METH_FASTCALL, nullptr},
+                         {"select", fast(select), METH_FASTCALL, nullptr},
+                         {"gemm", fast(gemm), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -85,6 +85,8 @@ struct Args {
   int T, H, I, E, k, e0, E_local, renormalize, y_f32;
   int polls;  // before a waiting workgroup looks for items
   void* y;
+  const int32_t* topk_idx;  // GIVEN: the selection [T, k]
+  const float* topk_w;
   // counters, kPitch apart
   int* queue;     // [kind][queue]: items handed out
   int* cnt_a;     // [expert][128 of I]: gate and up items done
@@ -448,8 +450,8 @@ __device__ __forceinline__ void gather_sums(float* s_sum, const f32x4v (&acc)[8]
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // TWO: an expert may have more than 16 rows (T > 16), which need two groups of
-// accumulators.
-template <bool TWO>
+// accumulators. GIVEN: the experts were chosen before.
+template <bool TWO, bool GIVEN>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) few_experts_kernel(Args a) {
   __shared__ Tables s;
   __shared__ __attribute__((aligned(16))) float s_sum[kWaves * 16 * kStride];
@@ -466,7 +468,15 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   ask();
   for (int i = tid; i < a.E_local; i += kThreads) s.mask[i] = 0;
   __syncthreads();
-  if (a.E <= 256 && a.T > kWaves) {
+  if constexpr (GIVEN) {
+    for (int i = tid; i < a.T * a.k; i += kThreads) {
+      const int e = a.topk_idx[i] - a.e0;
+      const bool local = e >= 0 && e < a.E_local;
+      s.sel[i] = int16_t(local ? e : -1);
+      s.wt[i] = a.topk_w[i];
+      if (local) atomicOr(&s.mask[e], 1u << (i / a.k));
+    }
+  } else if (a.E <= 256 && a.T > kWaves) {
     for (int t = tid >> 4; t < ((a.T + 15) & ~15); t += kThreads / 16) {
       if (a.E <= 32)
         pick<16, 2>(a, s, t);
@@ -889,32 +899,42 @@ size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {
   return few::layout(T, H, I, E, k, E_local).total;
 }
 
+namespace few {
+hipError_t score(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E, const Layout& L,
+                 char* ws, hipStream_t stream) {
+  auto go = [&](auto tb) {
+    hipLaunchKernelGGL(few_logits_kernel<decltype(tb)::value>, dim3(unsigned(E), unsigned(ceil_div(T, tb))),
+                       dim3(few::kThreads), 0, stream, x, w_router, bias, T, H, E,
+                       reinterpret_cast<float*>(ws + L.logits), reinterpret_cast<int*>(ws + L.counters),
+                       int(L.n_counters));
+    return hipGetLastError();
+  };
+  if (T == 1) return go(std::integral_constant<int, 1>{});
+  if (T <= 4) return go(std::integral_constant<int, 4>{});
+  return go(std::integral_constant<int, 8>{});
+}
+}  // namespace few
+
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream) {
+                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream, const Choice* choice,
+                      const float* choice_bias, int32_t* topk_idx, float* topk_w) {
   using namespace few;
   const Layout L = layout(T, H, I, E, k, E_local);
   float* logits = reinterpret_cast<float*>(ws + L.logits);
   int* ctr = reinterpret_cast<int*>(ws + L.counters);
-  auto score = [&](auto tb) {
-    hipLaunchKernelGGL(few_logits_kernel<decltype(tb)::value>, dim3(unsigned(E), unsigned(ceil_div(T, tb))),
-                       dim3(few::kThreads), 0, stream, x, w_router, bias, T, H, E, logits, ctr, int(L.n_counters));
-  };
-  if (T == 1)
-    score(std::integral_constant<int, 1>{});
-  else if (T <= 4)
-    score(std::integral_constant<int, 4>{});
-  else
-    score(std::integral_constant<int, 8>{});
-  hipError_t err = hipGetLastError();
+  hipError_t err = score(x, w_router, bias, T, H, E, L, ws, stream);
+  if (err == hipSuccess && choice)
+    err = launch_select(logits, nullptr, 0, nullptr, choice_bias, T, E, k, *choice, topk_idx, topk_w, stream);
   if (err != hipSuccess) return err;
-  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), polls, y, ctr,
-               ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
+  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), polls, y, topk_idx,
+               topk_w, ctr, ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
                reinterpret_cast<float*>(ws + L.part_b), reinterpret_cast<float*>(ws + L.h)};
   // (at least one workgroup per queue: return items are not taken from another's)
   const int grid = std::max(kQueues, workgroups > 0 ? workgroups : 2 * device_cu_count());
-  hipLaunchKernelGGL(T > 16 ? few_experts_kernel<true> : few_experts_kernel<false>, dim3(unsigned(grid)),
-                     dim3(few::kThreads), 0, stream, a);
+  auto* kern = choice ? (T > 16 ? few_experts_kernel<true, true> : few_experts_kernel<false, true>)
+                      : (T > 16 ? few_experts_kernel<true, false> : few_experts_kernel<false, false>);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(few::kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -126,6 +126,7 @@ const char* moe_status_string(int status) {
     case MOE_ERR_UNSUPPORTED:
       return "MOE_ERR_UNSUPPORTED: outside the supported sizes (E <= 1024, k <= 32, T*k < 2^31, H*I < 2^29; "
              "moe_forward_few: T <= 32; 8-bit products: K < 131072, N*K < 2^31; norms: H <= 32768; "
+             "moe_select: n_group <= 64; moe_gemm: K*columns < 2^30; "
              "the others stand at the entry point's declaration in moe.h)";
     case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE: workspace missing, misaligned or too small";
     case MOE_ERR_HIP: return "MOE_ERR_HIP: a HIP launch failed";
@@ -712,6 +713,202 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
     st = moe_norm_post(y, MOE_TYPE_F32, residual, r_type, w_post, gate, gate_kind, residual_scale, w_next, eps, T, H,
                        out, normed, stream);
   return st;
+}
+
+}  // extern "C"
+
+namespace moe {
+static bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) % kAlign) == 0; }
+
+// moe_select's sizes and kinds (T, E and k are check_route_dims').
+static int check_choice(int T, int E, int k, const Choice& c) {
+  if (T < 0 || E < 1 || k < 1 || k > E) return MOE_ERR_INVALID_ARG;
+  if ((c.score != MOE_SCORE_SOFTMAX && c.score != MOE_SCORE_SIGMOID) ||
+      (c.group_rule != MOE_GROUP_MAX && c.group_rule != MOE_GROUP_TOP2) || !std::isfinite(c.scale))
+    return MOE_ERR_INVALID_ARG;
+  if (c.n_group < 1 || E % c.n_group != 0 || c.topk_group < 1 || c.topk_group > c.n_group ||
+      k > c.topk_group * (E / c.n_group))
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxE || k > kMaxK || c.n_group > MOE_MAX_GROUPS || int64_t(T) * k >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Products of moe_gemm: 32-bit byte offsets into one expert's matrix, tiles
+// counted with 31 bits.
+static int check_gemm(int64_t capacity, int N, int K, int E_local, int activation) {
+  if (capacity < 0 || N <= 0 || K <= 0 || (N % 8) != 0 || (K % 8) != 0 || E_local < 1 || activation < MOE_ACT_NONE ||
+      activation > MOE_ACT_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  const int64_t cols = activation == MOE_ACT_SWIGLU ? 2 * int64_t(N) : N;
+  if (cols * K >= (int64_t(1) << 30) || E_local > kMaxE || !i8_rows_fit(capacity, E_local, cols))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The layer's own buffers (selection, float32 share, the shared expert's h) and
+// behind them the share's, in the form that the sizes take.
+static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
+struct LayerLayout {
+  size_t topk_idx, topk_w, share, h, rest, total;
+};
+static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k, int E_local) {
+  LayerLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes);
+    return at;
+  };
+  L.topk_idx = take(size_t(T) * k * sizeof(int32_t));
+  L.topk_w = take(size_t(T) * k * sizeof(float));
+  L.share = take(I_shared > 0 ? size_t(T) * H * sizeof(float) : 0);
+  L.h = take(size_t(T) * I_shared * sizeof(uint16_t));
+  L.rest = o;
+  L.total = o + (layer_is_few(T, H, I, k, E_local) ? few_workspace_bytes(T, H, I, E, k, E_local)
+                                                   : forward_layout(T, H, I, E, k, E_local).total);
+  return L;
+}
+}  // namespace moe
+
+extern "C" {
+
+int moe_select(const float* logits, const float* bias, int T, int E, int k, int score, int n_group, int topk_group,
+               int group_rule, int renormalize, float scale, int32_t* topk_idx, float* topk_w, hipStream_t stream) {
+  const Choice c{score, n_group, topk_group, group_rule, renormalize, scale};
+  const int st = check_choice(T, E, k, c);
+  if (st != MOE_OK || T == 0) return st;
+  if (!logits || !topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+  // (without parts the logits are only read)
+  return hip_status(launch_select(const_cast<float*>(logits), nullptr, 0, nullptr, bias, T, E, k, c, topk_idx, topk_w,
+                                  stream));
+}
+
+int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias, int T,
+                     int H, int E, int k, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                     float scale, float* logits, int32_t* topk_idx, float* topk_w, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+  const Choice c{score, n_group, topk_group, group_rule, renormalize, scale};
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_choice(T, E, k, c)) != MOE_OK || T == 0) return st;
+  if (!x || !w_router || !logits || !topk_idx || !topk_w || !aligned16(x) || !aligned16(w_router))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned256(workspace) || workspace_bytes < moe_route_workspace_size(T, H, E, k))
+    return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  float* part = reinterpret_cast<float*>(ws + align_up(size_t(3) * E * H * sizeof(uint16_t)));
+  bool split;
+  hipError_t err = launch_route_logits(x, w_router, bias, T, H, E, logits, reinterpret_cast<uint16_t*>(ws), part,
+                                       &split, stream);
+  if (err == hipSuccess)
+    err = launch_select(logits, split ? part : nullptr, route_k_parts(T, H, E) - 1, bias, choice_bias, T, E, k, c,
+                        topk_idx, topk_w, stream);
+  return hip_status(err);
+}
+
+int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
+             const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
+             int out_type, hipStream_t stream) {
+  const int st = check_gemm(capacity, N, K, E_local, activation);
+  if (st != MOE_OK) return st;
+  if (!type_ok(out_type) || (residual && !type_ok(res_type)) || (!offsets && E_local != 1)) return MOE_ERR_INVALID_ARG;
+  if (capacity == 0) return MOE_OK;
+  if (!a || !w || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_gemm_bf16({a, w, bias, residual, out, offsets, capacity, E_local, K, N, activation,
+                                      res_type == MOE_TYPE_F32, out_type == MOE_TYPE_F32}, stream));
+}
+
+size_t moe_layer_workspace_size(int T, int H, int I, int I_shared, int E, int k, int E_local) {
+  if (T < 0 || H <= 0 || I <= 0 || I_shared < 0 || E <= 0 || k <= 0 || E_local <= 0) return 0;
+  return layer_layout(T, H, I, I_shared, E, k, E_local).total;
+}
+
+int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+                      const moe_bf16* w_gate_up, const moe_bf16* w_down, const moe_bf16* w_shared_gate_up,
+                      const moe_bf16* w_shared_down, int T, int H, int I, int I_shared, int E, int k, int e0,
+                      int E_local, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                      float scale, void* y, int y_type, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const Choice c{score, n_group, topk_group, group_rule, renormalize, scale};
+  // every step's checks before the first launch
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_choice(T, E, k, c)) != MOE_OK || (st = check_local(E, e0, E_local)) != MOE_OK) return st;
+  if (I <= 0 || (I % 8) != 0 || I_shared < 0 || (I_shared % 8) != 0 || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
+  if (!expert_weights_fit(H, I) || !expert_weights_fit(H, I_shared) ||
+      min_capacity(T, k, E_local) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (I_shared > 0) {
+    if ((st = check_gemm(T, I_shared, H, 1, MOE_ACT_SWIGLU)) != MOE_OK) return st;
+    if ((st = check_gemm(T, H, I_shared, 1, MOE_ACT_NONE)) != MOE_OK) return st;
+  }
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router || !w_gate_up || !w_down || !y || (I_shared > 0) != (w_shared_gate_up != nullptr) ||
+      (I_shared > 0) != (w_shared_down != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(x), static_cast<const void*>(w_router),
+                        static_cast<const void*>(w_gate_up), static_cast<const void*>(w_down),
+                        static_cast<const void*>(w_shared_gate_up), static_cast<const void*>(w_shared_down),
+                        static_cast<const void*>(y)})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+  const LayerLayout L = layer_layout(T, H, I, I_shared, E, k, E_local);
+  if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(ws + L.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(ws + L.topk_w);
+  const bool y_f32 = y_type == MOE_TYPE_F32, shared = I_shared > 0;
+  // the share, float32 where the shared expert is added to it
+  void* share = shared ? static_cast<void*>(ws + L.share) : y;
+  const bool share_f32 = shared || y_f32;
+  hipError_t err;
+  if (layer_is_few(T, H, I, k, E_local)) {
+    err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32, 0,
+                     kFewPolls, ws + L.rest, stream, &c, choice_bias, topk_idx, topk_w);
+  } else {
+    const ForwardLayout F = forward_layout(T, H, I, E, k, E_local);
+    auto at = [&](size_t off) { return static_cast<void*>(ws + L.rest + off); };
+    const int64_t cap = min_capacity(T, k, E_local);
+    float* logits = static_cast<float*>(at(F.logits));
+    float* part = static_cast<float*>(at(F.part));
+    int32_t* offsets = static_cast<int32_t*>(at(F.offsets));
+    int32_t* perm_src = static_cast<int32_t*>(at(F.perm_src));
+    int32_t* inv = static_cast<int32_t*>(at(F.inv));
+    int32_t* counts = static_cast<int32_t*>(at(F.counts));
+    int32_t* chunks = static_cast<int32_t*>(at(F.chunks));
+    uint16_t* x_perm = static_cast<uint16_t*>(at(F.x_perm));
+    uint16_t* h = static_cast<uint16_t*>(at(F.h));
+    uint16_t* out = static_cast<uint16_t*>(at(F.out));
+    const bool gather = expert_gemm1_can_gather(T, H);
+    const int64_t rows_hint = ceil_div(int64_t(T) * k, E);
+    bool split;
+    err = launch_route_logits(x, w_router, bias, T, H, E, logits, static_cast<uint16_t*>(at(F.planes)), part, &split,
+                              stream);
+    if (err == hipSuccess)
+      err = launch_select(logits, split ? part : nullptr, route_k_parts(T, H, E) - 1, bias, choice_bias, T, E, k, c,
+                          topk_idx, topk_w, stream);
+    if (err == hipSuccess)
+      err = gather ? launch_dispatch_index(topk_idx, T, E, k, e0, E_local, counts, offsets, perm_src, inv, chunks, stream)
+                   : launch_dispatch(x, topk_idx, T, H, E, k, e0, E_local, counts, offsets, perm_src, inv, x_perm,
+                                     chunks, stream);
+    if (err == hipSuccess)
+      err = gather ? launch_expert_gemm1_gather(x, perm_src, T, k, offsets, w_gate_up, H, I, E_local, cap, h, stream,
+                                                rows_hint)
+                   : launch_expert_gemm1(x_perm, offsets, w_gate_up, H, I, E_local, cap, h, stream, rows_hint);
+    if (err == hipSuccess)
+      err = launch_expert_gemm2(h, offsets, w_down, H, I, E_local, cap, out, stream, rows_hint);
+    if (err == hipSuccess) err = launch_combine(out, inv, topk_w, T, H, k, share, share_f32, stream);
+  }
+  if (err == hipSuccess && shared) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
+    err = launch_gemm_bf16({x, w_shared_gate_up, nullptr, nullptr, h, nullptr, T, 1, H, I_shared, MOE_ACT_SWIGLU, 0, 0},
+                           stream);
+    if (err == hipSuccess)
+      err = launch_gemm_bf16({h, w_shared_down, nullptr, share, y, nullptr, T, 1, I_shared, H, MOE_ACT_NONE, 1, y_f32},
+                             stream);
+  }
+  return hip_status(err);
 }
 
 }  // extern "C"

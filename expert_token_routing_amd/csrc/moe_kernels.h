@@ -13,6 +13,13 @@ constexpr int kChunk = 64;  // tokens per dispatch chunk (one wave)
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// How experts are chosen from scores (select.hip); the numbers are MOE_SCORE_*
+// and MOE_GROUP_*.
+struct Choice {
+  int score, n_group, topk_group, group_rule, renormalize;
+  float scale;
+};
+
 // Router: planes must hold 3*E*H bf16.
 // planes: 3 x E x H bf16 scratch; part: T x E float32 scratch (second k half)
 // Parts the router's k range is split into (1: no split); the workspace holds
@@ -22,6 +29,12 @@ int route_k_parts(int T, int H, int E);
 hipError_t launch_route(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E, int k,
                         int renormalize, float* logits, int32_t* topk_idx, float* topk_w, uint16_t* planes, float* part,
                         hipStream_t stream);
+
+// The router's logits alone: logits [T, E] hold the sums with the bias, or, with
+// *split set, the first of route_k_parts(T, H, E) partial sums, the others being
+// in part and the bias not added yet.
+hipError_t launch_route_logits(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E,
+                               float* logits, uint16_t* planes, float* part, bool* split, hipStream_t stream);
 
 // Dispatch: chunk_table must hold E * ceil(T/64) int32.
 hipError_t launch_dispatch(const uint16_t* x, const int32_t* topk_idx, int T, int H, int E, int k, int e0,
@@ -108,13 +121,17 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
 
 // The whole share for T <= 32 tokens in two kernels (few.hip). workgroups of the
 // second (0: two per CU), and polls: how often a waiting one looks before it
-// turns to other work. The results depend on neither.
+// turns to other work. The results depend on neither. With a choice, a kernel
+// between the two chooses by it into topk_idx and topk_w [T, k] (renormalize is
+// then the choice's).
 constexpr int kFewPolls = 4096;
 bool few_supported(int T, int H, int I, int k, int E_local);
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local);
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream);
+                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream,
+                      const Choice* choice = nullptr, const float* choice_bias = nullptr, int32_t* topk_idx = nullptr,
+                      float* topk_w = nullptr);
 
 // 8-bit integer products (gemm_i8.hip). Rows of x quantised with a scale each;
 // rows at and past *end (device memory; NULL, for bf16 rows: none) are left alone.
@@ -137,6 +154,25 @@ int i8_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int 
 hipError_t launch_gate_up_i8(const int8_t* A, const float* sa, const int32_t* gather_src, int gather_k,
                              int gather_rows, const int32_t* offsets, int E_local, int64_t capacity, const int8_t* W,
                              const float* sw, int H, int I, float* h, int64_t rows_hint, hipStream_t stream);
+
+// logits [T, E]; with part, logits hold the first of nparts + 1 partial sums and
+// take the whole ones, logit_bias included (which is read only then).
+hipError_t launch_select(float* logits, const float* part, int nparts, const float* logit_bias, const float* bias, int T,
+                         int E, int k, const Choice& c, int32_t* topk_idx, float* topk_w, hipStream_t stream);
+
+// C = act(A W_e + bias_e) + res over the segments of offsets (NULL: one segment,
+// all capacity rows); gemm_bf16.hip. act: MOE_ACT_*.
+struct GemmBf16 {
+  const uint16_t* A;       // [capacity, K]
+  const uint16_t* W;       // [E_local][K, N], or [K, 2 N] for SwiGLU
+  const float* bias;       // [E_local][columns of W], or NULL
+  const void* res;         // [capacity, N], or NULL
+  void* C;                 // [capacity, N]
+  const int32_t* offsets;
+  int64_t capacity;
+  int E_local, K, N, act, res_f32, out_f32;
+};
+hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream);
 
 // Cached device facts of the current device.
 int device_cu_count();

@@ -842,12 +842,12 @@ int route_k_parts(int T, int H, int E) {
   return (nk_all + per - 1) / per;
 }
 
-hipError_t launch_route(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E, int k,
-                        int renormalize, float* logits, int32_t* topk_idx, float* topk_w, uint16_t* planes, float* part,
-                        hipStream_t stream) {
+hipError_t launch_route_logits(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E,
+                               float* logits, uint16_t* planes, float* part, bool* split_out, hipStream_t stream) {
   const int64_t n = int64_t(E) * H;
   const int parts = route_k_parts(T, H, E);
   const bool split = parts > 1;
+  *split_out = split;
   // Cutting the float32 weights in registers is repeated by every token tile:
   // it pays (no plane pass, a third less weight traffic) for a few tiles and
   // loses beyond (measured: ahead at 1 and 8 tiles of 256 tokens, behind at
@@ -879,9 +879,17 @@ hipError_t launch_route(const uint16_t* x, const float* w_router, const float* b
       dim3 grid(unsigned((T + 127) / 128), unsigned((E + 127) / 128));
       hipLaunchKernelGGL(route_logits_kernel, grid, dim3(kThreads), 0, stream, x, planes, bias, logits, T, H, E);
     }
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    return hipGetLastError();
   }
+}
+
+hipError_t launch_route(const uint16_t* x, const float* w_router, const float* bias, int T, int H, int E, int k,
+                        int renormalize, float* logits, int32_t* topk_idx, float* topk_w, uint16_t* planes, float* part,
+                        hipStream_t stream) {
+  const int parts = route_k_parts(T, H, E);
+  bool split;
+  const hipError_t err = launch_route_logits(x, w_router, bias, T, H, E, logits, planes, part, &split, stream);
+  if (err != hipSuccess) return err;
   {
     const float* pt = split ? part : nullptr;
     // the vector loads and stores need 16-byte aligned rows (8-byte for two

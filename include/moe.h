@@ -505,6 +505,119 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
                       int H, int I, int E, int k, int renormalize, void* out, moe_bf16* normed, void* workspace,
                       size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Routing by scores: sigmoid or softmax, choice bias, groups of experts.    */
+/* ------------------------------------------------------------------------ */
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+/* Value of a group of experts. */
+#define MOE_GROUP_MAX 0  /* its largest choice value */
+#define MOE_GROUP_TOP2 1 /* the sum of its two largest (a group of one: that one) */
+
+/* Most groups of experts. */
+#define MOE_MAX_GROUPS 64
+
+/*
+ * Experts of each token from given logits:
+ *   s_e = 1 / (1 + exp(-logits[t, e]))  or the softmax over all E experts,
+ *   c_e = s_e + bias[e]                 (bias NULL: s_e): the choice value;
+ *   the E experts are n_group groups of consecutive ones, of which the
+ *   topk_group with the largest value (group_rule, MOE_GROUP_*) stay;
+ *   topk_idx [T, k] i32 OUT: the k largest c_e of their experts, descending;
+ *   topk_w   [T, k] f32 OUT: scale * s_e of those (without the bias), and with
+ *            renormalize divided by the sum of the k scores.
+ * Equal values put the lower group and the lower expert first. The choice is
+ * that of the values in 64 bits: scores that differ by less than float32 tells
+ * apart are still told apart.
+ *   logits [T, E] f32, bias [E] f32: at any float address.
+ * A NaN logit counts as -infinity, a NaN choice value or group value too (the ids
+ * are distinct and in [0, E) whatever the inputs hold). A token without a
+ * logit above -infinity gets NaN weights; a logit of +infinity has the
+ * softmax score 1 / (how many there are).
+ * 1 <= k <= topk_group * (E / n_group), E a multiple of n_group,
+ * 1 <= topk_group <= n_group, scale finite; E <= 1024, k <= 32, n_group <=
+ * MOE_MAX_GROUPS, T * k < 2^31 (else MOE_ERR_UNSUPPORTED). n_group = 1: no
+ * groups.
+ */
+int moe_select(const float* logits, const float* bias, int T, int E, int k, int score, int n_group, int topk_group,
+               int group_rule, int renormalize, float scale, int32_t* topk_idx, float* topk_w, hipStream_t stream);
+
+/*
+ * moe_route with moe_select's choice: logits = x . w_router^T + bias as
+ * moe_route computes them (bias [E] f32 or NULL belongs to the logits), then
+ * moe_select of them with choice_bias ([E] f32 or NULL). logits [T, E] OUT
+ * holds what the choice was made from. workspace: moe_route_workspace_size
+ * bytes, 256-byte aligned. Other arguments and checks are the two calls'.
+ */
+int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias, int T,
+                     int H, int E, int k, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                     float scale, float* logits, int32_t* topk_idx, float* topk_w, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* bf16 products with bias, activation and residual in the epilogue.         */
+/* ------------------------------------------------------------------------ */
+
+/* Activations of moe_gemm. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2      /* z / (1 + exp(-z)) */
+#define MOE_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define MOE_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define MOE_ACT_SWIGLU 5    /* silu of columns [0, N) times columns [N, 2 N) */
+
+/*
+ * out[m] = act(a[m] . w[e] + bias[e]) + residual[m] for the rows m of segment
+ * e: float32 sums, one rounding at the end.
+ *   a        [capacity, K] bf16
+ *   w        [E_local, K, C] bf16, C = N, or 2 N for MOE_ACT_SWIGLU (the
+ *            layout of w_gate_up and w_down)
+ *   bias     [E_local, C] f32 or NULL
+ *   residual [capacity, N] of res_type (MOE_TYPE_*), or NULL; may be out itself
+ *            where the types are equal
+ *   offsets  [E_local+1] i32 DEVICE memory as for moe_expert_ffn, or NULL with
+ *            E_local = 1: all capacity rows
+ *   out      [capacity, N] of out_type OUT; rows >= offsets[E_local] untouched
+ * The order of a sum depends on the sizes, not on the other rows' values: two
+ * calls with the same arguments give the same bits. An infinity or a NaN in a
+ * row of a makes that row's outputs what the formula gives and touches no
+ * other row.
+ * K and N are multiples of 8, K * C < 2^30, E_local <= 1024, capacity < 2^31 -
+ * 1024 and (capacity / 16 + E_local) * C / 32 < 2^31 (rounded up), else
+ * MOE_ERR_UNSUPPORTED; all pointers but offsets are 16-byte aligned.
+ */
+int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
+             const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
+             int out_type, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* A layer with scored routing and an expert that every token shares.        */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * y = the rank's share of the MoE layer, routed as by moe_route_scored, plus
+ * swiglu(x . w_shared_gate_up) . w_shared_down (moe_gemm):
+ *   w_shared_gate_up [H, 2 I_shared] bf16, w_shared_down [I_shared, H] bf16; both
+ *   NULL with I_shared = 0: no shared expert. Under expert parallelism every
+ *   token's shared expert belongs to one rank's share: give it to one of the
+ *   ranks that a token passes through.
+ *   y        [T, H] of y_type (MOE_TYPE_*), rounded once where it is bf16 and
+ *            there is a shared expert or T is small (as in moe_forward_few)
+ * The share is that of moe_forward_few_f32 up to 16 tokens where its limits allow, of
+ * moe_forward_f32 otherwise. I_shared is a multiple of 8, H * I_shared < 2^29;
+ * other arguments and their checks are moe_forward's and moe_select's.
+ * workspace: moe_layer_workspace_size bytes, 256-byte aligned; no part of it
+ * needs to start at zero, calls that overlap need their own.
+ */
+size_t moe_layer_workspace_size(int T, int H, int I, int I_shared, int E, int k, int E_local);
+int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+                      const moe_bf16* w_gate_up, const moe_bf16* w_down, const moe_bf16* w_shared_gate_up,
+                      const moe_bf16* w_shared_down, int T, int H, int I, int I_shared, int E, int k, int e0,
+                      int E_local, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                      float scale, void* y, int y_type, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
