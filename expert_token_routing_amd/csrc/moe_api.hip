@@ -741,7 +741,7 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
       activation > MOE_ACT_SWIGLU)
     return MOE_ERR_INVALID_ARG;
   const int64_t cols = activation == MOE_ACT_SWIGLU ? 2 * int64_t(N) : N;
-  if (cols * K >= (int64_t(1) << 30) || E_local > kMaxE || !i8_rows_fit(capacity, E_local, cols))
+  if (cols * K >= (int64_t(1) << 30) || K >= (1 << 20) || E_local > kMaxE || !i8_rows_fit(capacity, E_local, cols))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -807,9 +807,9 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
   return hip_status(err);
 }
 
-int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
-             const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
-             int out_type, hipStream_t stream) {
+static int gemm_impl(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
+                     const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
+                     int out_type, int tile, hipStream_t stream) {
   const int st = check_gemm(capacity, N, K, E_local, activation);
   if (st != MOE_OK) return st;
   if (!type_ok(out_type) || (residual && !type_ok(res_type)) || (!offsets && E_local != 1)) return MOE_ERR_INVALID_ARG;
@@ -818,7 +818,26 @@ int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void
   if (!aligned16(a) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_gemm_bf16({a, w, bias, residual, out, offsets, capacity, E_local, K, N, activation,
-                                      res_type == MOE_TYPE_F32, out_type == MOE_TYPE_F32}, stream));
+                                      res_type == MOE_TYPE_F32, out_type == MOE_TYPE_F32}, stream, tile));
+}
+
+int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
+             const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
+             int out_type, hipStream_t stream) {
+  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type, -1,
+                   stream);
+}
+
+// moe_gemm on given tiles, and the tiles that a call takes, for the tests of every
+// kind at sizes that the rule gives to another. Not part of moe.h.
+int moe_internal_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
+                      const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
+                      int out_type, int tile, hipStream_t stream) {
+  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type, tile,
+                   stream);
+}
+int moe_internal_gemm_tile(int swiglu, int ragged, int E_local, int64_t capacity, int N, int K, int cus) {
+  return gemm_bf16_tile(swiglu != 0, ragged != 0, E_local, capacity, N, K, cus);
 }
 
 size_t moe_layer_workspace_size(int T, int H, int I, int I_shared, int E, int k, int E_local) {

@@ -172,7 +172,9 @@ struct GemmBf16 {
   int64_t capacity;
   int E_local, K, N, act, res_f32, out_f32;
 };
-hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream);
+// tile: one of gemm_bf16_tile's (-1: its choice for a device of `cus` CUs).
+hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream, int tile = -1);
+int gemm_bf16_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int cus);
 
 // Cached device facts of the current device.
 int device_cu_count();

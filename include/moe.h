@@ -584,7 +584,7 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
  * calls with the same arguments give the same bits. An infinity or a NaN in a
  * row of a makes that row's outputs what the formula gives and touches no
  * other row.
- * K and N are multiples of 8, K * C < 2^30, E_local <= 1024, capacity < 2^31 -
+ * K and N are multiples of 8, K < 2^20, K * C < 2^30, E_local <= 1024, capacity < 2^31 -
  * 1024 and (capacity / 16 + E_local) * C / 32 < 2^31 (rounded up), else
  * MOE_ERR_UNSUPPORTED; all pointers but offsets are 16-byte aligned.
  */

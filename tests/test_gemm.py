@@ -94,13 +94,35 @@ def inputs(Mr, K, N, act, bias, res, El, integers, seed):
     return a, w, b, r
 
 
-def run(Mr, K, N, act="none", bias=False, res=None, out=BF, El=1, offsets=None, integers=False, seed=0):
-    say(f"gemm {Mr} x {K} x {N} act={act} bias={bias} res={res} out={out} El={El} offsets={offsets} integers={integers}")
+TILES = ["stream16", "stream32", "stream64", "narrow", "narrow32", "narrow64", "small", "mid64", "mid", "midk", "mid2", "big"]
+
+
+def on_tile(tile, a, w, b, off, act, r, out):
+    """moe_gemm on given tiles (an entry point for the tests, not of the header)."""
+    fn = M.lib().moe_internal_gemm
+    fn.restype = ctypes.c_int
+    P, I = ctypes.c_void_p, ctypes.c_int
+    fn.argtypes = [P, P, P, P, I, P, ctypes.c_int64, I, I, I, I, P, I, I, P]
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+    st = fn(ptr(a), ptr(w), ptr(b), ptr(r), int(r is not None and r.dtype == F32), ptr(off), a.shape[0], out.shape[1],
+            a.shape[1], w.shape[0], ACTS.index(act), ptr(out), int(out.dtype == F32), TILES.index(tile),
+            torch.cuda.current_stream(a.device).cuda_stream)
+    M.check(st, f"moe_internal_gemm on {tile}")
+    return out
+
+
+def run(Mr, K, N, act="none", bias=False, res=None, out=BF, El=1, offsets=None, integers=False, seed=0, tile=None):
+    say(f"gemm {Mr} x {K} x {N} act={act} bias={bias} res={res} out={out} El={El} offsets={offsets} integers={integers} "
+        f"tile={tile}")
     a, w, b, r = inputs(Mr, K, N, act, bias, res, El, integers, seed)
     off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device=a.device)
     given = torch.full((Mr, N), -77.0, dtype=out, device=a.device)
-    got = M.moe_gemm(a, w, b, off, activation=act, residual=r, out=given)
-    assert got.data_ptr() == given.data_ptr()
+    if tile is None:
+        assert M.moe_gemm(a, w, b, off, activation=act, residual=r, out=given).data_ptr() == given.data_ptr()
+    else:
+        on_tile(tile, a, w, b, off, act, r, given)
     v, tol = reference(a, w, b, off, act, r, integers)
     written = ~torch.isnan(v)
     assert torch.all(given[~written] == -77.0)
@@ -203,6 +225,24 @@ def test_sizes_of_layers(Mr, K, N):
     run(Mr, K, N, integers=True, res=BF, out=F32, seed=N)
     run(Mr, K, N, act="swiglu", bias=True, res=F32, seed=K)
     run(Mr, K, N, act="silu", bias=True, seed=K + 1)
+
+
+@gpu
+@pytest.mark.parametrize("tile", TILES)
+def test_every_tile(tile):
+    """Each kind of tile at sizes that the rule may give to another one: rows and columns past and
+    inside a block, every end of k, fewer stages than groups of waves, several rounds of the grid."""
+    for i, (Mr, K, N) in enumerate(((1, 8, 8), (5, 64, 32), (16, 72, 40), (33, 136, 72), (70, 584, 136), (130, 1032, 264),
+                                    (300, 328, 520), (577, 2056, 1032))):
+        run(Mr, K, N, bias=True, res=(None, BF, F32)[i % 3], out=(BF, F32)[i % 2], integers=True, seed=i, tile=tile)
+        if tile != "narrow64":  # (32 columns hold no whole gate and up fragments of a wave there)
+            run(Mr, K, N, act="swiglu", bias=True, res=(F32, None, BF)[i % 3], out=(BF, F32)[i % 2], seed=i, tile=tile)
+        run(Mr, K, N, act="gelu", bias=True, res=BF, seed=i, tile=tile)
+    lens = [40, 0, 3, 100, 0, 333, 7, 1]
+    off = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    run(off[-1] + 9, 328, 264, bias=True, res=F32, El=8, offsets=off, integers=True, tile=tile)
+    run(off[-1], 128, 264, act="none" if tile == "narrow64" else "swiglu", bias=True, El=8, offsets=off, tile=tile)
+    run(6000, 72, 2056, integers=True, tile=tile)
 
 
 # --------------------------------------------------------------------------- #
