@@ -12,10 +12,10 @@ from ._binding import (  # noqa: F401
     LIB_PATH, MOE_ERR_HIP, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_OK, FEW_TOKENS,
     MAX_GROUPS, NOALLOC_SCRATCH_BYTES, SIGNATURES,
     MoEError, block_workspace_size, check, expert_ffn_i8_workspace_size, few_workspace_size,
-    forward_i8_workspace_size, forward_workspace_layout, forward_workspace_size, layer_workspace_size, lib,
-    moe_block_forward,
-    moe_combine, moe_combine_f32, moe_dispatch, moe_expert_ffn, moe_expert_ffn_i8, moe_forward, moe_forward_f32,
-    moe_forward_few, moe_forward_few_f32, moe_forward_fused, moe_forward_i8, moe_forward_noalloc,
-    moe_forward_profiled, moe_gemm, moe_gemm_i8, moe_layer_forward, moe_norm_post, moe_norm_pre, moe_quantize_rows, moe_quantize_weights,
-    moe_route, moe_route_scored, moe_select, status_string,
+    forward_i8_workspace_size, forward_workspace_layout, forward_workspace_size, gemm_workspace_size,
+    layer_workspace_size, lib, moe_block_forward, moe_combine, moe_combine_f32, moe_dispatch, moe_expert_ffn,
+    moe_expert_ffn_i8, moe_forward, moe_forward_f32, moe_forward_few, moe_forward_few_f32, moe_forward_fused,
+    moe_forward_i8, moe_forward_noalloc, moe_forward_profiled, moe_gemm, moe_gemm_i8, moe_layer_forward,
+    moe_norm_post, moe_norm_pre, moe_quantize_rows, moe_quantize_weights, moe_route, moe_route_scored, moe_select,
+    status_string,
 )

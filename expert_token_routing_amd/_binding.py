@@ -68,7 +68,8 @@ SIGNATURES = {
     "moe_select": (c_int, [_P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float, _P, _P, _P]),
     "moe_route_scored": (c_int, [_P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float,
                                  _P, _P, _P, _P, c_size_t, _P]),
-    "moe_gemm": (c_int, [_P, _P, _P, _P, c_int, _P, c_int64, c_int, c_int, c_int, c_int, _P, c_int, _P]),
+    "moe_gemm_workspace_size": (c_size_t, [c_int64, c_int, c_int, c_int, c_int]),
+    "moe_gemm": (c_int, [_P, _P, _P, _P, c_int, _P, c_int64, c_int, c_int, c_int, c_int, _P, c_int, _P, c_size_t, _P]),
     "moe_layer_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
     "moe_layer_forward": (c_int, [_P, _P, _P, _P, _P, _P, _P, _P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                   c_int, c_int, c_int, c_int, c_int, c_float, _P, c_int, _P, c_size_t, _P]),
@@ -134,7 +135,8 @@ def _calls():
         module.bind(*(ctypes.cast(getattr(L, n), c_void_p).value
                       for n in ("moe_norm_pre", "moe_norm_post", "moe_quantize_rows", "moe_gemm_i8",
                                 "moe_expert_ffn_i8_workspace_size", "moe_expert_ffn_i8", "moe_few_workspace_size",
-                                "moe_forward_few", "moe_forward_few_f32", "moe_select", "moe_gemm")))
+                                "moe_forward_few", "moe_forward_few_f32", "moe_select", "moe_gemm_workspace_size",
+                                "moe_gemm")))
         _calls_module = module
     return _calls_module
 
@@ -969,7 +971,13 @@ def moe_route_scored(x, w_router, bias, choice_bias, k, *, score="softmax", n_gr
 # --------------------------------------------------------------------------- #
 # bf16 products with an epilogue, and the layer with a shared expert           #
 # --------------------------------------------------------------------------- #
-def moe_gemm(a, w, bias=None, offsets=None, *, activation="none", residual=None, out_dtype=None, out=None, stream=None):
+def gemm_workspace_size(M, N, K, E_local=1, activation="none") -> int:
+    """Bytes of workspace moe_gemm needs for [M, K] rows and N outputs (0: none)."""
+    return int(lib().moe_gemm_workspace_size(M, N, K, E_local, _named(ACTIVATIONS, activation, "activation")))
+
+
+def moe_gemm(a, w, bias=None, offsets=None, *, activation="none", residual=None, out_dtype=None, out=None,
+             workspace=None, stream=None):
     """out [M, N] = act(a @ w[e] + bias[e]) + residual for the rows of segment e
     of ``offsets`` [E_local + 1] int32 (None: one weight matrix for all rows).
 
@@ -1006,8 +1014,10 @@ def moe_gemm(a, w, bias=None, offsets=None, *, activation="none", residual=None,
             _need(out, out_dtype, "out", (M, N))
         _ints(M, K, E_local, C)
         _placed(a.device, a=a, w=w, bias=bias, offsets=offsets, residual=residual, out=out)
+        if workspace is not None:
+            _workspace(lib().moe_gemm_workspace_size(M, N, K, E_local, kind), a.device, workspace)
     return _small_call("gemm", (a, w, bias, offsets, kind, residual,
-                                TYPE_F32 if out_dtype is torch.float32 else TYPE_BF16, out), stream, refuse)
+                                TYPE_F32 if out_dtype is torch.float32 else TYPE_BF16, out, workspace), stream, refuse)
 
 
 def layer_workspace_size(T, H, I, I_shared, E, k, E_local) -> int:

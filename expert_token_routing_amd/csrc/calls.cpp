@@ -43,6 +43,7 @@ struct {
   decltype(&moe_forward_few) forward_few;
   decltype(&moe_forward_few_f32) forward_few_f32;
   decltype(&moe_select) select;
+  decltype(&moe_gemm_workspace_size) gemm_workspace_size;
   decltype(&moe_gemm) gemm;
 } entry;
 
@@ -350,14 +351,15 @@ PyObject* select(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// gemm(a, w, bias, offsets, activation, residual, out_type, out)
+// gemm(a, w, bias, offsets, activation, residual, out_type, out, workspace)
 PyObject* gemm(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 8)) return nullptr;
+  if (!count(n, 9)) return nullptr;
   Call c;
   const Tensor* a = c.first(p[0], 2);
   if (!c.ok || a->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
-  const Tensor *w = c.arg(p[1]), *bias = c.arg(p[2]), *offsets = c.arg(p[3]), *res = c.arg(p[5]), *o = c.arg(p[7]);
+  const Tensor *w = c.arg(p[1]), *bias = c.arg(p[2]), *offsets = c.arg(p[3]), *res = c.arg(p[5]), *o = c.arg(p[7]),
+               *given = c.arg(p[8]);
   int act, out_type;
   if (!c.ok || !w || w->dim() != 3 || !whole(p[4], act) || !whole(p[6], out_type)) Py_RETURN_NONE;
   const int64_t M = a->size(0), K = a->size(1), E = w->size(0), C = w->size(2);
@@ -371,10 +373,14 @@ PyObject* gemm(PyObject*, PyObject* const* p, Py_ssize_t n) {
   if (res) c.need(res, res->scalar_type(), {M, N});
   c.may(o, type, {M, N});
   if (!c.ok || N > INT_MAX || E > INT_MAX || (!offsets && E != 1)) Py_RETURN_NONE;
+  const size_t bytes = entry.gemm_workspace_size(M, int(N), int(K), int(E), act);
+  const Tensor ws = given || bytes ? c.workspace(given, bytes) : Tensor();
+  if (!c.ok) Py_RETURN_NONE;
   const Tensor out = c.out(o, type, {M, N});
   const int st = unlocked([&] {
     return entry.gemm(in<moe_bf16>(a), in<moe_bf16>(w), in<float>(bias), in<void>(res), res ? type_of(*res) : 0,
-                      in<int32_t>(offsets), M, int(N), int(K), int(E), act, to<void>(out), out_type, c.stream());
+                      in<int32_t>(offsets), M, int(N), int(K), int(E), act, to<void>(out), out_type, to<void>(ws),
+                      ws.defined() ? ws.nbytes() : 0, c.stream());
   });
   return st == MOE_OK ? wrap(out) : PyLong_FromLong(st);
   END_HANDLE_TH_ERRORS

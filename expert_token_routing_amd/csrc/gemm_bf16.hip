@@ -12,8 +12,8 @@
 // are the first operand of v_mfma_f32_16x16x32_bf16, so a lane ends with 4
 // consecutive columns of one row.
 //
-// One kernel in a dozen tile shapes, from 16 x 32 (few rows: the weight stream
-// is the whole cost) to 288 x 256.
+// One kernel in four tile shapes, from 32 x 256 to 288 x 256. Where the tiles are
+// fewer than the CUs, k is cut into ranges whose sums a second kernel adds.
 #include "gemm_dma.h"
 #include "gemm_tile.h"
 #include "moe_kernels.h"
@@ -58,6 +58,20 @@ __device__ __forceinline__ float activate(int kind, float z) {
 // Tiles through LDS
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int chunk_pos(int r, int c) { return c ^ ((r >> 1) & 7); }
+
+// dma16 past the caches, for bytes that no other workgroup reads.
+__device__ __forceinline__ void dma16_stream(const i32x4& rsrc, uint32_t voff, uint32_t soff,
+                                             const MOE_LDS char* lds_base) {
+  const uint32_t lds_addr = uint32_t(reinterpret_cast<uintptr_t>(lds_base));
+  asm volatile("" : "+s"(soff));
+  uint32_t s;
+  // (the scalar move keeps a wait state between the write of M0 and the load, and
+  // the load off a scalar that a vector instruction may have written just before)
+  asm volatile("s_mov_b32 %0, %3\n\tbuffer_load_dwordx4 %1, %2, %0 offen nt lds"
+               : "=&s"(s)
+               : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds_addr)
+               : "memory");
+}
 
 // ROWS rows of A x 64 k: load i W + w (8 rows, 8 lanes each) is wave w's. Row r
 // sits at 128 r, its 16-byte chunk c at c ^ ((r >> 1) & 7) (conflict-free for
@@ -119,13 +133,16 @@ struct LoaderB {
   }
   // (past the end of K a lane reads one of the stage's first 8 rows instead)
   template <bool TAIL>
-  __device__ __forceinline__ void issue(MOE_LDS char* dst, int w, int stage, int valid) const {
+  __device__ __forceinline__ void issue(MOE_LDS char* dst, int w, int stage, int valid, bool once) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
       if (kLoads % W == 0 || j * W + w < kLoads) {
         const int r = row(j, w);
         const uint32_t back = TAIL && r >= 8 * valid ? uint32_t(r & ~7) * ld : 0u;
-        dma16(rsrc, voff[j] - back, uint32_t(stage) * kSK * ld, dst + 1024 * (j * W + w));
+        if (once)
+          dma16_stream(rsrc, voff[j] - back, uint32_t(stage) * kSK * ld, dst + 1024 * (j * W + w));
+        else
+          dma16(rsrc, voff[j] - back, uint32_t(stage) * kSK * ld, dst + 1024 * (j * W + w));
       }
   }
 };
@@ -142,14 +159,12 @@ __device__ __forceinline__ void alternate_mfma_reads() {
   for (int i = NM; i < NR; ++i) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 }
 
-// KG groups of WR x WC waves; a tile is 16 FM WR rows x 16 FN WC columns, S
-// stages in LDS per group. Group q takes k stages q, q + KG, ..; the groups'
-// sums meet in LDS, in the order of the groups. 16-row fragment f belongs to wave
-// row f % WR; wave column wn holds columns 16 FN wn .. (SwiGLU: 8 FN of gate,
-// then the matching up).
-template <int WR_, int WC_, int FN_, int S_, int KG_>
+// WR x WC waves; a tile is 16 FM WR rows x 16 FN WC columns, S stages in LDS.
+// 16-row fragment f belongs to wave row f % WR; wave column wn holds columns 16 FN
+// wn .. (SwiGLU: 8 FN of gate, then the matching up).
+template <int WR_, int WC_, int FN_, int S_>
 struct Shape {
-  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_, KG = KG_;
+  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_;
   static constexpr int W = WR * WC, BN = 16 * FN * WC;
 };
 
@@ -174,7 +189,7 @@ __device__ __forceinline__ void epilogue(MOE_LDS char* lds, const GemmBf16& p, c
   constexpr int CW = 16 * FN, OW = SWIGLU ? CW / 2 : CW;  // columns, outputs of a wave
   constexpr int kPitch = CW + 4;                          // (16 rows x 4 words: all banks)
   constexpr int VPR = OW / 8, RPP = 64 / VPR;             // lanes of a row, rows of a pass
-  constexpr int NI = FM < 3 ? FM : 3;
+  constexpr int NI = FM < 3 ? FM : FM < 8 ? 3 : 2;
   static_assert(T::W * 16 * NI * kPitch * 4 <= LDS, "the sums fit");
   const int wm = w % WR, wn = w / WR;
   const int lane = lane_id(), g = lane >> 4, l16 = lane & 15;
@@ -281,25 +296,48 @@ __device__ __forceinline__ void epilogue(MOE_LDS char* lds, const GemmBf16& p, c
   }
 }
 
+// A wave's sums of one k range as they are, for join_kernel.
+template <typename T, int FM, bool SWIGLU>
+__device__ __forceinline__ void store_part(const GemmBf16& p, const f32x4v (&acc)[FM][T::FN], int w, int r0, int rows,
+                                           int c0, int z) {
+  constexpr int FN = T::FN, WR = T::WR, kFrags = SWIGLU ? FN / 2 : FN;
+  const int wm = w % WR, wn = w / WR;
+  const int g = lane_id() >> 4, l16 = lane_id() & 15;
+  const int cols = SWIGLU ? 2 * p.N : p.N;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int row = 16 * (WR * i + wm) + l16;
+    if (row < rows) {
+      float* to = p.part + (int64_t(z) * p.capacity + r0 + row) * cols;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int o = c0 + 16 * kFrags * wn + 16 * (j % kFrags) + 4 * g;
+        if (o < p.N) *reinterpret_cast<f32x4v*>(to + (j < kFrags ? o : p.N + o)) = acc[i][j];
+      }
+    }
+  }
+}
+
 // TAIL: K is no multiple of 64, so the last stage holds fewer chunks of 8 k.
+// once: no other tile reads these columns, so they pass the caches by (32 experts
+// of 7168 x 4096, 64 rows: 282 -> 251 us; 1 x 7168 x 4096: 15.5 -> 14.6).
 template <typename T, int FM, bool SWIGLU, bool TAIL, int LDS>
-__device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, int e, int r0, int rows, int nj) {
-  constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN, KG = T::KG;
+__device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, int e, int r0, int rows, int nj,
+                                         int z, bool once) {
+  constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN;
   constexpr int BM = 16 * FM * WR;
   constexpr int kA = BM * kRowB, kStage = stage_bytes<T, FM>();
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kg = KG == 1 ? 0 : wave / W, w = wave % W, wm = w % WR, wn = w / WR;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w % WR, wn = w / WR;
   const int lane = lane_id();
   const int g = lane >> 4, l16 = lane & 15;
-  const int nk_all = (p.K + kSK - 1) / kSK;
-  const int nvalid = (p.K - (nk_all - 1) * kSK) / 8;  // chunks of the last stage (TAIL: fewer than 8)
-  const int nk = (nk_all + KG - 1) / KG;              // iterations of every group
-  const int mine = (nk_all - kg + KG - 1) / KG;       // stages of this one
+  const int last_stage = (p.K + kSK - 1) / kSK - 1;
+  const int nvalid = (p.K - last_stage * kSK) / 8;  // its chunks (TAIL: fewer than 8)
+  const int s0 = z * p.per;                         // the k range's stages
+  const int nk = min(p.per, last_stage + 1 - s0);
   constexpr int kCols = SWIGLU ? BN / 2 : BN;         // outputs of a tile
   constexpr int kFrags = SWIGLU ? FN / 2 : FN;        // fragments of a wave's outputs
   const int c0 = nj * kCols;
   const int cols = SWIGLU ? 2 * p.N : p.N;
-  MOE_LDS char* const ring = lds + kg * S * kStage;
 
   typedef LoaderA<BM, W> LA;
   typedef LoaderB<BN, W> LB;
@@ -313,27 +351,22 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   });
   const int nl = LA::count(w) + LB::count(w);
   auto issue = [&](int st) {
-    if (st < mine) {
-      MOE_LDS char* d = ring + st % S * kStage;
-      const int at = kg + KG * st;
-      if (TAIL && at == nk_all - 1) {
+    if (st < nk) {
+      MOE_LDS char* d = lds + st % S * kStage;
+      const int at = s0 + st;
+      if (TAIL && at == last_stage) {
         la.template issue<true>(d, w, at, nvalid);
-        lb.template issue<true>(d + kA, w, at, nvalid);
+        lb.template issue<true>(d + kA, w, at, nvalid, once);
       } else {
         la.template issue<false>(d, w, at, 8);
-        lb.template issue<false>(d + kA, w, at, 8);
+        lb.template issue<false>(d + kA, w, at, 8, once);
       }
     }
-  };
-  // chunks of k that stage st of this group holds
-  auto chunks = [&](int st) {
-    if (KG > 1 && st >= mine) return 0;
-    return TAIL && kg + KG * st == nk_all - 1 ? nvalid : 8;
   };
   // stage s landed for this wave; up to `last` were issued
   constexpr int kMaxAhead = (S - 1) * (LA::kPer + LB::kPer);
   auto wait_stage = [&](int s, int last) {
-    dma::wait_vm_barrier_dyn<kMaxAhead>(max(0, min(last, mine - 1) - s) * nl);
+    dma::wait_vm_barrier_dyn<kMaxAhead>(max(0, min(last, nk - 1) - s) * nl);
   };
   // fragment addresses: row 16 (WR i + wm) + l16 of A, chunk 4 q + g in k step q
   // (the swizzle does not depend on i); column block FN wn + j of W, blocks kq =
@@ -363,7 +396,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
   u32x4 a[FM], b[FN];
-  // k beyond K, or beyond the group's stages, counts as zeros on both sides
+  // k beyond K counts as zeros on both sides
   auto clear = [&] {
 #pragma unroll
     for (int i = 0; i < FM; ++i) a[i] = u32x4{0, 0, 0, 0};
@@ -374,15 +407,15 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   for (int st = 0; st < S; ++st) issue(st);
   wait_stage(0, S - 1);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) b[j] = read_b(ring, 0, j);
+  for (int j = 0; j < FN; ++j) b[j] = read_b(lds, 0, j);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) a[i] = read_a(ring, 0, i);
+  for (int i = 0; i < FM; ++i) a[i] = read_a(lds, 0, i);
 
   constexpr int kH1 = (FM + 1) / 2;
   for (int kt = 0; kt < nk; ++kt) {
-    const MOE_LDS char* cur = ring + kt % S * kStage;
-    const int have = TAIL || KG > 1 ? chunks(kt) : 8;
-    if ((TAIL || KG > 1) && have < 8 && g >= have) clear();
+    const MOE_LDS char* cur = lds + kt % S * kStage;
+    const bool tail = TAIL && s0 + kt == last_stage;
+    if (tail && g >= nvalid) clear();
     u32x4 bs[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) bs[j] = read_b(cur, 1, j);
@@ -395,7 +428,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
     alternate_mfma_reads<FM * FN, 2 * FN + FM>();
 #pragma unroll
     for (int j = 0; j < FN; ++j) b[j] = bs[j];
-    if ((TAIL || KG > 1) && have < 8 && 4 + g >= have) clear();
+    if (tail && 4 + g >= nvalid) clear();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kH1; ++i)
@@ -407,7 +440,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
     dma::wait_lgkm0();
     wait_stage(min(kt + 1, nk - 1), kt + S - 1);
     issue(kt + S);
-    const MOE_LDS char* nxt = ring + (kt + 1) % S * kStage;
+    const MOE_LDS char* nxt = lds + (kt + 1) % S * kStage;
     u32x4 bn[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) bn[j] = read_b(nxt, 0, j);
@@ -426,59 +459,35 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   }
   dma::wait_lds_barrier();  // the stages are free
 
-  if constexpr (KG > 1) {
-    // the other groups' sums into the first: [group - 1][wave][fragment][lane]
-    static_assert((KG - 1) * W * FM * FN * 1024 <= KG * S * kStage, "the sums fit the stages");
-    MOE_LDS f32x4v* const sums = (MOE_LDS f32x4v*)lds;
-    if (kg > 0) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) sums[((((kg - 1) * W + w) * FM + i) * FN + j) * 64 + lane] = acc[i][j];
-    }
-    dma::wait_lds_barrier();
-    if (kg == 0) {
-#pragma unroll
-      for (int q = 0; q < KG - 1; ++q)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] += sums[(((q * W + w) * FM + i) * FN + j) * 64 + lane];
-    }
-    dma::wait_lds_barrier();
+  if (p.ranges > 1) {
+    store_part<T, FM, SWIGLU>(p, acc, w, r0, rows, c0, z);
+    return;
   }
-  if (kg == 0) epilogue<T, FM, SWIGLU, LDS>(lds, p, acc, w, e, r0, rows, c0);
+  epilogue<T, FM, SWIGLU, LDS>(lds, p, acc, w, e, r0, rows, c0);
   dma::wait_lds_barrier();  // the next tile's loads may overwrite the stages
 }
 
-// Largest tile: 2 x 4 waves, 256 columns, blocks of up to 288 rows.
-typedef Shape<2, 4, 4, 2, 1> Big;
-constexpr int kBigFM = 9;
-// 128 rows x 128 columns, 8 waves for a group of k. Up to one tile per CU: four
-// stages (Mid), or for a long k two groups with two stages each (MidK). More
-// tiles: two stages and two workgroups per CU, so that one streams while the
-// other starts or ends a tile (Mid2).
-typedef Shape<2, 4, 2, 4, 1> Mid;
-typedef Shape<2, 4, 2, 2, 2> MidK;
-typedef Shape<2, 4, 2, 2, 1> Mid2;
+// 128 x 128, eight waves: up to one tile (or k range of one) per CU, four stages.
+// A block of fewer rows takes fewer fragments. (16 or 32 rows x 128 in 2, 4 or 8
+// waves, with up to eight stages, do no better for few rows: 1 x 7168 x 4096 in 8
+// ranges 14.6 us, 2 waves 15.7, 4 waves 16.9; 16 x 32 tiles, half lines of two
+// XCDs each, 32 in one range. Four waves of 64 x 64 for 1024 x 7168 x 4096: 85 us, eight of
+// 64 x 32: 72.)
+typedef Shape<2, 4, 2, 4> Mid;
 constexpr int kMidFM = 4;
-// Fewer tiles, whose time is the number of stages one after another: 64 x 128 in
-// two groups of 4 waves, 64 x 64 in four.
-typedef Shape<2, 2, 4, 3, 2> Mid64;
-typedef Shape<2, 2, 2, 2, 4> Small;
-constexpr int kSmallFM = 2;
-
-// Few rows, where only the weight stream counts: 16 or 32 rows x 64 columns,
-// two groups of k and two workgroups per CU, so that one streams while the
-// other starts or ends a tile (Stream; 64 rows: Stream64); with few tiles, 16
-// rows x 32 columns with eight groups (Narrow), or x 64 with four for SwiGLU.
-typedef Shape<1, 2, 2, 3, 2> Stream;
-typedef Shape<1, 2, 2, 2, 2> Stream64;  // 64 rows
-constexpr int kStreamLocal = 256;  // local experts (two workgroups fill the LDS)
-typedef Shape<1, 2, 1, 3, 8> Narrow;
-typedef Shape<1, 2, 2, 3, 4> NarrowGU;    // 16 or 32 rows
-typedef Shape<1, 2, 1, 2, 8> Narrow32;    // 32 rows x 32 columns
-typedef Shape<2, 2, 1, 3, 4> Narrow64;    // 64 rows x 32 columns
+// 256 x 128: fewer operand bytes per product, for about one such tile per CU
+// (2048 x 7168 x 4096: 124 us, Mid 146, Big 150).
+typedef Shape<4, 2, 4, 3> Tall;
+constexpr int kTallFM = 4;
+// Largest tile: 256 columns, blocks of up to 288 rows.
+typedef Shape<2, 4, 4, 2> Big;
+constexpr int kBigFM = 9;
+// Few rows and many tiles, where only the weight stream counts: 32 x 256, two
+// workgroups per CU, so that one streams while the other starts or ends a tile
+// (32 experts of 7168 x 4096, 64 / 256 rows: 254 / 300 us, 6.4 / 6.3 TB/s; Mid
+// 311 / 338).
+typedef Big Few;
+constexpr int kFewLocal = 256;  // local experts (two workgroups fill the LDS)
 
 // Row caps of the largest tile (the fewest rounds of the grid win, weighted by
 // the tallest block, as in the share's grouped GEMM); the others have one.
@@ -488,15 +497,16 @@ constexpr int kRowCapMin = 128;
 
 // MAXE: local experts its tables hold.
 template <typename T, int FMMAX, int MAXE, bool SWIGLU, bool TAIL>
-__global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmBf16 p) {
-  constexpr int kThreads = 64 * T::W * T::KG;
-  constexpr bool kVary = FMMAX == kBigFM;  // block heights vary: a row cap is chosen
+__global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
+  constexpr int kThreads = 64 * T::W;
+  static_assert(FMMAX == 1 || FMMAX == 4 || FMMAX == kBigFM, "fragments per wave row");
+  constexpr bool kVary = FMMAX == kBigFM;  // a row cap is chosen
   constexpr int kBM = 16 * FMMAX * T::WR;
-  constexpr int kLds = T::KG * T::S * stage_bytes<T, FMMAX>();
+  constexpr int kLds = T::S * stage_bytes<T, FMMAX>();
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   __shared__ int s_off[MAXE + 1];
   __shared__ int s_tpre[MAXE];
-  __shared__ int s_tmp[T::W * T::KG];
+  __shared__ int s_tmp[T::W];
   __shared__ unsigned long long s_ntile[kRowCaps];
   __shared__ int s_cand[kRowCaps];
   MOE_LDS char* lds = (MOE_LDS char*)smem;
@@ -598,8 +608,10 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmBf16 p) {
   // together, so the tiles an XCD works on at a time share both operands
   constexpr int kGroup = 8;
   const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
-  const int lo_t = int((int64_t(total) * xcd) / 8), hi_t = int((int64_t(total) * (xcd + 1)) / 8);
-  for (int tile = lo_t + int(blockIdx.x / 8); tile < hi_t; tile += per_xcd) {
+  const int64_t items = int64_t(total) * p.ranges;
+  const int lo_t = int(items * xcd / 8), hi_t = int(items * (xcd + 1) / 8);
+  for (int item = lo_t + int(blockIdx.x / 8); item < hi_t; item += per_xcd) {
+    const int z = p.ranges > 1 ? item / total : 0, tile = item - z * total;
     int e = 0, seg0 = only0, m_e = only_rows, first = 0;
     if (tables) {
       int lo = 0, hi = p.E_local - 1;
@@ -626,9 +638,19 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmBf16 p) {
     const int r0 = seg0 + mi * height;
     const int rows = min(height, seg0 + m_e - r0);
     if (rows <= 0) continue;
-    auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, kLds>(lds, p, e, r0, rows, nj); };
-    if constexpr (kVary) {
-      switch ((rows + 16 * T::WR - 1) / (16 * T::WR)) {
+    auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, kLds>(lds, p, e, r0, rows, nj, z, nrt == 1); };
+    const int fm = (rows + 16 * T::WR - 1) / (16 * T::WR);  // fragments a wave row needs
+    if constexpr (FMMAX == 1) {
+      go(std::integral_constant<int, 1>{});
+    } else if constexpr (FMMAX == 4) {
+      switch (fm) {
+        case 1: go(std::integral_constant<int, 1>{}); break;
+        case 2: go(std::integral_constant<int, 2>{}); break;
+        case 3: go(std::integral_constant<int, 3>{}); break;
+        default: go(std::integral_constant<int, 4>{}); break;
+      }
+    } else {
+      switch (fm) {
         case 1: case 2: go(std::integral_constant<int, 2>{}); break;
         case 3: case 4: go(std::integral_constant<int, 4>{}); break;
         case 5: go(std::integral_constant<int, 5>{}); break;
@@ -637,48 +659,158 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmBf16 p) {
         case 8: go(std::integral_constant<int, 8>{}); break;
         default: go(std::integral_constant<int, 9>{}); break;
       }
-    } else {
-      go(std::integral_constant<int, FMMAX>{});
     }
   }
 }
 
-// Which tiles a launch takes (names as the shapes above; 16, 32, 64: rows of a
-// block), by its sizes and the rows a segment is expected to hold.
-enum Tile { kStream16, kStream32, kStream64, kNarrow, kNarrow32, kNarrow64, kSmall, kMid64, kMid, kMidK, kMid2, kBig };
+// The ranges' sums added in order, then the epilogue. 4 outputs a thread.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(256) join_kernel(GemmBf16 p) {
+  const int nv = p.N / 4;
+  const int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = v / nv;
+  if (row >= p.capacity) return;
+  const int col = 4 * int(v - row * nv);
+  // the row's segment: the last one that starts at or before it
+  int e = 0;
+  if (p.offsets != nullptr) {
+    int lo = 0, hi = p.E_local - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.offsets[mid] <= row)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    e = lo;
+    int a, b;
+    segment(p, e, a, b);
+    if (row < a || row >= b) return;
+  }
+  constexpr int D = SWIGLU ? 2 : 1;
+  const int cols = D * p.N;
+  const float* from = p.part + row * cols + col;
+  const int64_t step = p.capacity * cols;
+  f32x4v z[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) z[d] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int q0 = 0; q0 < p.ranges; q0 += 8) {
+    f32x4v t[8][D];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (q0 + q < p.ranges) t[q][d] = *reinterpret_cast<const f32x4v*>(from + (q0 + q) * step + d * p.N);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (q0 + q < p.ranges) z[d] += t[q][d];
+  }
+  if (p.bias != nullptr)
+#pragma unroll
+    for (int d = 0; d < D; ++d) z[d] += *reinterpret_cast<const f32x4v*>(p.bias + int64_t(e) * cols + d * p.N + col);
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (SWIGLU)
+      o[i] = silu(z[0][i]) * z[D - 1][i];
+    else
+      o[i] = p.act != 0 ? activate(p.act, z[0][i]) : z[0][i];
+  }
+  const int64_t at = row * p.N + col;
+  if (p.res != nullptr) {
+    if (p.res_f32) {
+      const f32x4v r = *reinterpret_cast<const f32x4v*>(static_cast<const float*>(p.res) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += r[i];
+    } else {
+      const u32x2 r = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.res) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += i & 1 ? bf16_hi(r[i >> 1]) : bf16_lo(r[i >> 1]);
+    }
+  }
+  if (p.out_f32)
+    *reinterpret_cast<f32x4v*>(static_cast<float*>(p.C) + at) = f32x4v{o[0], o[1], o[2], o[3]};
+  else
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.C) + at) = u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
+}
 
-Tile pick_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int64_t cus) {
-  const int d = swiglu ? 2 : 1;  // columns of an output
-  const int64_t rows_hint = ceil_div(capacity, E_local);
-  // segments that can have rows
-  const int64_t active = std::min<int64_t>(E_local, capacity);
-  auto tiles = [&](int bm, int outputs) { return ceil_div(rows_hint, bm) * active * ceil_div(N, outputs); };
-  // Ragged segments spread around the expected length: twice as many rows as
-  // expected still make one block, and a block in two is a segment's last.
-  const int64_t rows = std::min(ragged ? 2 * rows_hint : rows_hint, capacity);
-  auto blocks = [&](int bm) {
-    const int64_t tall = std::min(ragged ? rows_hint + rows_hint / 4 : rows_hint, capacity);
-    return std::min(ceil_div(tall, bm) * active, ceil_div(rows_hint * active, bm) + active / 2);
+// Which tiles a launch takes (names as the shapes above), and into how many
+// ranges k is cut.
+enum Tile { kFew, kMid, kTall, kBig };
+struct Plan {
+  Tile tile;
+  int ranges;
+};
+
+// The plan of the shortest time by this model, from the sizes and the rows that a
+// segment is expected to hold (microseconds; stages of 64 k):
+//   a round of the CUs: stages x (0.48 .. 0.64 for Mid by its rows, 1.1 for Tall,
+//   1.72 (rows + 256) / 512 for Big) + 3
+//   k ranges: 2 for the second kernel, 0.06 for each, and the sums' bytes, written and
+//   read, at 7 TB/s
+//   no less than the operands' bytes at 6 TB/s
+Plan pick(bool swiglu, int E_local, int64_t capacity, int N, int K, int64_t cus) {
+  const int64_t cols = swiglu ? 2 * int64_t(N) : N, stages = ceil_div(K, kSK);
+  const bool ragged = E_local > 1;
+  const int64_t rows = ceil_div(capacity, E_local);  // expected of a segment
+  const int64_t active = std::min<int64_t>(E_local, capacity);  // segments that can have rows
+  // Ragged segments spread around the expected length; a block in two is a segment's
+  // last.
+  const int64_t tall = ragged ? std::min(rows + rows / 4, capacity) : rows;
+  auto blocks = [&](int64_t bm) {
+    const int64_t most = ceil_div(tall, bm) * active;
+    return tall <= bm ? most : std::min(most, ceil_div(rows * active, bm) + active / 2);
   };
-  const bool streams = E_local <= kStreamLocal;
-  if (rows <= 16 && streams && tiles(16, 32) > cus) return kStream16;
-  if (rows <= 32 && streams && tiles(32, 32) > cus) return kStream32;
-  if (rows <= 32) return kNarrow;
-  if (rows <= 64 && streams && tiles(64, 64 / d) > cus) return kStream64;
-  auto once = [&](int bm, int outputs) { return blocks(bm) * ceil_div(N, outputs) <= cus; };
-  if (once(16, 32)) return kNarrow;
-  if (once(32, 32)) return kNarrow32;
-  if (!swiglu && once(64, 32)) return kNarrow64;
-  if (once(64, 64 / d)) return kSmall;
-  if (once(64, 128 / d)) return kMid64;
-  const int64_t mid = blocks(128) * ceil_div(N, 128 / d);
-  if (rows_hint >= 128 && mid > 2 * cus && (K >= 1024 || mid * K >= (int64_t(5) << 19))) return kBig;
-  if (mid > cus) return kMid2;
-  return K > 1024 ? kMidK : kMid;
+  if (rows * (ragged ? 2 : 1) <= 32 && E_local <= kFewLocal && active * ceil_div(cols, 256) >= cus * 3 / 4)
+    return {kFew, 1};
+  const double least = (double(active) * K * cols + double(capacity) * K) * 2 / 6e6;
+  Plan best{kMid, 1};
+  double best_us = 1e30;
+  auto consider = [&](Tile tile, int64_t items, double per_stage, int64_t ranges) {
+    const int64_t per = ceil_div(stages, ranges), z = ceil_div(stages, per);
+    double us = double(ceil_div(items * z, cus)) * (double(per) * per_stage + 3);
+    if (z > 1) us += 2 + 0.06 * double(z) + double(z) * double(capacity) * double(cols) * 8 / 7e6;
+    us = std::max(us, least);
+    if (us < best_us * 0.999) {
+      best_us = us;
+      best = {tile, int(z)};
+    }
+  };
+  // one range, and as many as give each CU an item, of two or four stages at least
+  auto both = [&](Tile tile, int64_t items, double per_stage) {
+    consider(tile, items, per_stage, 1);
+    for (const int64_t depth : {4, 2}) {
+      const int64_t z = std::min(cus / items, stages / depth);
+      if (z > 1) consider(tile, items, per_stage, z);
+    }
+  };
+  both(kMid, blocks(128) * ceil_div(cols, 128), tall <= 32 ? 0.48 : tall <= 64 ? 0.52 : 0.64);
+  if (tall <= 128) return best;
+  both(kTall, blocks(256) * ceil_div(cols, 128), 1.1);
+  for (const int64_t cap : {288, 256, 224, 192, 160, 128}) {
+    const int64_t height = std::min<int64_t>(cap, (ceil_div(tall, ceil_div(tall, cap)) + 15) / 16 * 16);
+    consider(kBig, blocks(cap) * ceil_div(cols, 256), 1.72 * double(height + 256) / 512, 1);
+  }
+  return best;
+}
+
+Plan plan_of(const GemmBf16& p, int tile, int ranges) {
+  if (tile >= 0) return {Tile(tile), ranges};
+  return pick(p.act == 5, p.E_local, p.capacity, p.N, p.K, device_cu_count() / 8 * 8);
+}
+
+// Stages of a range, and so many ranges.
+void cut(int K, int ranges, int& per, int& n) {
+  const int stages = int(ceil_div(K, kSK));
+  per = int(ceil_div(stages, std::max(1, std::min(ranges, stages))));
+  n = int(ceil_div(stages, per));
 }
 
 template <bool SWIGLU>
-hipError_t launch(const GemmBf16& p, int forced, hipStream_t stream) {
+hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
+  cut(p.K, plan.ranges, p.per, p.ranges);
   const bool tail = p.K % kSK != 0;
   const int64_t cus = device_cu_count() / 8 * 8;
   constexpr int d = SWIGLU ? 2 : 1;
@@ -686,49 +818,49 @@ hipError_t launch(const GemmBf16& p, int forced, hipStream_t stream) {
     typedef decltype(shape) T;
     constexpr int FM = decltype(fm_t)::value, MAXE = decltype(maxe_t)::value;
     if (p.E_local > MAXE) return hipErrorInvalidValue;
-    const int64_t n = (ceil_div(p.capacity, bm) + p.E_local) * ceil_div(p.N, T::BN / d);
+    const int64_t n = (ceil_div(p.capacity, bm) + p.E_local) * ceil_div(p.N, T::BN / d) * p.ranges;
     // the kernels index tiles with 31 bits
     if (n >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     const unsigned grid = unsigned(std::max<int64_t>(8, std::min<int64_t>(cus * per_cu, ceil_div(n, 8) * 8)));
     auto* kern = tail ? tile_kernel<T, FM, MAXE, SWIGLU, true> : tile_kernel<T, FM, MAXE, SWIGLU, false>;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W * T::KG), 0, stream, p);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W), 0, stream, p);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, kMaxLocal> AnyE;
-  typedef std::integral_constant<int, kStreamLocal> StreamE;
-  typedef std::integral_constant<int, 1> One;
-  typedef std::integral_constant<int, 2> Two;
-  typedef std::integral_constant<int, 4> Four;
-  typedef std::integral_constant<int, kSmallFM> SmallFM;
-  typedef std::integral_constant<int, kMidFM> MidFM;
-  typedef std::conditional_t<SWIGLU, NarrowGU, Narrow> Narrow16;
-  switch (forced >= 0 ? forced : pick_tile(SWIGLU, p.offsets != nullptr, p.E_local, p.capacity, p.N, p.K, cus)) {
-    case kStream16: return go(Stream{}, One{}, StreamE{}, 16, 2);
-    case kStream32: return go(Stream{}, Two{}, StreamE{}, 32, 2);
-    case kStream64: return go(Stream64{}, Four{}, StreamE{}, 64, 2);
-    case kNarrow: return go(Narrow16{}, One{}, AnyE{}, 16, 1);
-    case kNarrow32: return go(std::conditional_t<SWIGLU, NarrowGU, Narrow32>{}, Two{}, AnyE{}, 32, 1);
-    case kNarrow64:
-      if constexpr (!SWIGLU) return go(Narrow64{}, Two{}, AnyE{}, 64, 1);
-      return hipErrorInvalidValue;
-    case kSmall: return go(Small{}, SmallFM{}, AnyE{}, 64, 1);
-    case kMid64: return go(Mid64{}, SmallFM{}, AnyE{}, 64, 1);
-    case kMid: return go(Mid{}, MidFM{}, AnyE{}, 128, 1);
-    case kMidK: return go(MidK{}, MidFM{}, AnyE{}, 128, 1);
-    case kMid2: return go(Mid2{}, MidFM{}, AnyE{}, 128, 2);
-    case kBig: return go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
+  hipError_t err = hipErrorInvalidValue;
+  switch (plan.tile) {
+    case kFew:
+      err = go(Few{}, std::integral_constant<int, 1>{}, std::integral_constant<int, kFewLocal>{}, 32, 2);
+      break;
+    case kMid: err = go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1); break;
+    case kTall: err = go(Tall{}, std::integral_constant<int, kTallFM>{}, AnyE{}, 256, 1); break;
+    case kBig: err = go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1); break;
   }
-  return hipErrorInvalidValue;
+  if (err == hipSuccess && p.ranges > 1) {
+    const int64_t threads = p.capacity * (p.N / 4);
+    hipLaunchKernelGGL(join_kernel<SWIGLU>, dim3(unsigned(ceil_div(threads, 256))), dim3(256), 0, stream, p);
+    err = hipGetLastError();
+  }
+  return err;
 }
 
 }  // namespace bfgemm
 
-hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream, int tile) {
-  return p.act == 5 ? bfgemm::launch<true>(p, tile, stream) : bfgemm::launch<false>(p, tile, stream);
+hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream, int tile, int ranges) {
+  const bfgemm::Plan plan = bfgemm::plan_of(p, tile, ranges);
+  return p.act == 5 ? bfgemm::launch<true>(p, plan, stream) : bfgemm::launch<false>(p, plan, stream);
 }
 
-int gemm_bf16_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int cus) {
-  return bfgemm::pick_tile(swiglu, ragged, E_local, capacity, N, K, cus);
+size_t gemm_bf16_part_bytes(const GemmBf16& p, int tile, int ranges) {
+  int per, n;
+  bfgemm::cut(p.K, bfgemm::plan_of(p, tile, ranges).ranges, per, n);
+  return n > 1 ? size_t(n) * size_t(p.capacity) * size_t(p.act == 5 ? 2 * int64_t(p.N) : p.N) * sizeof(float) : 0;
+}
+
+int gemm_bf16_plan(bool swiglu, int E_local, int64_t capacity, int N, int K, int cus, int* ranges) {
+  const bfgemm::Plan plan = bfgemm::pick(swiglu, E_local, capacity, N, K, cus);
+  *ranges = plan.ranges;
+  return plan.tile;
 }
 
 }  // namespace moe

@@ -750,7 +750,7 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
 // behind them the share's, in the form that the sizes take.
 static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
 struct LayerLayout {
-  size_t topk_idx, topk_w, share, h, rest, total;
+  size_t topk_idx, topk_w, share, h, part, part_bytes, rest, total;
 };
 static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k, int E_local) {
   LayerLayout L{};
@@ -764,6 +764,10 @@ static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k,
   L.topk_w = take(size_t(T) * k * sizeof(float));
   L.share = take(I_shared > 0 ? size_t(T) * H * sizeof(float) : 0);
   L.h = take(size_t(T) * I_shared * sizeof(uint16_t));
+  if (I_shared > 0 && T > 0)
+    L.part_bytes = std::max(moe_gemm_workspace_size(T, I_shared, H, 1, MOE_ACT_SWIGLU),
+                            moe_gemm_workspace_size(T, H, I_shared, 1, MOE_ACT_NONE));
+  L.part = take(L.part_bytes);
   L.rest = o;
   L.total = o + (layer_is_few(T, H, I, k, E_local) ? few_workspace_bytes(T, H, I, E, k, E_local)
                                                    : forward_layout(T, H, I, E, k, E_local).total);
@@ -809,7 +813,8 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
 
 static int gemm_impl(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
                      const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
-                     int out_type, int tile, hipStream_t stream) {
+                     int out_type, void* workspace, size_t workspace_bytes, hipStream_t stream, int tile = -1,
+                     int ranges = 1) {
   const int st = check_gemm(capacity, N, K, E_local, activation);
   if (st != MOE_OK) return st;
   if (!type_ok(out_type) || (residual && !type_ok(res_type)) || (!offsets && E_local != 1)) return MOE_ERR_INVALID_ARG;
@@ -817,27 +822,43 @@ static int gemm_impl(const moe_bf16* a, const moe_bf16* w, const float* bias, co
   if (!a || !w || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_gemm_bf16({a, w, bias, residual, out, offsets, capacity, E_local, K, N, activation,
-                                      res_type == MOE_TYPE_F32, out_type == MOE_TYPE_F32}, stream, tile));
+  const GemmBf16 p{a, w, bias, residual, out, offsets, capacity, E_local, K, N, activation, res_type == MOE_TYPE_F32,
+                   out_type == MOE_TYPE_F32, static_cast<float*>(workspace)};
+  const size_t need = gemm_bf16_part_bytes(p, tile, ranges);
+  if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  return hip_status(launch_gemm_bf16(p, stream, tile, ranges));
+}
+
+size_t moe_gemm_workspace_size(int64_t capacity, int N, int K, int E_local, int activation) {
+  if (check_gemm(capacity, N, K, E_local, activation) != MOE_OK || capacity == 0) return 0;
+  GemmBf16 p{};
+  p.capacity = capacity;
+  p.E_local = E_local;
+  p.K = K;
+  p.N = N;
+  p.act = activation;
+  return gemm_bf16_part_bytes(p);
 }
 
 int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
              const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
-             int out_type, hipStream_t stream) {
-  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type, -1,
-                   stream);
+             int out_type, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type,
+                   workspace, workspace_bytes, stream);
 }
 
-// moe_gemm on given tiles, and the tiles that a call takes, for the tests of every
-// kind at sizes that the rule gives to another. Not part of moe.h.
+// moe_gemm on given tiles and k ranges, and those that a call takes, for the tests
+// of every kind at sizes that the rule gives to another. Not part of moe.h.
 int moe_internal_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
                       const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
-                      int out_type, int tile, hipStream_t stream) {
-  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type, tile,
-                   stream);
+                      int out_type, int tile, int ranges, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  if (tile < 0 || ranges < 1) return MOE_ERR_INVALID_ARG;
+  return gemm_impl(a, w, bias, residual, res_type, offsets, capacity, N, K, E_local, activation, out, out_type,
+                   workspace, workspace_bytes, stream, tile, ranges);
 }
-int moe_internal_gemm_tile(int swiglu, int ragged, int E_local, int64_t capacity, int N, int K, int cus) {
-  return gemm_bf16_tile(swiglu != 0, ragged != 0, E_local, capacity, N, K, cus);
+int moe_internal_gemm_plan(int swiglu, int E_local, int64_t capacity, int N, int K, int cus, int* ranges) {
+  return gemm_bf16_plan(swiglu != 0, E_local, capacity, N, K, cus, ranges);
 }
 
 size_t moe_layer_workspace_size(int T, int H, int I, int I_shared, int E, int k, int E_local) {
@@ -921,11 +942,12 @@ int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bia
   }
   if (err == hipSuccess && shared) {
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
-    err = launch_gemm_bf16({x, w_shared_gate_up, nullptr, nullptr, h, nullptr, T, 1, H, I_shared, MOE_ACT_SWIGLU, 0, 0},
-                           stream);
+    float* gemm_part = reinterpret_cast<float*>(ws + L.part);
+    err = launch_gemm_bf16({x, w_shared_gate_up, nullptr, nullptr, h, nullptr, T, 1, H, I_shared, MOE_ACT_SWIGLU, 0, 0,
+                            gemm_part}, stream);
     if (err == hipSuccess)
-      err = launch_gemm_bf16({h, w_shared_down, nullptr, share, y, nullptr, T, 1, I_shared, H, MOE_ACT_NONE, 1, y_f32},
-                             stream);
+      err = launch_gemm_bf16({h, w_shared_down, nullptr, share, y, nullptr, T, 1, I_shared, H, MOE_ACT_NONE, 1, y_f32,
+                              gemm_part}, stream);
   }
   return hip_status(err);
 }

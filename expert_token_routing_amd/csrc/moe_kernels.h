@@ -171,10 +171,13 @@ struct GemmBf16 {
   const int32_t* offsets;
   int64_t capacity;
   int E_local, K, N, act, res_f32, out_f32;
+  float* part;             // gemm_bf16_part_bytes: [k range][capacity, columns of W]
+  int ranges = 1, per = 0; // set by the launch: k ranges, and the stages of one
 };
-// tile: one of gemm_bf16_tile's (-1: its choice for a device of `cus` CUs).
-hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream, int tile = -1);
-int gemm_bf16_tile(bool swiglu, bool ragged, int E_local, int64_t capacity, int N, int K, int cus);
+// tile, ranges: gemm_bf16_plan's (tile -1: its choice).
+hipError_t launch_gemm_bf16(const GemmBf16& p, hipStream_t stream, int tile = -1, int ranges = 1);
+size_t gemm_bf16_part_bytes(const GemmBf16& p, int tile = -1, int ranges = 1);
+int gemm_bf16_plan(bool swiglu, int E_local, int64_t capacity, int N, int K, int cus, int* ranges);
 
 // Cached device facts of the current device.
 int device_cu_count();

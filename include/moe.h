@@ -580,6 +580,10 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
  *   offsets  [E_local+1] i32 DEVICE memory as for moe_expert_ffn, or NULL with
  *            E_local = 1: all capacity rows
  *   out      [capacity, N] of out_type OUT; rows >= offsets[E_local] untouched
+ *   workspace: moe_gemm_workspace_size bytes, 256-byte aligned (0 bytes for most
+ *            sizes: NULL then): sums of k ranges, where there are fewer tiles than
+ *            CUs. No part of it needs to start at zero; calls that overlap need
+ *            workspaces of their own.
  * The order of a sum depends on the sizes, not on the other rows' values: two
  * calls with the same arguments give the same bits. An infinity or a NaN in a
  * row of a makes that row's outputs what the formula gives and touches no
@@ -588,9 +592,10 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
  * 1024 and (capacity / 16 + E_local) * C / 32 < 2^31 (rounded up), else
  * MOE_ERR_UNSUPPORTED; all pointers but offsets are 16-byte aligned.
  */
+size_t moe_gemm_workspace_size(int64_t capacity, int N, int K, int E_local, int activation);
 int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
              const int32_t* offsets, int64_t capacity, int N, int K, int E_local, int activation, void* out,
-             int out_type, hipStream_t stream);
+             int out_type, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* A layer with scored routing and an expert that every token shares.        */

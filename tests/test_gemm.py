@@ -94,35 +94,37 @@ def inputs(Mr, K, N, act, bias, res, El, integers, seed):
     return a, w, b, r
 
 
-TILES = ["stream16", "stream32", "stream64", "narrow", "narrow32", "narrow64", "small", "mid64", "mid", "midk", "mid2", "big"]
+TILES = ["few", "mid", "tall", "big"]
 
 
-def on_tile(tile, a, w, b, off, act, r, out):
+def on_tile(tile, a, w, b, off, act, r, out, ranges=1):
     """moe_gemm on given tiles (an entry point for the tests, not of the header)."""
     fn = M.lib().moe_internal_gemm
     fn.restype = ctypes.c_int
     P, I = ctypes.c_void_p, ctypes.c_int
-    fn.argtypes = [P, P, P, P, I, P, ctypes.c_int64, I, I, I, I, P, I, I, P]
+    fn.argtypes = [P, P, P, P, I, P, ctypes.c_int64, I, I, I, I, P, I, I, I, P, ctypes.c_size_t, P]
 
     def ptr(t):
         return None if t is None else t.data_ptr()
+    part = torch.full((ranges, a.shape[0], w.shape[2]), math.nan, device=a.device) if ranges > 1 else None
     st = fn(ptr(a), ptr(w), ptr(b), ptr(r), int(r is not None and r.dtype == F32), ptr(off), a.shape[0], out.shape[1],
             a.shape[1], w.shape[0], ACTS.index(act), ptr(out), int(out.dtype == F32), TILES.index(tile),
-            torch.cuda.current_stream(a.device).cuda_stream)
+            ranges, ptr(part), 0 if part is None else 4 * part.numel(), torch.cuda.current_stream(a.device).cuda_stream)
     M.check(st, f"moe_internal_gemm on {tile}")
     return out
 
 
-def run(Mr, K, N, act="none", bias=False, res=None, out=BF, El=1, offsets=None, integers=False, seed=0, tile=None):
+def run(Mr, K, N, act="none", bias=False, res=None, out=BF, El=1, offsets=None, integers=False, seed=0, tile=None,
+        ranges=1):
     say(f"gemm {Mr} x {K} x {N} act={act} bias={bias} res={res} out={out} El={El} offsets={offsets} integers={integers} "
-        f"tile={tile}")
+        f"tile={tile} ranges={ranges}")
     a, w, b, r = inputs(Mr, K, N, act, bias, res, El, integers, seed)
     off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device=a.device)
     given = torch.full((Mr, N), -77.0, dtype=out, device=a.device)
     if tile is None:
         assert M.moe_gemm(a, w, b, off, activation=act, residual=r, out=given).data_ptr() == given.data_ptr()
     else:
-        on_tile(tile, a, w, b, off, act, r, given)
+        on_tile(tile, a, w, b, off, act, r, given, ranges)
     v, tol = reference(a, w, b, off, act, r, integers)
     written = ~torch.isnan(v)
     assert torch.all(given[~written] == -77.0)
@@ -148,13 +150,16 @@ def run(Mr, K, N, act="none", bias=False, res=None, out=BF, El=1, offsets=None, 
     (dict(N=1 << 15, K=1 << 15), M.MOE_ERR_UNSUPPORTED), (dict(N=1 << 14, K=1 << 15, act=5), M.MOE_ERR_UNSUPPORTED),
     (dict(El=1025), M.MOE_ERR_UNSUPPORTED), (dict(cap=2 ** 31 - 1000), M.MOE_ERR_UNSUPPORTED),
     (dict(cap=1 << 30, N=1 << 16, K=8), M.MOE_ERR_UNSUPPORTED),
+    (dict(K=1 << 20, N=8), M.MOE_ERR_UNSUPPORTED),
+    (dict(K=7168), M.MOE_ERR_WORKSPACE), (dict(K=7168, ws=ODD, nws=1 << 30), M.MOE_ERR_WORKSPACE),
+    (dict(K=7168, ws=FAKE, nws=1024), M.MOE_ERR_WORKSPACE),
     (dict(cap=0, a=None, w=None, out=None), M.MOE_OK),
 ])
 def test_gemm_rejects(kw, want):
-    p = dict(a=FAKE, w=FAKE, bias=FAKE, res=FAKE, rt=0, offsets=FAKE, cap=16, N=64, K=64, El=1, act=0, out=FAKE, ot=0)
+    p = dict(a=FAKE, w=FAKE, bias=FAKE, res=FAKE, rt=0, offsets=FAKE, cap=16, N=64, K=64, El=1, act=0, out=FAKE, ot=0, ws=None, nws=0)
     p.update(kw)
     assert M.lib().moe_gemm(p["a"], p["w"], p["bias"], p["res"], p["rt"], p["offsets"], p["cap"], p["N"], p["K"], p["El"],
-                            p["act"], p["out"], p["ot"], None) == want
+                            p["act"], p["out"], p["ot"], p["ws"], p["nws"], None) == want
 
 
 def test_gemm_rejects_mismatched_tensors():
@@ -228,21 +233,21 @@ def test_sizes_of_layers(Mr, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("ranges", [1, 2, 3, 16])
 @pytest.mark.parametrize("tile", TILES)
-def test_every_tile(tile):
+def test_every_tile(tile, ranges):
     """Each kind of tile at sizes that the rule may give to another one: rows and columns past and
     inside a block, every end of k, fewer stages than groups of waves, several rounds of the grid."""
     for i, (Mr, K, N) in enumerate(((1, 8, 8), (5, 64, 32), (16, 72, 40), (33, 136, 72), (70, 584, 136), (130, 1032, 264),
                                     (300, 328, 520), (577, 2056, 1032))):
-        run(Mr, K, N, bias=True, res=(None, BF, F32)[i % 3], out=(BF, F32)[i % 2], integers=True, seed=i, tile=tile)
-        if tile != "narrow64":  # (32 columns hold no whole gate and up fragments of a wave there)
-            run(Mr, K, N, act="swiglu", bias=True, res=(F32, None, BF)[i % 3], out=(BF, F32)[i % 2], seed=i, tile=tile)
-        run(Mr, K, N, act="gelu", bias=True, res=BF, seed=i, tile=tile)
+        run(Mr, K, N, bias=True, res=(None, BF, F32)[i % 3], out=(BF, F32)[i % 2], integers=True, seed=i, tile=tile, ranges=ranges)
+        run(Mr, K, N, act="swiglu", bias=True, res=(F32, None, BF)[i % 3], out=(BF, F32)[i % 2], seed=i, tile=tile, ranges=ranges)
+        run(Mr, K, N, act="gelu", bias=True, res=BF, seed=i, tile=tile, ranges=ranges)
     lens = [40, 0, 3, 100, 0, 333, 7, 1]
     off = [sum(lens[:i]) for i in range(len(lens) + 1)]
-    run(off[-1] + 9, 328, 264, bias=True, res=F32, El=8, offsets=off, integers=True, tile=tile)
-    run(off[-1], 128, 264, act="none" if tile == "narrow64" else "swiglu", bias=True, El=8, offsets=off, tile=tile)
-    run(6000, 72, 2056, integers=True, tile=tile)
+    run(off[-1] + 9, 328, 264, bias=True, res=F32, El=8, offsets=off, integers=True, tile=tile, ranges=ranges)
+    run(off[-1], 128, 264, act="swiglu", bias=True, El=8, offsets=off, tile=tile, ranges=ranges)
+    run(6000, 72, 2056, integers=True, tile=tile, ranges=ranges)
 
 
 # --------------------------------------------------------------------------- #
