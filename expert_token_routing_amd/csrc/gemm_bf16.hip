@@ -321,7 +321,9 @@ __device__ __forceinline__ void store_part(const GemmBf16& p, const f32x4v (&acc
 // TAIL: K is no multiple of 64, so the last stage holds fewer chunks of 8 k.
 // once: no other tile reads these columns, so they pass the caches by (32 experts
 // of 7168 x 4096, 64 rows: 282 -> 251 us; 1 x 7168 x 4096: 15.5 -> 14.6).
-template <typename T, int FM, bool SWIGLU, bool TAIL, int LDS>
+// SPLIT: z is one of several k ranges; without, the tile is of all k, and its weights
+// take the caches.
+template <typename T, int FM, bool SWIGLU, bool TAIL, bool SPLIT, int LDS>
 __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, int e, int r0, int rows, int nj,
                                          int z, bool once) {
   constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN;
@@ -332,8 +334,8 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   const int g = lane >> 4, l16 = lane & 15;
   const int last_stage = (p.K + kSK - 1) / kSK - 1;
   const int nvalid = (p.K - last_stage * kSK) / 8;  // its chunks (TAIL: fewer than 8)
-  const int s0 = z * p.per;                         // the k range's stages
-  const int nk = min(p.per, last_stage + 1 - s0);
+  const int s0 = SPLIT ? z * p.per : 0;             // the k range's stages
+  const int nk = SPLIT ? min(p.per, last_stage + 1 - s0) : last_stage + 1;
   constexpr int kCols = SWIGLU ? BN / 2 : BN;         // outputs of a tile
   constexpr int kFrags = SWIGLU ? FN / 2 : FN;        // fragments of a wave's outputs
   const int c0 = nj * kCols;
@@ -356,10 +358,10 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
       const int at = s0 + st;
       if (TAIL && at == last_stage) {
         la.template issue<true>(d, w, at, nvalid);
-        lb.template issue<true>(d + kA, w, at, nvalid, once);
+        lb.template issue<true>(d + kA, w, at, nvalid, SPLIT && once);
       } else {
         la.template issue<false>(d, w, at, 8);
-        lb.template issue<false>(d + kA, w, at, 8, once);
+        lb.template issue<false>(d + kA, w, at, 8, SPLIT && once);
       }
     }
   };
@@ -459,7 +461,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   }
   dma::wait_lds_barrier();  // the stages are free
 
-  if (p.ranges > 1) {
+  if (SPLIT && p.ranges > 1) {
     store_part<T, FM, SWIGLU>(p, acc, w, r0, rows, c0, z);
     return;
   }
@@ -500,7 +502,7 @@ template <typename T, int FMMAX, int MAXE, bool SWIGLU, bool TAIL>
 __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
   constexpr int kThreads = 64 * T::W;
   static_assert(FMMAX == 1 || FMMAX == 4 || FMMAX == kBigFM, "fragments per wave row");
-  constexpr bool kVary = FMMAX == kBigFM;  // a row cap is chosen
+  constexpr bool kVary = FMMAX == kBigFM;  // a row cap is chosen; one k range
   constexpr int kBM = 16 * FMMAX * T::WR;
   constexpr int kLds = T::S * stage_bytes<T, FMMAX>();
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
@@ -608,10 +610,10 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
   // together, so the tiles an XCD works on at a time share both operands
   constexpr int kGroup = 8;
   const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
-  const int64_t items = int64_t(total) * p.ranges;
+  const int64_t items = kVary ? int64_t(total) : int64_t(total) * p.ranges;
   const int lo_t = int(items * xcd / 8), hi_t = int(items * (xcd + 1) / 8);
   for (int item = lo_t + int(blockIdx.x / 8); item < hi_t; item += per_xcd) {
-    const int z = p.ranges > 1 ? item / total : 0, tile = item - z * total;
+    const int z = !kVary && p.ranges > 1 ? item / total : 0, tile = item - z * total;
     int e = 0, seg0 = only0, m_e = only_rows, first = 0;
     if (tables) {
       int lo = 0, hi = p.E_local - 1;
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
     const int r0 = seg0 + mi * height;
     const int rows = min(height, seg0 + m_e - r0);
     if (rows <= 0) continue;
-    auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, kLds>(lds, p, e, r0, rows, nj, z, nrt == 1); };
+    auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, !kVary, kLds>(lds, p, e, r0, rows, nj, z, nrt == 1); };
     const int fm = (rows + 16 * T::WR - 1) / (16 * T::WR);  // fragments a wave row needs
     if constexpr (FMMAX == 1) {
       go(std::integral_constant<int, 1>{});
@@ -834,7 +836,9 @@ hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
       break;
     case kMid: err = go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1); break;
     case kTall: err = go(Tall{}, std::integral_constant<int, kTallFM>{}, AnyE{}, 256, 1); break;
-    case kBig: err = go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1); break;
+    case kBig:
+      if (p.ranges == 1) err = go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
+      break;
   }
   if (err == hipSuccess && p.ranges > 1) {
     const int64_t threads = p.capacity * (p.N / 4);
