@@ -85,8 +85,13 @@ struct Args {
   int T, H, I, E, k, e0, E_local, renormalize, y_f32;
   int polls;  // before a waiting workgroup looks for items
   void* y;
-  const int32_t* topk_idx;  // GIVEN: the selection [T, k]
+  // GIVEN: the selection [T, k - shared], and the expert that every token shares, as
+  // `shared` more experts of I beside the E_local (k counts them)
+  const int32_t* topk_idx;
   const float* topk_w;
+  int shared;
+  const uint16_t* s_gate_up;  // [H, 2 shared I]
+  const uint16_t* s_down;     // [shared I, H]
   // counters, kPitch apart
   int* queue;     // [kind][queue]: items handed out
   int* cnt_a;     // [expert][128 of I]: gate and up items done
@@ -308,15 +313,28 @@ __device__ __forceinline__ void static_for(F&& f) {
 // 16 gi + m (this wave's share of k). ready(): called once, after the first
 // weights are asked for and before the first activations.
 // Returns false, with nothing added, where ready() did.
-template <bool DOWN, int G, int D, typename Ready>
+template <bool DOWN, int G, int D, bool GIVEN, typename Ready>
 __device__ __forceinline__ bool stream(const Args& a, const Tables& s, int e, int col0, int cols, int unit0,
                                        int units, int row0, int rows, f32x4v (&acc)[G][8], Ready ready) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), g = lane >> 4, m = lane & 15;
-  const int K = DOWN ? a.I : a.H, ldw = DOWN ? a.H : 2 * a.I;
+  const int K = DOWN ? a.I : a.H;
+  int ldw = DOWN ? a.H : 2 * a.I;
+  const uint16_t* base = (DOWN ? a.w_down : a.w_gate_up) + int64_t(e) * K * ldw;
+  int64_t skip = 0;  // columns before the expert's
+  if (GIVEN && e >= a.E_local) {
+    const int j = e - a.E_local;
+    if constexpr (DOWN) {
+      base = a.s_down + int64_t(j) * K * ldw;
+    } else {
+      ldw *= a.shared;
+      skip = int64_t(j) * a.I;
+      base = a.s_gate_up + skip;
+    }
+  }
   const int col = 8 * m;
   const uint32_t wvo = col < cols ? uint32_t(8 * g * ldw + col0 + col) * 2u : kOutside;
-  const rsrc_t wr = make_rsrc((DOWN ? a.w_down : a.w_gate_up) + int64_t(e) * K * ldw, int64_t(K) * ldw * 2);
+  const rsrc_t wr = make_rsrc(base, (int64_t(K) * ldw - skip) * 2);
   // activations: x as it is (bf16), h as float32
   const rsrc_t xr = DOWN ? make_rsrc(a.h + int64_t(row0) * a.I, int64_t(rows) * a.I * 4)
                          : make_rsrc(a.x, int64_t(a.T) * a.H * 2);
@@ -466,15 +484,18 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     if (tid == 0 && my_kind < 3) asked = raise(queue(my_kind, my_queue), 1);
   };
   ask();
-  for (int i = tid; i < a.E_local; i += kThreads) s.mask[i] = 0;
+  const int n_exp = GIVEN ? a.E_local + a.shared : a.E_local;
+  for (int i = tid; i < n_exp; i += kThreads) s.mask[i] = 0;
   __syncthreads();
   if constexpr (GIVEN) {
+    const int k = a.k - a.shared;
     for (int i = tid; i < a.T * a.k; i += kThreads) {
-      const int e = a.topk_idx[i] - a.e0;
-      const bool local = e >= 0 && e < a.E_local;
+      const int t = i / a.k, j = i - t * a.k;
+      const int e = j < k ? a.topk_idx[t * k + j] - a.e0 : a.E_local + j - k;
+      const bool local = j >= k || (e >= 0 && e < a.E_local);
       s.sel[i] = int16_t(local ? e : -1);
-      s.wt[i] = a.topk_w[i];
-      if (local) atomicOr(&s.mask[e], 1u << (i / a.k));
+      s.wt[i] = j < k ? a.topk_w[t * k + j] : 1.f;
+      if (local) atomicOr(&s.mask[e], 1u << t);
     }
   } else if (a.E <= 256 && a.T > kWaves) {
     for (int t = tid >> 4; t < ((a.T + 15) & ~15); t += kThreads / 16) {
@@ -503,7 +524,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
     for (int q = 0; q < kPerT; ++q) {
       const int e = tid * kPerT + q;
-      rows[q] = e < a.E_local ? __popc(s.mask[e]) : 0;
+      rows[q] = e < n_exp ? __popc(s.mask[e]) : 0;
       sum += rows[q] * 65536 + (rows[q] > 0);
     }
     int pre = block_exclusive_scan<kThreads>(sum, s_tmp, total);
@@ -511,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
     for (int q = 0; q < kPerT; ++q) {
       const int e = tid * kPerT + q;
-      if (e < a.E_local) {
+      if (e < n_exp) {
         s.row0[e] = pre >> 16;
         if (rows[q] > 0) s.act[pre & 0xFFFF] = e;
       }
@@ -717,7 +738,8 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     const int units = min(down ? sb.units : sa.units, (down ? units_b : units_a) - unit0);
     if (!down) {
       const int block = panel < blocks ? panel : panel - blocks;
-      const int col0 = kCols * block + (panel < blocks ? 0 : a.I), cols = min(kCols, a.I - kCols * block);
+      const int up = GIVEN && e >= a.E_local ? a.shared * a.I : a.I;  // columns from gate to up
+      const int col0 = kCols * block + (panel < blocks ? 0 : up), cols = min(kCols, a.I - kCols * block);
       auto ready = [] { return true; };
       ask_next();
       auto put = [&](int gi) {
@@ -729,12 +751,12 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       };
       if (!TWO || rows <= 16) {
         f32x4v acc[1][8];
-        stream<false, 1, 4>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
+        stream<false, 1, 4, GIVEN>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
         if (!rescued) settle();
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
-        stream<false, 2, 2>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
+        stream<false, 2, 2, GIVEN>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready);
         if (!rescued) settle();
         gather_sums(s_sum, acc[0], 16, put(0));
         gather_sums(s_sum, acc[1], rows - 16, put(1));
@@ -826,7 +848,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       };
       if (!TWO || rows <= 16) {
         f32x4v acc[1][8];
-        if (!stream<true, 1, 4>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
+        if (!stream<true, 1, 4, GIVEN>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
           put_aside();
           continue;
         }
@@ -834,7 +856,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         gather_sums(s_sum, acc[0], rows, put(0));
       } else if constexpr (TWO) {
         f32x4v acc[2][8];
-        if (!stream<true, 2, 2>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
+        if (!stream<true, 2, 2, GIVEN>(a, s, e, col0, cols, unit0, units, row0, rows, acc, ready)) {
           put_aside();
           continue;
         }
@@ -862,9 +884,10 @@ inline int64_t row_ranges(int64_t cap, int T, int K, int panels) {
   const int64_t u = ceil_div(K, kSub);
   return std::min(cap * u, cap + int64_t(T) * ceil_div(kItems, panels));
 }
-inline Layout layout(int T, int H, int I, int E, int k, int E_local) {
+inline Layout layout(int T, int H, int I, int E, int k, int E_local, int shared) {
   Layout L{};
-  const int64_t cap = int64_t(T) * std::min(k, E_local), act = std::min<int64_t>(E_local, cap);
+  const int64_t picks = int64_t(T) * std::min(k, E_local), act = std::min<int64_t>(E_local, picks) + shared;
+  const int64_t cap = picks + int64_t(T) * shared;
   const int blocks = int(ceil_div(I, kCols)), pa = 2 * blocks, pb = int(ceil_div(H, kCols));
   size_t o = 0;
   auto take = [&](int64_t n) {
@@ -895,8 +918,16 @@ bool few_supported(int T, int H, int I, int k, int E_local) {
          int64_t(T) * I < (int64_t(1) << 29) && int64_t(T) * H < (int64_t(1) << 30);
 }
 
-size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local) {
-  return few::layout(T, H, I, E, k, E_local).total;
+// The shared expert's k: it goes with the others where it is a whole number of their
+// size and the tables hold it.
+int few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
+  if (I_shared <= 0 || I_shared % I != 0) return 0;
+  const int64_t n = I_shared / I;
+  return k + n <= 32 && E_local + n <= few::kMaxE && few_supported(T, H, I, int(k + n), int(E_local + n)) ? int(n) : 0;
+}
+
+size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local, int shared) {
+  return few::layout(T, H, I, E, k, E_local, shared).total;
 }
 
 namespace few {
@@ -917,23 +948,25 @@ hipError_t score(const uint16_t* x, const float* w_router, const float* bias, in
 
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
-                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream, const Choice* choice,
-                      const float* choice_bias, int32_t* topk_idx, float* topk_w) {
+                      void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream, const FewScored* sc) {
   using namespace few;
-  const Layout L = layout(T, H, I, E, k, E_local);
+  const int shared = sc ? sc->shared : 0;
+  const Layout L = layout(T, H, I, E, k, E_local, shared);
   float* logits = reinterpret_cast<float*>(ws + L.logits);
   int* ctr = reinterpret_cast<int*>(ws + L.counters);
   hipError_t err = score(x, w_router, bias, T, H, E, L, ws, stream);
-  if (err == hipSuccess && choice)
-    err = launch_select(logits, nullptr, 0, nullptr, choice_bias, T, E, k, *choice, topk_idx, topk_w, stream);
+  if (err == hipSuccess && sc)
+    err = launch_select(logits, nullptr, 0, nullptr, sc->choice_bias, T, E, k, sc->choice, sc->topk_idx, sc->topk_w, stream);
   if (err != hipSuccess) return err;
-  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, int(y_f32), polls, y, topk_idx,
-               topk_w, ctr, ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b, reinterpret_cast<float*>(ws + L.part_a),
-               reinterpret_cast<float*>(ws + L.part_b), reinterpret_cast<float*>(ws + L.h)};
+  const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k + shared, e0, E_local, renormalize, int(y_f32), polls, y,
+               sc ? sc->topk_idx : nullptr, sc ? sc->topk_w : nullptr, shared, sc ? sc->s_gate_up : nullptr,
+               sc ? sc->s_down : nullptr, ctr, ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b,
+               reinterpret_cast<float*>(ws + L.part_a), reinterpret_cast<float*>(ws + L.part_b),
+               reinterpret_cast<float*>(ws + L.h)};
   // (at least one workgroup per queue: return items are not taken from another's)
   const int grid = std::max(kQueues, workgroups > 0 ? workgroups : 2 * device_cu_count());
-  auto* kern = choice ? (T > 16 ? few_experts_kernel<true, true> : few_experts_kernel<false, true>)
-                      : (T > 16 ? few_experts_kernel<true, false> : few_experts_kernel<false, false>);
+  auto* kern = sc ? (T > 16 ? few_experts_kernel<true, true> : few_experts_kernel<false, true>)
+                  : (T > 16 ? few_experts_kernel<true, false> : few_experts_kernel<false, false>);
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(few::kThreads), 0, stream, a);
   return hipGetLastError();
 }

@@ -746,9 +746,15 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
   return MOE_OK;
 }
 
-// The layer's own buffers (selection, float32 share, the shared expert's h) and
-// behind them the share's, in the form that the sizes take.
+// The layer's own buffers (selection; where the shared expert is a product of its own,
+// the float32 share, h and the products' sums) and behind them the share's, in the form
+// that the sizes take. Up to 16 tokens that is the share for a few tokens, with the
+// shared expert among the local ones where it is a whole number of their size (DeepSeek-R1
+// TP=8 share, one token: 57 us with separate products, 44 without).
 static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
+static int layer_few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
+  return layer_is_few(T, H, I, k, E_local) ? few_shared(T, H, I, k, E_local, I_shared) : 0;
+}
 struct LayerLayout {
   size_t topk_idx, topk_w, share, h, part, part_bytes, rest, total;
 };
@@ -760,16 +766,18 @@ static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k,
     o = align_up(o + bytes);
     return at;
   };
+  const int inside = layer_few_shared(T, H, I, k, E_local, I_shared);
+  const bool apart = I_shared > 0 && inside == 0 && T > 0;
   L.topk_idx = take(size_t(T) * k * sizeof(int32_t));
   L.topk_w = take(size_t(T) * k * sizeof(float));
-  L.share = take(I_shared > 0 ? size_t(T) * H * sizeof(float) : 0);
-  L.h = take(size_t(T) * I_shared * sizeof(uint16_t));
-  if (I_shared > 0 && T > 0)
+  L.share = take(apart ? size_t(T) * H * sizeof(float) : 0);
+  L.h = take(apart ? size_t(T) * I_shared * sizeof(uint16_t) : 0);
+  if (apart)
     L.part_bytes = std::max(moe_gemm_workspace_size(T, I_shared, H, 1, MOE_ACT_SWIGLU),
                             moe_gemm_workspace_size(T, H, I_shared, 1, MOE_ACT_NONE));
   L.part = take(L.part_bytes);
   L.rest = o;
-  L.total = o + (layer_is_few(T, H, I, k, E_local) ? few_workspace_bytes(T, H, I, E, k, E_local)
+  L.total = o + (layer_is_few(T, H, I, k, E_local) ? few_workspace_bytes(T, H, I, E, k, E_local, inside)
                                                    : forward_layout(T, H, I, E, k, E_local).total);
   return L;
 }
@@ -898,14 +906,16 @@ int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bia
   char* ws = static_cast<char*>(workspace);
   int32_t* topk_idx = reinterpret_cast<int32_t*>(ws + L.topk_idx);
   float* topk_w = reinterpret_cast<float*>(ws + L.topk_w);
-  const bool y_f32 = y_type == MOE_TYPE_F32, shared = I_shared > 0;
+  const int inside = layer_few_shared(T, H, I, k, E_local, I_shared);
+  const bool y_f32 = y_type == MOE_TYPE_F32, shared = I_shared > 0 && inside == 0;
   // the share, float32 where the shared expert is added to it
   void* share = shared ? static_cast<void*>(ws + L.share) : y;
   const bool share_f32 = shared || y_f32;
   hipError_t err;
   if (layer_is_few(T, H, I, k, E_local)) {
+    const FewScored scored{c, choice_bias, topk_idx, topk_w, inside, w_shared_gate_up, w_shared_down};
     err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32, 0,
-                     kFewPolls, ws + L.rest, stream, &c, choice_bias, topk_idx, topk_w);
+                     kFewPolls, ws + L.rest, stream, &scored);
   } else {
     const ForwardLayout F = forward_layout(T, H, I, E, k, E_local);
     auto at = [&](size_t off) { return static_cast<void*>(ws + L.rest + off); };

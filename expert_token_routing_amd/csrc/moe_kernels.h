@@ -121,17 +121,27 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
 
 // The whole share for T <= 32 tokens in two kernels (few.hip). workgroups of the
 // second (0: two per CU), and polls: how often a waiting one looks before it
-// turns to other work. The results depend on neither. With a choice, a kernel
-// between the two chooses by it into topk_idx and topk_w [T, k] (renormalize is
-// then the choice's).
+// turns to other work. The results depend on neither.
 constexpr int kFewPolls = 4096;
 bool few_supported(int T, int H, int I, int k, int E_local);
-size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local);
+// With `scored`, a kernel between the two chooses by it into topk_idx and topk_w [T, k]
+// (the choice's renormalize counts), and the expert that every token shares goes with
+// the local ones, as few_shared(..) > 0 experts of I (0: none).
+struct FewScored {
+  Choice choice;
+  const float* choice_bias;
+  int32_t* topk_idx;
+  float* topk_w;
+  int shared;
+  const uint16_t* s_gate_up;
+  const uint16_t* s_down;
+};
+int few_shared(int T, int H, int I, int k, int E_local, int I_shared);
+size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local, int shared = 0);
 hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bias, const uint16_t* w_gate_up,
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
                       void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream,
-                      const Choice* choice = nullptr, const float* choice_bias = nullptr, int32_t* topk_idx = nullptr,
-                      float* topk_w = nullptr);
+                      const FewScored* scored = nullptr);
 
 // 8-bit integer products (gemm_i8.hip). Rows of x quantised with a scale each;
 // rows at and past *end (device memory; NULL, for bf16 rows: none) are left alone.

@@ -241,8 +241,9 @@ template <int EPL>
 __global__ void __launch_bounds__(kThreads) wave_kernel(Args a) {
   __shared__ Exact<EPL> s[kWaves];
   const int wv = threadIdx.x >> 6;
-  const int t = blockIdx.x * kWaves + wv;
-  if (t >= a.T) return;
+  const int64_t token = int64_t(blockIdx.x) * kWaves + wv;
+  if (token >= a.T) return;
+  const int t = int(token);
   float l[EPL];
   logits_of<EPL>(a, int64_t(t) * a.E, lane_id(), 64, (a.E - lane_id() + 63) / 64, l);
 #pragma unroll
@@ -331,9 +332,10 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   __shared__ Exact<EPL> s_exact[kWaves];
   __shared__ float s_l[kWaves][4][16 * kPitch];
   const int lane = lane_id(), r = lane & 15, row4 = lane >> 4, wv = threadIdx.x >> 6;
-  const int t0 = 4 * (blockIdx.x * kWaves + wv);
-  if (t0 >= a.T) return;
-  const bool here = t0 + row4 < a.T;
+  const int64_t first_token = 4 * (int64_t(blockIdx.x) * kWaves + wv);
+  if (first_token >= a.T) return;
+  const int t0 = int(first_token);
+  const bool here = first_token + row4 < a.T;
   const int t = here ? t0 + row4 : a.T - 1;  // (rows past the end repeat the last token and write nothing)
   const int64_t row = int64_t(t) * a.E;
   const int L = 1 << map.log_l;

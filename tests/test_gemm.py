@@ -192,6 +192,34 @@ def test_gemm_sizes_past_31_bits_are_refused():
         M.moe_gemm(big, torch.empty(1, 16, 16, dtype=BF, device="meta"))
 
 
+def plan(swiglu, E_local, capacity, N, K, cus=256):
+    fn = M.lib().moe_internal_gemm_plan
+    fn.restype, fn.argtypes = ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                             ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
+    ranges = ctypes.c_int(0)
+    return TILES[fn(int(swiglu), E_local, capacity, N, K, cus, ctypes.byref(ranges))], ranges.value
+
+
+def test_plan():
+    """Every kind of tile is some size's, k is cut into whole ranges where tiles are few, and the
+    sums of the ranges stay small."""
+    assert plan(False, 1, 1, 4096, 7168) == ("mid", 8)
+    assert plan(False, 1, 1, 7168, 256) == ("mid", 1)
+    assert plan(True, 1, 2048, 2048, 7168) == ("tall", 1)
+    assert plan(True, 1, 8192, 2048, 7168) == ("big", 1)
+    assert plan(True, 32, 256, 2048, 7168) == ("few", 1)
+    for E_local, capacity, N, K in ((1, 1, 8, 8), (1, 1, 8, (1 << 20) - 8), (1, 2 ** 31 - 2000, 8, 8), (1024, 1, 8, 8),
+                                    (1024, 3, 1032, 1032), (7, 2, 16, 7168), (1, 300, 256, 65536), (300, 300, 256, 2048),
+                                    (1, 128, 128, 520192)):
+        for swiglu in (False, True):
+            tile, ranges = plan(swiglu, E_local, capacity, N, K)
+            assert 1 <= ranges <= max(1, -(-K // 64) // 2) and (ranges == 1 or tile in ("mid", "tall"))
+            nbytes = M.gemm_workspace_size(capacity, N, K, E_local, "swiglu" if swiglu else "none")
+            assert nbytes == (0 if ranges == 1 else 4 * ranges * capacity * N * (2 if swiglu else 1))
+            assert nbytes <= 64 << 20
+    assert M.gemm_workspace_size(4, 12, 8) == 0  # (a size that the call refuses)
+
+
 # --------------------------------------------------------------------------- #
 # One matrix                                                                   #
 # --------------------------------------------------------------------------- #
@@ -373,6 +401,25 @@ def test_rows_past_32_bit_offsets(Mr, K, N):
     got = M.moe_gemm(a, w)
     for s in (slice(0, 50), slice(Mr // 2, Mr // 2 + 300), slice(Mr - 300, Mr)):
         assert torch.equal(got[s], (a[s].double() @ w[0].double()).to(BF))
+
+
+@gpu
+def test_workspaces():
+    """A given workspace of any content, too small ones refused, two calls on two streams with their own."""
+    dev = device()
+    a, w, _, _ = inputs(2, 7168, 512, "none", False, None, 1, True, 11)
+    n = M.gemm_workspace_size(2, 512, 7168)
+    assert n > 0
+    want = (a.double() @ w[0].double()).to(BF)
+    ws = [torch.full((n,), 0xFF, dtype=torch.uint8, device=dev) for _ in range(2)]
+    with pytest.raises(ValueError, match="workspace holds"):
+        M.moe_gemm(a, w, workspace=ws[0][:-256])
+    side = torch.cuda.Stream(device=dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    for _ in range(20):
+        got = [M.moe_gemm(a, w, workspace=ws[0]), M.moe_gemm(a, w, workspace=ws[1], stream=side)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
 
 
 @gpu

@@ -106,7 +106,8 @@ def test_layer_is_its_steps(case, out_dtype):
 
 @gpu
 @pytest.mark.parametrize("T", [1, 3, 16, 17, 40])
-@pytest.mark.parametrize("score,renorm,Is", [("sigmoid", True, 72), ("softmax", False, 72), ("sigmoid", False, 0)])
+@pytest.mark.parametrize("score,renorm,Is", [("sigmoid", True, 72), ("softmax", False, 72), ("sigmoid", False, 0),
+                                             ("sigmoid", True, 136), ("softmax", True, 408)])
 def test_layer_against_the_oracle(T, score, renorm, Is):
     H, I, E, El, e0, k = 192, 136, 32, 12, 8, 5
     d = weights(T, H, I, Is, E, El, 10 * T + Is)
@@ -137,9 +138,10 @@ def test_layer_against_the_oracle(T, score, renorm, Is):
 
 
 @gpu
-def test_shares_add_up_to_the_layer():
+@pytest.mark.parametrize("T,Is", [(48, 64), (7, 64), (7, 128), (16, 384)])
+def test_shares_add_up_to_the_layer(T, Is):
     """The shared expert on one of four ranks; float32 shares added."""
-    T, H, I, Is, E, k = 48, 256, 128, 64, 32, 6
+    H, I, E, k = 256, 128, 32, 6
     d = weights(T, H, I, Is, E, E, 3)
     kw = dict(score="sigmoid", n_group=8, topk_group=4, group_score="top2", out_dtype=F32)
     a = (d["x"], d["w_router"], d["bias"], d["choice_bias"])
@@ -153,9 +155,9 @@ def test_shares_add_up_to_the_layer():
 
 
 @gpu
-@pytest.mark.parametrize("T", [1, 16, 300])
-def test_layer_in_a_graph_and_on_a_stream(T):
-    H, I, Is, E, k = 256, 128, 136, 64, 8
+@pytest.mark.parametrize("T,Is", [(1, 136), (16, 136), (300, 136), (1, 128), (13, 256)])
+def test_layer_in_a_graph_and_on_a_stream(T, Is):
+    H, I, E, k = 256, 128, 64, 8
     d = weights(T, H, I, Is, E, E, T)
     kw = dict(score="sigmoid", n_group=8, topk_group=4, group_score="top2")
 
