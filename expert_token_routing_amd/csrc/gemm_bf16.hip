@@ -181,7 +181,7 @@ __device__ __forceinline__ void wave_sync() {  // LDS of one wave, written befor
 // consecutive outputs of a row, the loads and stores are whole vectors, and the
 // activation is a loop instead of a copy of its code per register. The residual of
 // the next slab is asked for before this one's sums are turned (8192 x 2048 x 7168,
-// bf16 residual: 268 -> RES us).
+// bf16 residual: 269 -> 257 us).
 // LDS: bytes there are.
 template <typename T, int FM, bool SWIGLU, int LDS>
 __device__ __forceinline__ void epilogue(MOE_LDS char* lds, const GemmBf16& p, const f32x4v (&acc)[FM][T::FN], int w,
@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
   constexpr int kThreads = 64 * T::W;
   static_assert(FMMAX == 1 || FMMAX == 4 || FMMAX == kBigFM, "fragments per wave row");
   constexpr bool kVary = FMMAX == kBigFM;  // a row cap is chosen; one k range
+  constexpr bool kHalves = kVary && MAXE == 1;
   constexpr int kBM = 16 * FMMAX * T::WR;
   constexpr int kLds = T::S * stage_bytes<T, FMMAX>();
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
   constexpr int kPerT = (MAXE + kThreads - 1) / kThreads;
   int row_cap = kBM, total = 0;
   int only0 = 0, only_rows = 0;  // the one segment of a launch without tables
-  const bool tables = p.E_local > 1;
+  const bool tables = MAXE > 1 && p.E_local > 1;
   // rounds of the grid for `tl` tiles of up to `hm` rows, weighted
   auto estimate = [&](unsigned long long tl, int hm) {
     return (tl + gridDim.x - 1) / gridDim.x * (unsigned long long)(hm + T::BN);
@@ -619,8 +620,16 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
   constexpr int kGroup = 8;
   const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
   const int64_t items = kVary ? int64_t(total) : int64_t(total) * p.ranges;
-  const int lo_t = int(items * xcd / 8), hi_t = int(items * (xcd + 1) / 8);
-  for (int item = lo_t + int(blockIdx.x / 8); item < hi_t; item += per_xcd) {
+  const int lo_t = int(items * xcd / 8), n_t = int(items * (xcd + 1) / 8) - lo_t;
+  // kHalves: a last round of no more tiles than half the CUs goes in halves of their
+  // rows (8192 x 2048 x 7168, 3.5 rounds: 231 -> 224 us, with a residual 263 -> 250.
+  // Ragged segments gain nothing and their loop grows by it: 853 -> 863 us.)
+  const int last = n_t % per_xcd;
+  const bool halves = kHalves && 2 * last <= per_xcd;
+  const int end_t = halves ? n_t + last : n_t;
+  for (int i_t = int(blockIdx.x / 8); i_t < end_t; i_t += per_xcd) {
+    const bool half = halves && i_t >= n_t - last;
+    const int item = lo_t + (half ? (n_t - last + i_t) >> 1 : i_t);
     const int z = !kVary && p.ranges > 1 ? item / total : 0, tile = item - z * total;
     int e = 0, seg0 = only0, m_e = only_rows, first = 0;
     if (tables) {
@@ -645,8 +654,17 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
     const int nj = rest / in_grp;
     const int mi = grp * kGroup + rest - nj * in_grp;
     const int height = ((m_e + nrt - 1) / nrt + 15) & ~15;
-    const int r0 = seg0 + mi * height;
-    const int rows = min(height, seg0 + m_e - r0);
+    int r0 = seg0 + mi * height;
+    int rows = min(height, seg0 + m_e - r0);
+    if (half) {
+      const int upper = min(rows, (rows / 2 + 31) & ~31);
+      if ((n_t - last + i_t) & 1) {
+        r0 += upper;
+        rows -= upper;
+      } else {
+        rows = upper;
+      }
+    }
     if (rows <= 0) continue;
     auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, !kVary, kLds>(lds, p, e, r0, rows, nj, z, nrt == 1); };
     const int fm = (rows + 16 * T::WR - 1) / (16 * T::WR);  // fragments a wave row needs
@@ -837,6 +855,7 @@ hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
     return hipGetLastError();
   };
   typedef std::integral_constant<int, kMaxLocal> AnyE;
+  typedef std::integral_constant<int, 1> OneE;
   hipError_t err = hipErrorInvalidValue;
   switch (plan.tile) {
     case kFew:
@@ -845,7 +864,9 @@ hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
     case kMid: err = go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1); break;
     case kTall: err = go(Tall{}, std::integral_constant<int, kTallFM>{}, AnyE{}, 256, 1); break;
     case kBig:
-      if (p.ranges == 1) err = go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
+      if (p.ranges == 1)
+        err = p.E_local == 1 ? go(Big{}, std::integral_constant<int, kBigFM>{}, OneE{}, kRowCapMin, 1)
+                             : go(Big{}, std::integral_constant<int, kBigFM>{}, AnyE{}, kRowCapMin, 1);
       break;
   }
   if (err == hipSuccess && p.ranges > 1) {

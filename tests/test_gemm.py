@@ -277,6 +277,15 @@ def test_every_tile(tile, ranges):
     run(6000, 72, 2056, integers=True, tile=tile, ranges=ranges)
 
 
+@gpu
+@pytest.mark.parametrize("Mr,K,N", [(3826, 72, 14592), (3350, 136, 11000), (6918, 8, 11736), (5125, 64, 12504), (2901, 264, 12544)])
+def test_last_round_in_halves(Mr, K, N):
+    """Largest tiles, some left for the last round of a grid of 256: those go in halves, the last
+    block of 6 to 242 rows among them."""
+    run(Mr, K, N, bias=True, res=BF, integers=True, tile="big")
+    run(Mr, K, N // 16 * 8, act="swiglu", res=F32, seed=1, tile="big")
+
+
 # --------------------------------------------------------------------------- #
 # Segments                                                                     #
 # --------------------------------------------------------------------------- #
