@@ -443,6 +443,9 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   // 2^-21.7; a softmax's, whose denominator is 9 additions deep, below 2^-20.
   const float s_max = a.score == 0 ? rden : __builtin_amdgcn_rcpf(1.f + exp_quick(-m));
   const float s_off = by_logit ? 0.f : s_max * (a.score == 0 ? 0x1p-20f : 0x1.4p-22f);
+  // Logits below this apart may have the same score in 64 bits, and then the lower id
+  // comes first.
+  constexpr float kSame = 0x1p-50f;
   // (scores without all their bits; infinite maxima, which the differences do not bear)
   bool unsure = !(s_max >= 0x1p-100f) || !(fabsf(m) < INFINITY);
   if (a.bias != nullptr) {
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
     // Up to two scores on both sides, a rounding of 2^-24 for each bias and sum. Equal
     // values keep more groups, and values at -infinity differ by no number.
     const float size = over<16>(fmaxf(fabsf(b1), a.rule == 0 || map.per == 1 || !(b2 > -INFINITY) ? 0.f : fabsf(b2)), Max());
-    const bool border = lanes != (a.topk_group << map.log_l) || !(lo - hi > (by_logit ? 0.f : 4.f * s_off + size * 0x1p-22f));
+    const bool border = lanes != (a.topk_group << map.log_l) || !(lo - hi > (by_logit ? kSame : 4.f * s_off + size * 0x1p-22f));
     // such tokens' groups in 64 bits, by the whole wave
     wave_sync();
     for (uint64_t todo = __ballot(border && r == 0); todo != 0; todo &= todo - 1) {
@@ -549,6 +552,8 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
       if (row4 == which && !none) v = ranked(s / z + double(a.bias[e]));
     }
   }
+  // (infinite values, whose difference is no number, among those that are never sure)
+  if (by_logit) unsure = unsure || ((__ballot(is && r > 0 && ahead != v && !(fabs(ahead - v) > kSame)) >> (16 * row4)) & 0xFFFFu) != 0;
   int rank = r;
   if (__ballot(is && r > 0 && !(peer<0x121>(v) > v)) != 0) rank = before(v, e);
   const bool chosen = is && rank < a.k;
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   // lie at most the MASK steps that a key drops above the next key's.
   const double least = over<16>(chosen ? v : INFINITY, [](double x, double y) { return fmin(x, y); });
   const float limit = value_of<MASK>(next);
-  unsure = unsure || (next != 0 && !(least > double(limit) + double(fabsf(limit) * (N == 16 ? 0x1p-14f : 0x1p-13f) + 2.f * s_off)));
+  unsure = unsure || (next != 0 && !(least > double(limit) + double(fabsf(limit) * (N == 16 ? 0x1p-14f : 0x1p-13f) + 2.f * s_off + kSame)));
   // softmax scores so far below the largest that they are equal, and sigmoids whose sum
   // would lose bits
   const float low = over<16>(chosen ? ml : INFINITY, Min());

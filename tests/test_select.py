@@ -194,6 +194,21 @@ def test_scores_that_float32_cannot_tell_apart(E):
 
 
 @gpu
+@pytest.mark.parametrize("E,G,top", [(64, 1, 1), (256, 1, 1), (256, 8, 4), (160, 8, 3), (1000, 10, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_logits_next_to_zero(E, G, top, score):
+    """Logits whose scores are equal in 64 bits, the smallest steps of float32 among them, and
+    logits 2^-30 apart, whose scores are not (but are in float32)."""
+    g = torch.Generator().manual_seed(E)
+    steps = torch.randint(-300, 300, (9, E), generator=g).double()
+    for unit in (2.0 ** -149, 2.0 ** -100, 2.0 ** -70, 2.0 ** -30):
+        l = (steps * unit).float()
+        for renorm in (True, False):
+            check(l, None, 6, score=score, n_group=G, topk_group=top, renormalize=renorm)
+        check(l, None, 6, score=score, n_group=G, topk_group=top, group_score="top2")
+
+
+@gpu
 @pytest.mark.parametrize("E,G,top", [(64, 8, 4), (256, 8, 4), (100, 4, 2)])
 def test_far_logits(E, G, top):
     logits, bias = draw(40, E, seed=9, spread=40.0)
