@@ -1,11 +1,12 @@
 // The Python side of the small calls (norms, row quantiser, 8-bit and bf16
-// products, choice of experts, the share for a few tokens), whose kernels take 4 to 20 us, less than the checks
-// and allocations around them in Python: the same checks on the tensors
-// themselves, the outputs, and the call of the C entry point. Calling thread per
-// call, ctypes -> here (a launch alone is 3.2 us): norm before the block
-// 8.4 -> 4.5 us, after it with two outputs 11.9 -> 5.4, quantiser 9 -> 5.3,
-// product 8.6 -> 4.6, few tokens 14.6 -> 8.3 (two launches), 8-bit MLPs 20.5 ->
-// 16.7 (four).
+// products, choice of experts, the share for a few tokens), whose kernels take 4
+// to 20 us, less than the checks and allocations around them in Python: the same
+// checks on the tensors themselves, the outputs, and the call of the C entry
+// point. Calling thread per call, ctypes -> here (a launch alone is 3.2 us): norm
+// before the block 8.4 -> 4.5 us, after it with two outputs 11.9 -> 5.4, quantiser
+// 9 -> 5.3, 8-bit product 8.6 -> 4.6, few tokens 14.6 -> 8.3 (two launches), 8-bit
+// MLPs 20.5 -> 16.7 (four). The later ones here alone: choice of experts 5.4, bf16
+// product 4.8, in k ranges 8.3 (two launches and a workspace).
 //
 // Each function returns None where its arguments do not fit (or the tensors
 // are not on the current device): the caller's checks then say why. A status

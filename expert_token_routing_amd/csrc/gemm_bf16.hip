@@ -12,7 +12,7 @@
 // are the first operand of v_mfma_f32_16x16x32_bf16, so a lane ends with 4
 // consecutive columns of one row.
 //
-// One kernel in four tile shapes, from 32 x 256 to 288 x 256. Where the tiles are
+// One kernel in five tile shapes, from 32 x 256 and 64 x 64 to 288 x 256. Where the tiles are
 // fewer than the CUs, k is cut into ranges whose sums a second kernel adds.
 #include "gemm_dma.h"
 #include "gemm_tile.h"
@@ -162,9 +162,10 @@ __device__ __forceinline__ void alternate_mfma_reads() {
 // WR x WC waves; a tile is 16 FM WR rows x 16 FN WC columns, S stages in LDS.
 // 16-row fragment f belongs to wave row f % WR; wave column wn holds columns 16 FN
 // wn .. (SwiGLU: 8 FN of gate, then the matching up).
-template <int WR_, int WC_, int FN_, int S_>
+// KG groups of such waves take every KG-th stage and meet in LDS at the end.
+template <int WR_, int WC_, int FN_, int S_, int KG_ = 1>
 struct Shape {
-  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_;
+  static constexpr int WR = WR_, WC = WC_, FN = FN_, S = S_, KG = KG_;
   static constexpr int W = WR * WC, BN = 16 * FN * WC;
 };
 
@@ -337,13 +338,20 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   constexpr int WR = T::WR, FN = T::FN, S = T::S, W = T::W, BN = T::BN;
   constexpr int BM = 16 * FM * WR;
   constexpr int kA = BM * kRowB, kStage = stage_bytes<T, FM>();
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w % WR, wn = w / WR;
+  constexpr int KG = T::KG;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), grp = KG > 1 ? wv / W : 0;
+  const int w = KG > 1 ? wv % W : wv, wm = w % WR, wn = w / WR;
   const int lane = lane_id();
   const int g = lane >> 4, l16 = lane & 15;
+  static_assert(KG <= 2, "their sums meet in pairs");
+  MOE_LDS char* const all = lds;
+  lds += grp * S * kStage;
   const int last_stage = (p.K + kSK - 1) / kSK - 1;
   const int nvalid = (p.K - last_stage * kSK) / 8;  // its chunks (TAIL: fewer than 8)
-  const int s0 = SPLIT ? z * p.per : 0;             // the k range's stages
-  const int nk = SPLIT ? min(p.per, last_stage + 1 - s0) : last_stage + 1;
+  const int s0 = (SPLIT ? z * p.per : 0) + grp;     // the k range's stages, the group's first
+  const int n_st = SPLIT ? min(p.per, last_stage + 1 - (s0 - grp)) : last_stage + 1;
+  const int turns = (n_st + KG - 1) / KG;           // of the first group
+  const int nk = KG > 1 ? (n_st - grp + KG - 1) / KG : n_st;
   constexpr int kCols = SWIGLU ? BN / 2 : BN;         // outputs of a tile
   constexpr int kFrags = SWIGLU ? FN / 2 : FN;        // fragments of a wave's outputs
   const int c0 = nj * kCols;
@@ -363,7 +371,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   auto issue = [&](int st) {
     if (st < nk) {
       MOE_LDS char* d = lds + st % S * kStage;
-      const int at = s0 + st;
+      const int at = s0 + st * KG;
       if (TAIL && at == last_stage) {
         la.template issue<true>(d, w, at, nvalid);
         lb.template issue<true>(d + kA, w, at, nvalid, SPLIT && once);
@@ -422,10 +430,11 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   for (int i = 0; i < FM; ++i) a[i] = read_a(lds, 0, i);
 
   constexpr int kH1 = (FM + 1) / 2;
-  for (int kt = 0; kt < nk; ++kt) {
+  for (int kt = 0; kt < turns; ++kt) {
     const MOE_LDS char* cur = lds + kt % S * kStage;
-    const bool tail = TAIL && s0 + kt == last_stage;
-    if (tail && g >= nvalid) clear();
+    const bool none = KG > 1 && kt >= nk;  // this group has no stage left
+    const bool tail = TAIL && s0 + kt * KG == last_stage;
+    if (none || (tail && g >= nvalid)) clear();
     u32x4 bs[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) bs[j] = read_b(cur, 1, j);
@@ -438,7 +447,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
     alternate_mfma_reads<FM * FN, 2 * FN + FM>();
 #pragma unroll
     for (int j = 0; j < FN; ++j) b[j] = bs[j];
-    if (tail && 4 + g >= nvalid) clear();
+    if (none || (tail && 4 + g >= nvalid)) clear();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kH1; ++i)
@@ -448,7 +457,7 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
     // this wave's reads of stage kt returned; after the barrier every wave's
     // have, and stage kt + 1 is in LDS: stage kt's buffer takes stage kt + S
     dma::wait_lgkm0();
-    wait_stage(min(kt + 1, nk - 1), kt + S - 1);
+    wait_stage(min(kt + 1, turns - 1), kt + S - 1);
     issue(kt + S);
     const MOE_LDS char* nxt = lds + (kt + 1) % S * kStage;
     u32x4 bn[FN];
@@ -468,6 +477,39 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
     __builtin_amdgcn_sched_barrier(0);
   }
   dma::wait_lds_barrier();  // the stages are free
+  // Two groups: each adds up and ends half of the rows (the first all of one fragment).
+  if constexpr (KG == 2) {
+    constexpr int HM = FM / KG == 0 ? 1 : FM / KG;
+    static_assert(FM == 1 || FM % KG == 0, "halves");
+    static_assert(KG * W * HM * FN * 1024 <= LDS, "a half's sums fit");
+    MOE_LDS f32x4v* const area = (MOE_LDS f32x4v*)all + w * HM * FN * 64 + lane;
+    constexpr int kArea = W * HM * FN * 64;
+    const bool ends = FM > 1 || grp == 0;
+    f32x4v half[HM][FN];
+#pragma unroll
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if (FM > 1 || grp > 0) area[grp * kArea + 64 * (i * FN + j)] = FM > 1 && grp == 0 ? acc[FM > 1 ? HM + i : 0][j] : acc[i][j];
+        half[i][j] = FM > 1 && grp > 0 ? acc[FM > 1 ? HM + i : 0][j] : acc[i][j];
+      }
+    dma::wait_lds_barrier();
+    if (ends)
+#pragma unroll
+      for (int i = 0; i < HM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) half[i][j] += area[(1 - grp) * kArea + 64 * (i * FN + j)];
+    dma::wait_lds_barrier();
+    const int skip = 16 * WR * HM * grp;
+    if (ends && skip < rows) {
+      if (SPLIT && p.ranges > 1)
+        store_part<T, HM, SWIGLU>(p, half, w, r0 + skip, rows - skip, c0, z);
+      else
+        epilogue<T, HM, SWIGLU, LDS / KG>(all + grp * (LDS / KG), p, half, w, e, r0 + skip, rows - skip, c0);
+    }
+    if (!(SPLIT && p.ranges > 1)) dma::wait_lds_barrier();  // the next tile's loads may overwrite it
+    return;
+  }
 
   if (SPLIT && p.ranges > 1) {
     store_part<T, FM, SWIGLU>(p, acc, w, r0, rows, c0, z);
@@ -477,16 +519,23 @@ __device__ __forceinline__ void run_tile(MOE_LDS char* lds, const GemmBf16& p, i
   dma::wait_lds_barrier();  // the next tile's loads may overwrite the stages
 }
 
-// 128 x 128, eight waves: up to one tile (or k range of one) per CU, four stages.
-// A block of fewer rows takes fewer fragments. (16 or 32 rows x 128 in 2, 4 or 8
-// waves, with up to eight stages, do no better for few rows: 1 x 7168 x 4096 in 8
-// ranges 14.6 us, 2 waves 15.7, 4 waves 16.9; 16 x 32 tiles, half lines of two
-// XCDs each, 32 in one range. Four waves of 64 x 64 for 1024 x 7168 x 4096: 85 us, eight of
-// 64 x 32: 72.)
+// 128 x 128, eight waves, four stages: blocks of 65 to 128 rows, or a few where the
+// weights are the most of it. (16 x 32 tiles for one row, half lines of two XCDs
+// each, 1 x 7168 x 4096: 32 us, ranges of this 16.6. Four waves of 64 x 64 for
+// 1024 x 7168 x 4096: 85 us, eight of 64 x 32: 72.)
 typedef Shape<2, 4, 2, 4> Mid;
 constexpr int kMidFM = 4;
+// 64 x 64 in two groups of four waves, four stages each: where larger tiles would need
+// k ranges, and so a second kernel, to be as many as the CUs, or few columns leave few
+// tiles (333 x 2880 x 1536: 17.0 us, Mid in seven ranges 19.2; 1000 x 2880 x 768: 17.4,
+// Mid 20.8; 700 x 1408 x 640: 9.6, Mid 14.8; 128 x 4096 x 1024 in 8 ranges: 11.1, Mid
+// 15.3). Four groups of two stages take 22.4 us for 512 x 2880 x 1536, three of three
+// 19.4, these 18.7.
+typedef Shape<2, 2, 2, 4, 2> Small;
+constexpr int kSmallFM = 2;
 // 256 x 128: fewer operand bytes per product, for about one such tile per CU
-// (2048 x 7168 x 4096: 124 us, Mid 146, Big 150).
+// (2048 x 7168 x 4096: 124 us, Mid 146, Big 150). Its blocks of up to 64 rows
+// stream weights as well as Mid's (1 x 7168 x 4096 in 8 ranges: 16.3, Mid 16.6).
 typedef Shape<4, 2, 4, 3> Tall;
 constexpr int kTallFM = 4;
 // Largest tile: 256 columns, blocks of up to 288 rows.
@@ -507,17 +556,17 @@ constexpr int kRowCapMin = 128;
 
 // MAXE: local experts its tables hold.
 template <typename T, int FMMAX, int MAXE, bool SWIGLU, bool TAIL>
-__global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
-  constexpr int kThreads = 64 * T::W;
-  static_assert(FMMAX == 1 || FMMAX == 4 || FMMAX == kBigFM, "fragments per wave row");
+__global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmBf16 p) {
+  constexpr int kThreads = 64 * T::W * T::KG;
+  static_assert(FMMAX == 1 || FMMAX == 2 || FMMAX == 4 || FMMAX == kBigFM, "fragments per wave row");
   constexpr bool kVary = FMMAX == kBigFM;  // a row cap is chosen; one k range
   constexpr bool kHalves = kVary && MAXE == 1;
   constexpr int kBM = 16 * FMMAX * T::WR;
-  constexpr int kLds = T::S * stage_bytes<T, FMMAX>();
+  constexpr int kLds = T::KG * T::S * stage_bytes<T, FMMAX>();
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   __shared__ int s_off[MAXE + 1];
   __shared__ int s_tpre[MAXE];
-  __shared__ int s_tmp[T::W];
+  __shared__ int s_tmp[T::W * T::KG];
   __shared__ unsigned long long s_ntile[kRowCaps];
   __shared__ int s_cand[kRowCaps];
   MOE_LDS char* lds = (MOE_LDS char*)smem;
@@ -667,9 +716,16 @@ __global__ void __launch_bounds__(64 * T::W) tile_kernel(GemmBf16 p) {
     }
     if (rows <= 0) continue;
     auto go = [&](auto fm_t) { run_tile<T, decltype(fm_t)::value, SWIGLU, TAIL, !kVary, kLds>(lds, p, e, r0, rows, nj, z, nrt == 1); };
-    const int fm = (rows + 16 * T::WR - 1) / (16 * T::WR);  // fragments a wave row needs
+    // fragments that a wave row needs (a shorter last block runs the others' code where
+    // there is little to save: fetching code of its own takes 2 us)
+    const int fm = ((kVary ? rows : height) + 16 * T::WR - 1) / (16 * T::WR);
     if constexpr (FMMAX == 1) {
       go(std::integral_constant<int, 1>{});
+    } else if constexpr (FMMAX == 2) {
+      if (fm == 1)
+        go(std::integral_constant<int, 1>{});
+      else
+        go(std::integral_constant<int, 2>{});
     } else if constexpr (FMMAX == 4) {
       switch (fm) {
         case 1: go(std::integral_constant<int, 1>{}); break;
@@ -766,7 +822,7 @@ __global__ void __launch_bounds__(256) join_kernel(GemmBf16 p) {
 
 // Which tiles a launch takes (names as the shapes above), and into how many
 // ranges k is cut.
-enum Tile { kFew, kMid, kTall, kBig };
+enum Tile { kFew, kMid, kTall, kBig, kSmall };
 struct Plan {
   Tile tile;
   int ranges;
@@ -774,11 +830,12 @@ struct Plan {
 
 // The plan of the shortest time by this model, from the sizes and the rows that a
 // segment is expected to hold (microseconds; stages of 64 k):
-//   a round of the CUs: stages x (0.48 .. 0.64 for Mid by its rows, 1.1 for Tall,
-//   1.72 (rows + 256) / 512 for Big) + 3
-//   k ranges: 2 for the second kernel, 0.06 for each, and the sums' bytes, written and
-//   read, at 7 TB/s
-//   no less than the operands' bytes at 6 TB/s
+//   a round of the CUs: stages x a time by tile and fragments, and a start and end
+//   k ranges: 1.6 for the second kernel, 0.05 for each, and the sums' bytes, written
+//   and read, at 4.4 TB/s
+//   no less than the operands' bytes at 6 TB/s, and the second kernel
+// (184 sizes of 1 to 16384 rows, every tile and up to 28 ranges of each timed: 2%
+// behind the best of them on average, one by more than 20%.)
 Plan pick(bool swiglu, int E_local, int64_t capacity, int N, int K, int64_t cus) {
   const int64_t cols = swiglu ? 2 * int64_t(N) : N, stages = ceil_div(K, kSK);
   const bool ragged = E_local > 1;
@@ -791,36 +848,35 @@ Plan pick(bool swiglu, int E_local, int64_t capacity, int N, int K, int64_t cus)
     const int64_t most = ceil_div(tall, bm) * active;
     return tall <= bm ? most : std::min(most, ceil_div(rows * active, bm) + active / 2);
   };
-  if (rows * (ragged ? 2 : 1) <= 32 && E_local <= kFewLocal && active * ceil_div(cols, 256) >= cus * 3 / 4)
-    return {kFew, 1};
   const double least = (double(active) * K * cols + double(capacity) * K) * 2 / 6e6;
   Plan best{kMid, 1};
   double best_us = 1e30;
-  auto consider = [&](Tile tile, int64_t items, double per_stage, int64_t ranges) {
+  auto consider = [&](Tile tile, int64_t tiles, int64_t places, double per_stage, double ends, int64_t ranges) {
     const int64_t per = ceil_div(stages, ranges), z = ceil_div(stages, per);
-    double us = double(ceil_div(items * z, cus)) * (double(per) * per_stage + 3);
-    if (z > 1) us += 2 + 0.06 * double(z) + double(z) * double(capacity) * double(cols) * 8 / 7e6;
-    us = std::max(us, least);
-    if (us < best_us * 0.999) {
+    double us = double(ceil_div(tiles * z, places)) * (double(per) * per_stage + ends);
+    if (z > 1) us += 1.6 + 0.05 * double(z) + double(z) * double(capacity) * double(cols) * 8 / 4.4e6;
+    us = std::max(us, z > 1 ? least + 1.6 : least) + 0.05 * us;
+    if (us < best_us) {
       best_us = us;
       best = {tile, int(z)};
     }
   };
-  // one range, and as many as give each CU an item, of two or four stages at least
-  auto both = [&](Tile tile, int64_t items, double per_stage) {
-    consider(tile, items, per_stage, 1);
-    for (const int64_t depth : {4, 2}) {
-      const int64_t z = std::min(cus / items, stages / depth);
-      if (z > 1) consider(tile, items, per_stage, z);
-    }
+  auto ranged = [&](Tile tile, int64_t tiles, int64_t places, double per_stage, double ends) {
+    // (a range has two stages at least)
+    for (const int64_t z : {1, 2, 3, 4, 5, 6, 8, 12, 16, 28})
+      if (z == 1 || z <= stages / 2) consider(tile, tiles, places, per_stage, ends, z);
   };
-  both(kMid, blocks(128) * ceil_div(cols, 128), tall <= 32 ? 0.48 : tall <= 64 ? 0.52 : 0.64);
-  if (tall <= 128) return best;
-  both(kTall, blocks(256) * ceil_div(cols, 128), 1.1);
-  for (const int64_t cap : {288, 256, 224, 192, 160, 128}) {
-    const int64_t height = std::min<int64_t>(cap, (ceil_div(tall, ceil_div(tall, cap)) + 15) / 16 * 16);
-    consider(kBig, blocks(cap) * ceil_div(cols, 256), 1.72 * double(height + 256) / 512, 1);
-  }
+  // fragments of a wave row in blocks of up to `most` rows
+  auto frags = [&](int64_t most) { return ceil_div(std::min(tall, most), most / 4); };
+  ranged(kMid, blocks(128) * ceil_div(cols, 128), cus, frags(128) == 1 ? 0.40 : frags(128) == 2 ? 0.48 : 0.65, 2.2);
+  ranged(kSmall, blocks(64) * ceil_div(cols, 64), cus, 0.28, 1.9);
+  ranged(kTall, blocks(256) * ceil_div(cols, 128), cus, frags(256) == 1 ? 0.42 : frags(256) < 4 ? 0.85 : 1.05, 1.75);
+  if (tall <= 128 && E_local <= kFewLocal) ranged(kFew, blocks(32) * ceil_div(cols, 256), 2 * cus, 1.1, 2.2);
+  if (tall > 128)
+    for (const int64_t cap : {288, 256, 224, 192, 160, 128}) {
+      const int64_t height = std::min<int64_t>(cap, (ceil_div(tall, ceil_div(tall, cap)) + 15) / 16 * 16);
+      consider(kBig, blocks(cap) * ceil_div(cols, 256), cus, 1.75 * double(height + 256) / 512, 3.8, 1);
+    }
   return best;
 }
 
@@ -851,7 +907,7 @@ hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
     if (n >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     const unsigned grid = unsigned(std::max<int64_t>(8, std::min<int64_t>(cus * per_cu, ceil_div(n, 8) * 8)));
     auto* kern = tail ? tile_kernel<T, FM, MAXE, SWIGLU, true> : tile_kernel<T, FM, MAXE, SWIGLU, false>;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W), 0, stream, p);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * T::W * T::KG), 0, stream, p);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, kMaxLocal> AnyE;
@@ -862,6 +918,7 @@ hipError_t launch(GemmBf16 p, Plan plan, hipStream_t stream) {
       err = go(Few{}, std::integral_constant<int, 1>{}, std::integral_constant<int, kFewLocal>{}, 32, 2);
       break;
     case kMid: err = go(Mid{}, std::integral_constant<int, kMidFM>{}, AnyE{}, 128, 1); break;
+    case kSmall: err = go(Small{}, std::integral_constant<int, kSmallFM>{}, AnyE{}, 64, 1); break;
     case kTall: err = go(Tall{}, std::integral_constant<int, kTallFM>{}, AnyE{}, 256, 1); break;
     case kBig:
       if (p.ranges == 1)

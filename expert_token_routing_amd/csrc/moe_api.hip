@@ -750,7 +750,7 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
 // the float32 share, h and the products' sums) and behind them the share's, in the form
 // that the sizes take. Up to 16 tokens that is the share for a few tokens, with the
 // shared expert among the local ones where it is a whole number of their size (DeepSeek-R1
-// TP=8 share, one token: 57 us with separate products, 44 without).
+// TP=8 share, one token: 58 us with separate products, 43 without).
 static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
 static int layer_few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
   return layer_is_few(T, H, I, k, E_local) ? few_shared(T, H, I, k, E_local, I_shared) : 0;

@@ -603,7 +603,7 @@ int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void
 
 /*
  * y = the rank's share of the MoE layer, routed as by moe_route_scored, plus
- * swiglu(x . w_shared_gate_up) . w_shared_down (moe_gemm):
+ * swiglu(x . w_shared_gate_up) . w_shared_down:
  *   w_shared_gate_up [H, 2 I_shared] bf16, w_shared_down [I_shared, H] bf16; both
  *   NULL with I_shared = 0: no shared expert. Under expert parallelism every
  *   token's shared expert belongs to one rank's share: give it to one of the
@@ -611,7 +611,10 @@ int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void
  *   y        [T, H] of y_type (MOE_TYPE_*), rounded once where it is bf16 and
  *            there is a shared expert or T is small (as in moe_forward_few)
  * The share is that of moe_forward_few_f32 up to 16 tokens where its limits allow, of
- * moe_forward_f32 otherwise. I_shared is a multiple of 8, H * I_shared < 2^29;
+ * moe_forward_f32 otherwise. In the first case a shared expert whose I_shared is a
+ * whole multiple of I goes with the local ones, its hidden values in float32; else
+ * it is two products of moe_gemm, its hidden values rounded to bf16 as
+ * moe_expert_ffn's are. I_shared is a multiple of 8, H * I_shared < 2^29;
  * other arguments and their checks are moe_forward's and moe_select's.
  * workspace: moe_layer_workspace_size bytes, 256-byte aligned; no part of it
  * needs to start at zero, calls that overlap need their own.

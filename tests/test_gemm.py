@@ -94,7 +94,7 @@ def inputs(Mr, K, N, act, bias, res, El, integers, seed):
     return a, w, b, r
 
 
-TILES = ["few", "mid", "tall", "big"]
+TILES = ["few", "mid", "tall", "big", "small"]
 
 
 def on_tile(tile, a, w, b, off, act, r, out, ranges=1):
@@ -203,17 +203,19 @@ def plan(swiglu, E_local, capacity, N, K, cus=256):
 def test_plan():
     """Every kind of tile is some size's, k is cut into whole ranges where tiles are few, and the
     sums of the ranges stay small."""
-    assert plan(False, 1, 1, 4096, 7168) == ("mid", 8)
-    assert plan(False, 1, 1, 7168, 256) == ("mid", 1)
+    assert plan(False, 1, 1, 4096, 7168) == ("tall", 8)
+    assert plan(False, 1, 1, 7168, 256) == ("small", 1)
+    assert plan(False, 1, 1024, 4096, 7168) == ("mid", 1)
     assert plan(True, 1, 2048, 2048, 7168) == ("tall", 1)
     assert plan(True, 1, 8192, 2048, 7168) == ("big", 1)
     assert plan(True, 32, 256, 2048, 7168) == ("few", 1)
+    assert plan(False, 1, 512, 512, 2048) == ("small", 4)
     for E_local, capacity, N, K in ((1, 1, 8, 8), (1, 1, 8, (1 << 20) - 8), (1, 2 ** 31 - 2000, 8, 8), (1024, 1, 8, 8),
                                     (1024, 3, 1032, 1032), (7, 2, 16, 7168), (1, 300, 256, 65536), (300, 300, 256, 2048),
                                     (1, 128, 128, 520192)):
         for swiglu in (False, True):
             tile, ranges = plan(swiglu, E_local, capacity, N, K)
-            assert 1 <= ranges <= max(1, -(-K // 64) // 2) and (ranges == 1 or tile in ("mid", "tall"))
+            assert 1 <= ranges <= max(1, -(-K // 64) // 2) and (ranges == 1 or tile != "big")
             nbytes = M.gemm_workspace_size(capacity, N, K, E_local, "swiglu" if swiglu else "none")
             assert nbytes == (0 if ranges == 1 else 4 * ranges * capacity * N * (2 if swiglu else 1))
             assert nbytes <= 64 << 20
