@@ -437,12 +437,16 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
 #pragma unroll
     for (int i = 0; i < Q; ++i) c[i] = __builtin_amdgcn_rcpf(1.f + exp_quick(-l[i]));
   }
-  // How far a float32 score may be from the 64-bit one, from the row's largest score: a
-  // sigmoid's exponential (its argument rounded, 2^-24 of it, and a step: together 0.35
-  // steps of 2^-23 of the score, whose slope is s (1 - s)), sum, reciprocal: below
-  // 2^-21.7; a softmax's, whose denominator is 9 additions deep, below 2^-20.
+  // How far a float32 score may be from the 64-bit one, as a part of the row's largest. A
+  // sigmoid's: the exponential is a step (2^-23) off, and its argument's rounding and the
+  // constant's are 1.22 x 2^-24 of |l|, all times 1 - s; the sum rounds by 2^-24, the
+  // reciprocal by a step. Below 0 that is (5 + 1.22 |l|) x 2^-24 of the score, at the most
+  // for the largest one; where that is above 0, 1 - s keeps all within 4 x 2^-24. A
+  // softmax's: its denominator, which is 9 additions deep and scales the whole row alike,
+  // and the rest below 2^-22.
   const float s_max = a.score == 0 ? rden : __builtin_amdgcn_rcpf(1.f + exp_quick(-m));
-  const float s_off = by_logit ? 0.f : s_max * (a.score == 0 ? 0x1p-20f : 0x1.4p-22f);
+  const float s_off =
+      by_logit ? 0.f : s_max * (a.score == 0 ? 0x1p-20f : fmaf(fmaxf(-m, 0.f), 0x1.4p-24f, 0x1.4p-22f));
   // Logits below this apart may have the same score in 64 bits, and then the lower id
   // comes first.
   constexpr float kSame = 0x1p-50f;

@@ -1,0 +1,74 @@
+"""moe_select where its float32 candidates and groups are nearly tied: inputs that
+lie next to the bounds by which it trusts a float32 value, made on the CPU, and the
+choice compared with the definition in 64 bits (tests/test_select.py's oracle)."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_select import check
+
+f32 = np.float32
+gpu = pytest.mark.gpu
+
+
+def sigmoid32(l):
+    """A sigmoid as float32 instructions form it: each step rounded to nearest (the GPU's
+    exponential and reciprocal may be a step off that)."""
+    e = np.exp2(((-l).astype(f32) * f32(1.44269504)).astype(np.float64)).astype(f32)
+    return (1 / (f32(1) + e).astype(np.float64)).astype(f32)
+
+
+def sigmoid64(l):
+    return 1 / (1 + np.exp(-l.astype(np.float64)))
+
+
+def low_pairs(level, rows, seed):
+    """Logits [rows, 4] about `level` whose first two and last two have nearly the same sum of
+    scores, in the wrong order where float32 forms it, by more than 5 steps of 2^-24 of the
+    largest score for each of the four (what four sigmoids near 1 may be off)."""
+    rng = np.random.default_rng(seed)
+    got = []
+    while sum(map(len, got)) < rows:
+        l = (level + 0.1 * rng.standard_normal((400000, 4))).astype(f32)
+        s = sigmoid64(l)
+        last = s[:, 0] + s[:, 1] - s[:, 2]
+        l = l[last > 0]
+        last = last[last > 0]
+        l[:, 3] = np.log(last / (1 - last)).astype(f32)
+        s, q = sigmoid64(l), sigmoid32(l)
+        right = (s[:, 0] + s[:, 1]) - (s[:, 2] + s[:, 3])
+        seen = (q[:, 0] + q[:, 1]).astype(np.float64) - (q[:, 2] + q[:, 3])
+        margin = 4 * s.max(1) * 5 * 2.0 ** -24 + q.max(1) * 2.0 ** -22
+        got.append(l[(right * seen < 0) & (np.abs(seen) > 1.1 * margin)])
+    return np.concatenate(got)[:rows]
+
+
+@gpu
+@pytest.mark.parametrize("level", [-13.0, -25.0, -31.0, -60.0])
+@pytest.mark.parametrize("E,G,top,at", [(4, 2, 1, (0, 1)), (32, 8, 4, (2, 6)), (60, 5, 2, (4, 1)), (256, 8, 4, (5, 3))])
+def test_groups_of_low_sigmoids(level, E, G, top, at):
+    """A sigmoid far below 0 is off by |logit| steps in float32: two groups whose sums differ by
+    less than that, at the border of those that stay."""
+    pairs = torch.from_numpy(low_pairs(level, 200, 7 + E))
+    per = E // G
+    rng = torch.Generator().manual_seed(E)
+    logits = level - 3 - torch.rand(len(pairs), E, generator=rng)
+    above = [g for g in range(G) if g not in at][: top - 1]
+    for g in above:  # groups that stay whatever the two are
+        logits[:, g * per:g * per + 2] = pairs.max(1, keepdim=True).values + 0.03
+    for g, p in zip(at, (pairs[:, :2], pairs[:, 2:])):
+        logits[:, g * per:g * per + 2] = p
+    for bias in (None, torch.zeros(E)):
+        check(logits, bias, 2 * top, score="sigmoid", n_group=G, topk_group=top, group_score="top2")
+
+
+@gpu
+@pytest.mark.parametrize("level", [-13.0, -25.0, -60.0])
+@pytest.mark.parametrize("E,k", [(256, 8), (64, 4), (100, 6)])
+def test_low_sigmoids_beside_a_bias_that_cancels_them(level, E, k):
+    """Choice values of 1e-4 of the scores, whose order float32's error of a score hides."""
+    g = torch.Generator().manual_seed(E)
+    logits = level + 1e-4 * torch.randn(300, E, generator=g)
+    bias = torch.full((E,), -float(sigmoid64(np.array([level], f32))[0]))
+    check(logits, bias, k, score="sigmoid")
+    check(logits, bias, k, score="sigmoid", n_group=4, topk_group=2, group_score="max")
