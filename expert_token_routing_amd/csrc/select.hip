@@ -484,7 +484,9 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
     const int lanes = __popc(uint32_t(__ballot(kept) >> (16 * row4)) & 0xFFFFu);
     // Up to two scores on both sides, a rounding of 2^-24 for each bias and sum. Equal
     // values keep more groups, and values at -infinity differ by no number.
-    const float size = over<16>(fmaxf(fabsf(b1), a.rule == 0 || map.per == 1 || !(b2 > -INFINITY) ? 0.f : fabsf(b2)), Max());
+    // (lanes without a group hold -infinity and count for nothing)
+    const float most = fmaxf(fabsf(b1), a.rule == 0 || map.per == 1 || !(b2 > -INFINITY) ? 0.f : fabsf(b2));
+    const float size = over<16>(real ? most : 0.f, Max());
     const bool border = lanes != (a.topk_group << map.log_l) || !(lo - hi > (by_logit ? kSame : 4.f * s_off + size * 0x1p-22f));
     // such tokens' groups in 64 bits, by the whole wave
     wave_sync();

@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+import expert_token_routing_amd as M
+from tests.gpu_helpers import device, say
 from tests.test_select import check
 
 f32 = np.float32
@@ -72,3 +74,37 @@ def test_low_sigmoids_beside_a_bias_that_cancels_them(level, E, k):
     bias = torch.full((E,), -float(sigmoid64(np.array([level], f32))[0]))
     check(logits, bias, k, score="sigmoid")
     check(logits, bias, k, score="sigmoid", n_group=4, topk_group=2, group_score="max")
+
+
+def seconds(call, times=30):
+    """Median time of one of `times` calls on an otherwise idle GPU."""
+    marks = [torch.cuda.Event(enable_timing=True) for _ in range(times + 1)]
+    for _ in range(3):
+        call()
+    marks[0].record()
+    for m in marks[1:]:
+        call()
+        m.record()
+    torch.cuda.synchronize()
+    return float(np.median([a.elapsed_time(b) for a, b in zip(marks, marks[1:])]))
+
+
+@gpu
+@pytest.mark.parametrize("G,top", [(10, 4), (5, 2), (3, 1)])
+def test_groups_that_leave_lanes_empty_are_chosen_in_float32(G, top):
+    """Only rows at the border go the 64-bit way, also where the groups are no power of two and
+    leave lanes without any: the time is not a multiple of that of a power of two (all rows in 64
+    bits: 2.6 to 3.6 times as long)."""
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(G)
+    T, per = 65536, 16
+    logits, bias = torch.randn(T, per * 16, generator=g, device=dev), 0.1 * torch.randn(per * 16, generator=g, device=dev)
+
+    def call(n_group, topk_group):
+        l, b = logits.view(-1)[:T * per * n_group].view(T, per * n_group), bias[:per * n_group]
+        return lambda: M.moe_select(l, 4, b, score="sigmoid", n_group=n_group, topk_group=topk_group, group_score="top2")
+    full = 4 if G < 8 else 16
+    say(f"times of {G} and {full} groups")
+    mine, other = seconds(call(G, top)), seconds(call(full, top))
+    print(f"{G} groups {1e3 * mine:.1f} us, {full} groups {1e3 * other:.1f} us")
+    assert mine <= 2 * other
