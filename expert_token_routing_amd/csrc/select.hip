@@ -442,8 +442,9 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   // constant's are 1.22 x 2^-24 of |l|, all times 1 - s; the sum rounds by 2^-24, the
   // reciprocal by a step. Below 0 that is (5 + 1.22 |l|) x 2^-24 of the score, at the most
   // for the largest one; where that is above 0, 1 - s keeps all within 4 x 2^-24. A
-  // softmax's: its denominator, which is 9 additions deep and scales the whole row alike,
-  // and the rest below 2^-22.
+  // softmax's: 22 x 2^-24 from the denominator (terms that are 10.6 x 2^-24 off on average at
+  // the most, for 512 experts, added 9 deep; its reciprocal), which scales the whole row alike,
+  // and 4 x 2^-24 of its own: the difference of two sums of two is at most 4 x 2^-20 off.
   const float s_max = a.score == 0 ? rden : __builtin_amdgcn_rcpf(1.f + exp_quick(-m));
   const float s_off =
       by_logit ? 0.f : s_max * (a.score == 0 ? 0x1p-20f : fmaf(fmaxf(-m, 0.f), 0x1.4p-24f, 0x1.4p-22f));
@@ -482,12 +483,13 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
     bool kept = real && above(v) < (a.topk_group << map.log_l);
     const float lo = over<16>(kept ? v : INFINITY, Min()), hi = over<16>(real && !kept ? v : -INFINITY, Max());
     const int lanes = __popc(uint32_t(__ballot(kept) >> (16 * row4)) & 0xFFFFu);
-    // Up to two scores on both sides, a rounding of 2^-24 for each bias and sum. Equal
-    // values keep more groups, and values at -infinity differ by no number.
+    // Up to two scores on both sides, and on each side a rounding of 2^-24 of a value for
+    // each bias and of up to two values for the sum: 2^-22 of the largest. Equal values keep
+    // more groups, and values at -infinity differ by no number.
     // (lanes without a group hold -infinity and count for nothing)
     const float most = fmaxf(fabsf(b1), a.rule == 0 || map.per == 1 || !(b2 > -INFINITY) ? 0.f : fabsf(b2));
     const float size = over<16>(real ? most : 0.f, Max());
-    const bool border = lanes != (a.topk_group << map.log_l) || !(lo - hi > (by_logit ? kSame : 4.f * s_off + size * 0x1p-22f));
+    const bool border = lanes != (a.topk_group << map.log_l) || !(lo - hi > (by_logit ? kSame : 4.f * s_off + size * 0x1p-21f));
     // such tokens' groups in 64 bits, by the whole wave
     wave_sync();
     for (uint64_t todo = __ballot(border && r == 0); todo != 0; todo &= todo - 1) {
