@@ -448,9 +448,10 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   const float s_max = a.score == 0 ? rden : __builtin_amdgcn_rcpf(1.f + exp_quick(-m));
   const float s_off =
       by_logit ? 0.f : s_max * (a.score == 0 ? 0x1p-20f : fmaf(fmaxf(-m, 0.f), 0x1.4p-24f, 0x1.4p-22f));
-  // Logits below this apart may have the same score in 64 bits, and then the lower id
-  // comes first.
-  constexpr float kSame = 0x1p-50f;
+  // Logits up to this apart may have the same score in 64 bits, and then the lower id
+  // comes first: their distances to the largest, below 600 where they count, round to
+  // 2^-43 (and exponentials and quotients merge what is 2^-51 apart).
+  constexpr float kSame = 0x1p-42f;
   // (scores without all their bits; infinite maxima, which the differences do not bear)
   bool unsure = !(s_max >= 0x1p-100f) || !(fabsf(m) < INFINITY);
   if (a.bias != nullptr) {

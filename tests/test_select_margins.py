@@ -108,3 +108,18 @@ def test_groups_that_leave_lanes_empty_are_chosen_in_float32(G, top):
     mine, other = seconds(call(G, top)), seconds(call(full, top))
     print(f"{G} groups {1e3 * mine:.1f} us, {full} groups {1e3 * other:.1f} us")
     assert mine <= 2 * other
+
+
+@gpu
+@pytest.mark.parametrize("E,G,top", [(64, 1, 1), (256, 8, 4), (160, 8, 3), (1000, 10, 4)])
+@pytest.mark.parametrize("largest", [17.0, 500.0])
+def test_logits_that_their_distance_to_the_largest_makes_equal(E, G, top, largest):
+    """exp(l - m) of logits next to 0: l - m rounds to 2^-49 at 17 and to 2^-44 at 500, so logits
+    less than that apart have the same score in 64 bits and go by id."""
+    g = torch.Generator().manual_seed(E)
+    steps = torch.randint(-3, 4, (60, E), generator=g).double()
+    for unit in (2.0 ** -51, 2.0 ** -49, 2.0 ** -46, 2.0 ** -44, 2.0 ** -42):
+        l = (steps * unit).float()
+        l[:, 5] = largest
+        for renorm in (True, False):
+            check(l, None, 6, n_group=G, topk_group=top, renormalize=renorm)
