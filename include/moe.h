@@ -530,7 +530,9 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
  *            renormalize divided by the sum of the k scores.
  * Equal values put the lower group and the lower expert first. The choice is
  * that of the values in 64 bits: scores that differ by less than float32 tells
- * apart are still told apart.
+ * apart are still told apart. Weights are formed in 64 bits and rounded once
+ * (2^-24); of a softmax without renormalize the denominator's terms are float32,
+ * which makes it 4 x 2^-24.
  *   logits [T, E] f32, bias [E] f32: at any float address.
  * A NaN logit counts as -infinity, a NaN choice value or group value too (the ids
  * are distinct and in [0, E) whatever the inputs hold). A token without a

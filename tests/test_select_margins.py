@@ -7,7 +7,7 @@ import torch
 
 import expert_token_routing_amd as M
 from tests.gpu_helpers import device, say
-from tests.test_select import check
+from tests.test_select import check, oracle
 
 f32 = np.float32
 gpu = pytest.mark.gpu
@@ -123,3 +123,25 @@ def test_logits_that_their_distance_to_the_largest_makes_equal(E, G, top, larges
         l[:, 5] = largest
         for renorm in (True, False):
             check(l, None, 6, n_group=G, topk_group=top, renormalize=renorm)
+
+
+@gpu
+@pytest.mark.parametrize("E,G,top,k", [(64, 1, 1, 4), (256, 8, 4, 8), (160, 8, 3, 6), (99, 3, 2, 12),
+                                       (512, 1, 1, 16), (1000, 10, 4, 12)])
+@pytest.mark.parametrize("spread", [0.01, 1.0, 8.0])
+def test_weights_of_a_softmax_over_all_experts(E, G, top, k, spread):
+    """Without renormalisation the denominator counts. Its terms' exponentials may be a step
+    (2 x 2^-24) off and round once more, the weight rounds once: 4 x 2^-24, whatever kernel and
+    way the sizes take."""
+    g = torch.Generator().manual_seed(E)
+    logits = spread * torch.randn(300, E, generator=g)
+    logits[0, 1::2] = -float("inf")
+    logits[1, ::3] = float("nan")
+    logits[2] = 0.25
+    logits[3] += 1000.0
+    for bias in (None, 0.01 * torch.randn(E, generator=g)):
+        for rule in ("max", "top2"):
+            kw = dict(n_group=G, topk_group=top, group_score=rule, renormalize=False, scale=1.0)
+            _, w = check(logits, bias, k, **kw)
+            _, want = oracle(logits.numpy(), None if bias is None else bias.numpy(), k, **kw)
+            assert np.all(np.abs(w.cpu().numpy() - want) <= 4.1 * 2.0 ** -24 * want + 2.0 ** -126)
