@@ -145,3 +145,19 @@ def test_weights_of_a_softmax_over_all_experts(E, G, top, k, spread):
             _, w = check(logits, bias, k, **kw)
             _, want = oracle(logits.numpy(), None if bias is None else bias.numpy(), k, **kw)
             assert np.all(np.abs(w.cpu().numpy() - want) <= 4.1 * 2.0 ** -24 * want + 2.0 ** -126)
+
+
+@gpu
+@pytest.mark.parametrize("E,G,top", [(64, 1, 1), (256, 8, 4), (100, 5, 3), (1000, 10, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_bias_does_not_bring_a_nan_logit_back(E, G, top, score):
+    """A logit of -infinity has score 0 and its bias; one that is NaN has no choice value at all."""
+    g = torch.Generator().manual_seed(E)
+    logits, bias = torch.randn(20, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    per = E // G
+    logits[:, 3], logits[:, per // 2] = float("nan"), float("nan")
+    logits[:, 4] = -float("inf")
+    bias[3], bias[4], bias[per // 2] = 9.0, 8.0, 7.0
+    for rule in ("max", "top2"):
+        idx, _ = check(logits, bias, 4, score=score, n_group=G, topk_group=top, group_score=rule)
+        assert bool((idx[:, 0] == 4).all()) and not bool(((idx == 3) | (idx == per // 2)).any())
