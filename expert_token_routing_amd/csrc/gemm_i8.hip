@@ -437,9 +437,9 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
       unsigned long long best = ~0ull;
 #pragma unroll
       for (int c = 0; c < kRowCaps; ++c) {
-        const int nrt = max(1, (only_rows + kRowCap[c] - 1) / kRowCap[c]);
+        const int nrt = max(1, row_blocks(only_rows, kRowCap[c]));
         const unsigned long long tl = (unsigned long long)nrt * (unsigned long long)ntn;
-        const int hm = (((only_rows + nrt - 1) / nrt) + 15) & ~15;
+        const int hm = block_height(only_rows, nrt);
         const unsigned long long est = (tl + gridDim.x - 1) / gridDim.x * (unsigned long long)(hm + T::BN);
         if (tl < (1ull << 31) && est < best) {
           best = est;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
         }
       }
     }
-    total = (only_rows + row_cap - 1) / row_cap * ntn;
+    total = row_blocks(only_rows, row_cap) * ntn;
   } else {
   int me[kPerT];
 #pragma unroll
@@ -475,9 +475,9 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
 #pragma unroll
       for (int q = 0; q < kPerT; ++q) {
         if (me[q] > 0) {
-          const int nrt = (me[q] + kRowCap[c] - 1) / kRowCap[c];
+          const int nrt = row_blocks(me[q], kRowCap[c]);
           tl += (unsigned long long)nrt * (unsigned long long)ntn;
-          hm = max(hm, (((me[q] + nrt - 1) / nrt) + 15) & ~15);
+          hm = max(hm, block_height(me[q], nrt));
         }
       }
       if (tl > 0) atomicAdd(&s_ntile[c], tl);
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
   int sum = 0;
 #pragma unroll
   for (int q = 0; q < kPerT; ++q) {
-    mt[q] = (me[q] + row_cap - 1) / row_cap * ntn;
+    mt[q] = row_blocks(me[q], row_cap) * ntn;
     sum += mt[q];
   }
   int pre = block_exclusive_scan<kThreads>(sum, s_tmp, total);
@@ -536,14 +536,14 @@ __global__ void __launch_bounds__(64 * T::W * T::KG) tile_kernel(GemmArgs p) {
       m_e = __builtin_amdgcn_readfirstlane(s_off[e + 1]) - seg0;
       first = __builtin_amdgcn_readfirstlane(s_tpre[e]);
     }
-    const int nrt = (m_e + row_cap - 1) / row_cap;
+    const int nrt = row_blocks(m_e, row_cap);
     const int local = tile - first;
     const int grp = local / (kGroup * ntn);
     const int in_grp = min(kGroup, nrt - grp * kGroup);
     const int rest = local - grp * kGroup * ntn;
     const int nj = rest / in_grp;
     const int mi = grp * kGroup + rest - nj * in_grp;
-    const int height = ((m_e + nrt - 1) / nrt + 15) & ~15;
+    const int height = block_height(m_e, nrt);
     const int r0 = seg0 + mi * height;
     const int rows = min(height, seg0 + m_e - r0);
     if (rows <= 0) continue;

@@ -537,6 +537,14 @@ static ForwardI8Layout forward_i8_layout(int T, int H, int I, int E, int k, int 
 
 extern "C" {
 
+// The row blocks of the grouped products, for the tests of sizes next to 2^31. Not part
+// of moe.h.
+int moe_internal_row_blocks(int rows, int cap, int* height) {
+  const int n = row_blocks(rows, cap);
+  *height = block_height(rows, std::max(n, 1));
+  return n;
+}
+
 // The tiles of a product, for the tests of the rule. Not part of moe.h.
 int moe_internal_i8_tile(int swiglu, int ragged, int E_local, int64_t capacity, int N, int K, int64_t rows_hint,
                          int cus) {
