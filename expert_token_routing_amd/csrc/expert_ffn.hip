@@ -465,7 +465,7 @@ panel_gemm_kernel(const uint16_t* __restrict__ A, int lda, const int32_t* __rest
       if (me[q] > 0) {
         const int nrt = (me[q] + kRowCap[c] - 1) / kRowCap[c];
         tl += (unsigned long long)nrt * (unsigned long long)ntn;
-        hm = max(hm, (((me[q] + nrt - 1) / nrt) + 15) & ~15);
+        hm = max(hm, block_height(me[q], nrt));
       }
     }
     if (tl > 0) atomicAdd(&s_ntile[c], tl);
@@ -527,7 +527,7 @@ panel_gemm_kernel(const uint16_t* __restrict__ A, int lda, const int32_t* __rest
     const int local = tile - t0;
     const int nj = local / nrt;
     const int mi = local - nj * nrt;
-    const int height = ((m_e + nrt - 1) / nrt + 15) & ~15;
+    const int height = block_height(m_e, nrt);
     const int r0 = seg0 + mi * height;
     const int rows = min(height, seg0 + m_e - r0);
     if (rows <= 0) continue;

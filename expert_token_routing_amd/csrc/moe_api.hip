@@ -73,6 +73,8 @@ static int check_local(int E, int e0, int E_local) {
   return MOE_OK;
 }
 static int64_t min_capacity(int T, int k, int E_local) { return int64_t(T) * std::min(k, E_local); }
+// Rows of the grouped GEMMs, which round them up to blocks in an int.
+static bool rows_fit(int64_t rows) { return rows < (int64_t(1) << 31) - 1024; }
 // The GEMMs address one expert's weight matrix through a buffer resource
 // whose range and offsets are 32-bit: gate_up (H x 2I bf16, the larger of the
 // two) must stay below 2 GiB, i.e. H * I < 2^29.
@@ -187,7 +189,7 @@ int moe_expert_ffn(const moe_bf16* x_perm, const int32_t* offsets, const moe_bf1
                    moe_bf16* out, hipStream_t stream) {
   if (H <= 0 || I <= 0 || (H % 8) != 0 || (I % 8) != 0 || E_local < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
   if (E_local > kMaxE || !expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
-  if (capacity >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!rows_fit(capacity)) return MOE_ERR_UNSUPPORTED;
   if (capacity == 0) return MOE_OK;
   if (!x_perm || !offsets || !w_gate_up || !w_down || !h || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_perm) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(h) || !aligned16(out))
@@ -237,7 +239,7 @@ static int forward_impl(const moe_bf16* x, const float* w_router, const float* b
   if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
   if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
   if (!expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
-  if (min_capacity(T, k, E_local) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!rows_fit(min_capacity(T, k, E_local))) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y))
@@ -420,7 +422,7 @@ static int check_i8(int K, int64_t channels) {
 // Rows and tiles of a grouped product are counted with 31 bits: at the smallest
 // blocks (16 rows) and narrowest tiles (32 channels).
 static bool i8_rows_fit(int64_t capacity, int E_local, int64_t channels) {
-  return capacity < (int64_t(1) << 31) - 1024 &&
+  return rows_fit(capacity) &&
          (ceil_div(capacity, 16) + E_local) * ceil_div(channels, 32) < (int64_t(1) << 31);
 }
 
@@ -694,7 +696,7 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
   int st = check_route_dims(T, H, E, k);
   if (st != MOE_OK) return st;
   if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
-  if (!expert_weights_fit(H, I) || min_capacity(T, k, E) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!expert_weights_fit(H, I) || !rows_fit(min_capacity(T, k, E))) return MOE_ERR_UNSUPPORTED;
   if ((st = check_post(r_type, MOE_TYPE_F32, gate, gate_kind, w_next, normed, T, H, eps)) != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!residual || !w_pre || !w_router || !w_gate_up || !w_down || !out) return MOE_ERR_INVALID_ARG;
@@ -893,8 +895,7 @@ int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bia
   if (st != MOE_OK) return st;
   if ((st = check_choice(T, E, k, c)) != MOE_OK || (st = check_local(E, e0, E_local)) != MOE_OK) return st;
   if (I <= 0 || (I % 8) != 0 || I_shared < 0 || (I_shared % 8) != 0 || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
-  if (!expert_weights_fit(H, I) || !expert_weights_fit(H, I_shared) ||
-      min_capacity(T, k, E_local) >= (int64_t(1) << 31))
+  if (!expert_weights_fit(H, I) || !expert_weights_fit(H, I_shared) || !rows_fit(min_capacity(T, k, E_local)))
     return MOE_ERR_UNSUPPORTED;
   if (I_shared > 0) {
     if ((st = check_gemm(T, I_shared, H, 1, MOE_ACT_SWIGLU)) != MOE_OK) return st;

@@ -13,13 +13,11 @@ constexpr int kChunk = 64;  // tokens per dispatch chunk (one wave)
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A segment of `rows` rows (any int) in blocks of at most `cap`, a multiple of 16: so
-// many, of such a height, a multiple of 16 too (the last is shorter, or empty). Next to
-// 2^31 the sums in between need 32 bits without a sign.
-__host__ __device__ inline int row_blocks(int rows, int cap) { return int((unsigned(rows) + unsigned(cap) - 1u) / unsigned(cap)); }
-__host__ __device__ inline int block_height(int rows, int blocks) {
-  return int(((unsigned(rows) + unsigned(blocks) - 1u) / unsigned(blocks) + 15u) & ~15u);
-}
+// A segment of `rows` rows in blocks of at most `cap`, a multiple of 16: so many, of such
+// a height, a multiple of 16 too (the last is shorter, or empty). No sum passes an int,
+// whatever the rows.
+__host__ __device__ inline int row_blocks(int rows, int cap) { return rows > 0 ? (rows - 1) / cap + 1 : 0; }
+__host__ __device__ inline int block_height(int rows, int blocks) { return ((rows - 1) / blocks + 16) & ~15; }
 
 // How experts are chosen from scores (select.hip); the numbers are MOE_SCORE_*
 // and MOE_GROUP_*.

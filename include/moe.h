@@ -163,6 +163,8 @@ int moe_dispatch(const moe_bf16* x, const int32_t* topk_idx, int T, int H, int E
  *   w_down    [E_local, I, H]  bf16
  *   h         [capacity, I] bf16   OUT (intermediate activations)
  *   out       [capacity, H] bf16   OUT; rows >= offsets[E_local] untouched
+ * capacity < 2^31 - 1024 (so T * min(k, E_local) of the calls that run these MLPs),
+ * else MOE_ERR_UNSUPPORTED.
  */
 int moe_expert_ffn(const moe_bf16* x_perm, const int32_t* offsets, const moe_bf16* w_gate_up,
                    const moe_bf16* w_down, int H, int I, int E_local, int64_t capacity,

@@ -30,6 +30,14 @@ def test_blocks_cover_every_segment(cap):
         assert n * h >= rows and (n - 1) * h <= top, rows
 
 
+@pytest.mark.parametrize("rows", [2 ** 31 - 1024, 2 ** 31 - 1, 2 ** 31])
+def test_rows_that_blocks_do_not_take_are_refused(rows):
+    p = ctypes.c_void_p(0x10000)
+    L = M.lib()
+    assert L.moe_expert_ffn(p, p, p, p, 32, 32, 4, rows, p, p, None) == M.MOE_ERR_UNSUPPORTED
+    assert L.moe_gemm(p, p, None, None, 0, None, rows, 8, 8, 1, 0, p, 0, None, 0, None) == M.MOE_ERR_UNSUPPORTED
+
+
 def far(M_rows, K, N, dtype):
     """A row pattern of 2^20 rows, repeated over `M_rows` rows."""
     dev = device()
