@@ -884,17 +884,19 @@ size_t moe_layer_workspace_size(int T, int H, int I, int I_shared, int E, int k,
   return layer_layout(T, H, I, I_shared, E, k, E_local).total;
 }
 
-int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+static int layer_impl(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
                       const moe_bf16* w_gate_up, const moe_bf16* w_down, const moe_bf16* w_shared_gate_up,
                       const moe_bf16* w_shared_down, int T, int H, int I, int I_shared, int E, int k, int e0,
                       int E_local, int score, int n_group, int topk_group, int group_rule, int renormalize,
-                      float scale, void* y, int y_type, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                      float scale, void* y, int y_type, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                      int workgroups = 0, int polls = kFewPolls) {
   const Choice c{score, n_group, topk_group, group_rule, renormalize, scale};
   // every step's checks before the first launch
   int st = check_route_dims(T, H, E, k);
   if (st != MOE_OK) return st;
   if ((st = check_choice(T, E, k, c)) != MOE_OK || (st = check_local(E, e0, E_local)) != MOE_OK) return st;
-  if (I <= 0 || (I % 8) != 0 || I_shared < 0 || (I_shared % 8) != 0 || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
+  if (I <= 0 || (I % 8) != 0 || I_shared < 0 || (I_shared % 8) != 0 || !type_ok(y_type) || workgroups < 0 || polls < 1)
+    return MOE_ERR_INVALID_ARG;
   if (!expert_weights_fit(H, I) || !expert_weights_fit(H, I_shared) || !rows_fit(min_capacity(T, k, E_local)))
     return MOE_ERR_UNSUPPORTED;
   if (I_shared > 0) {
@@ -923,8 +925,8 @@ int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bia
   hipError_t err;
   if (layer_is_few(T, H, I, k, E_local)) {
     const FewScored scored{c, choice_bias, topk_idx, topk_w, inside, w_shared_gate_up, w_shared_down};
-    err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32, 0,
-                     kFewPolls, ws + L.rest, stream, &scored);
+    err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32,
+                     workgroups, polls, ws + L.rest, stream, &scored);
   } else {
     const ForwardLayout F = forward_layout(T, H, I, E, k, E_local);
     auto at = [&](size_t off) { return static_cast<void*>(ws + L.rest + off); };
@@ -969,6 +971,29 @@ int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bia
                               gemm_part}, stream);
   }
   return hip_status(err);
+}
+
+int moe_layer_forward(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+                      const moe_bf16* w_gate_up, const moe_bf16* w_down, const moe_bf16* w_shared_gate_up,
+                      const moe_bf16* w_shared_down, int T, int H, int I, int I_shared, int E, int k, int e0,
+                      int E_local, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                      float scale, void* y, int y_type, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return layer_impl(x, w_router, bias, choice_bias, w_gate_up, w_down, w_shared_gate_up, w_shared_down, T, H, I,
+                    I_shared, E, k, e0, E_local, score, n_group, topk_group, group_rule, renormalize, scale, y, y_type,
+                    workspace, workspace_bytes, stream);
+}
+
+// moe_layer_forward with another number of workgroups and of polls in the kernel of a few
+// tokens, as moe_internal_forward_few. Not part of moe.h.
+int moe_internal_layer_forward(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+                               const moe_bf16* w_gate_up, const moe_bf16* w_down, const moe_bf16* w_shared_gate_up,
+                               const moe_bf16* w_shared_down, int T, int H, int I, int I_shared, int E, int k, int e0,
+                               int E_local, int score, int n_group, int topk_group, int group_rule, int renormalize,
+                               float scale, void* y, int y_type, void* workspace, size_t workspace_bytes,
+                               int workgroups, int polls, hipStream_t stream) {
+  return layer_impl(x, w_router, bias, choice_bias, w_gate_up, w_down, w_shared_gate_up, w_shared_down, T, H, I,
+                    I_shared, E, k, e0, E_local, score, n_group, topk_group, group_rule, renormalize, scale, y, y_type,
+                    workspace, workspace_bytes, stream, workgroups, polls);
 }
 
 }  // extern "C"
