@@ -64,6 +64,7 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxSel = 1024;  // T k
+constexpr int kMaxPicks = 64;  // k (32, and parts of a shared expert)
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kSub = 512;       // k of a unit: 4 steps of 32 for each of the 4 waves
 constexpr int kCols = 128;      // weight columns of an item
@@ -86,12 +87,13 @@ struct Args {
   int polls;  // before a waiting workgroup looks for items
   void* y;
   // GIVEN: the selection [T, k - shared], and the expert that every token shares, as
-  // `shared` more experts of I beside the E_local (k counts them)
+  // `shared` more experts of I_part (I in whole blocks of 128) beside the E_local (k counts
+  // them), the last of what is left of I_shared
   const int32_t* topk_idx;
   const float* topk_w;
-  int shared;
-  const uint16_t* s_gate_up;  // [H, 2 shared I]
-  const uint16_t* s_down;     // [shared I, H]
+  int shared, I_shared, I_part;
+  const uint16_t* s_gate_up;  // [H, 2 I_shared]
+  const uint16_t* s_down;     // [I_shared, H]
   // counters, kPitch apart
   int* queue;     // [kind][queue]: items handed out
   int* cnt_a;     // [expert][128 of I]: gate and up items done
@@ -99,7 +101,7 @@ struct Args {
   int* cnt_b;     // [down panel]: items done
   float* part_a;  // [row][k range][gate panels, up panels][128]
   float* part_b;  // [row][k range][H]
-  float* h;       // [row][I]
+  float* h;       // [row][I], with a shared expert [row][I_part]
 };
 
 // k ranges of an item: units of 512 per range, ranges. More experts, fewer
@@ -287,8 +289,8 @@ __device__ __forceinline__ void pick(const Args& a, Tables& s, int t) {
 // The local slots of a return item's tokens.
 struct Returns {
   int n[kTokens];
-  int16_t row[kTokens][32];
-  float wt[kTokens][32];
+  int16_t row[kTokens][kMaxPicks];
+  float wt[kTokens][kMaxPicks];
 };
 
 // ---------------------------------------------------------------------------
@@ -308,6 +310,14 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
+// Columns of an expert's gate.
+template <bool GIVEN>
+__device__ __forceinline__ int width_of(const Args& a, int e) {
+  return GIVEN && e >= a.E_local ? min(a.I_part, a.I_shared - (e - a.E_local) * a.I_part) : a.I;
+}
+template <bool GIVEN>
+__device__ __forceinline__ int h_pitch(const Args& a) { return GIVEN ? a.I_part : a.I; }
+
 // Sums over k range [unit0, unit0 + units) x 512 of the `cols` (at most 128)
 // columns from col0 for `rows` rows: acc[gi][c][v] of lane 16 g + m is column 8 (4 g + v) + c of row
 // 16 gi + m (this wave's share of k). ready(): called once, after the first
@@ -318,17 +328,18 @@ __device__ __forceinline__ bool stream(const Args& a, const Tables& s, int e, in
                                        int units, int row0, int rows, f32x4v (&acc)[G][8], Ready ready) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id(), g = lane >> 4, m = lane & 15;
-  const int K = DOWN ? a.I : a.H;
-  int ldw = DOWN ? a.H : 2 * a.I;
+  const int pitch = DOWN ? h_pitch<GIVEN>(a) : a.H;  // of the activations' rows
+  int K = DOWN ? a.I : a.H, ldw = DOWN ? a.H : 2 * a.I;
   const uint16_t* base = (DOWN ? a.w_down : a.w_gate_up) + int64_t(e) * K * ldw;
   int64_t skip = 0;  // columns before the expert's
   if (GIVEN && e >= a.E_local) {
-    const int j = e - a.E_local;
+    const int64_t first = int64_t(e - a.E_local) * a.I_part;
     if constexpr (DOWN) {
-      base = a.s_down + int64_t(j) * K * ldw;
+      base = a.s_down + first * ldw;
+      K = width_of<GIVEN>(a, e);
     } else {
-      ldw *= a.shared;
-      skip = int64_t(j) * a.I;
+      ldw = 2 * a.I_shared;
+      skip = first;
       base = a.s_gate_up + skip;
     }
   }
@@ -336,14 +347,14 @@ __device__ __forceinline__ bool stream(const Args& a, const Tables& s, int e, in
   const uint32_t wvo = col < cols ? uint32_t(8 * g * ldw + col0 + col) * 2u : kOutside;
   const rsrc_t wr = make_rsrc(base, (int64_t(K) * ldw - skip) * 2);
   // activations: x as it is (bf16), h as float32
-  const rsrc_t xr = DOWN ? make_rsrc(a.h + int64_t(row0) * a.I, int64_t(rows) * a.I * 4)
+  const rsrc_t xr = DOWN ? make_rsrc(a.h + int64_t(row0) * pitch, int64_t(rows) * pitch * 4)
                          : make_rsrc(a.x, int64_t(a.T) * a.H * 2);
   uint32_t xvo[G];
 #pragma unroll
   for (int gi = 0; gi < G; ++gi) {
     const int r = 16 * gi + m;
     const uint32_t src = DOWN ? uint32_t(r) : uint32_t(s.tok[row0 + min(r, rows - 1)]);
-    xvo[gi] = r < rows ? src * uint32_t(K) * (DOWN ? 4u : 2u) + uint32_t(g) * (DOWN ? 32u : 16u) : kOutside;
+    xvo[gi] = r < rows ? src * uint32_t(pitch) * (DOWN ? 4u : 2u) + uint32_t(g) * (DOWN ? 32u : 16u) : kOutside;
   }
   const int nsteps = 4 * units;
   const int kb = unit0 * kSub + 32 * w;  // step st covers k kb + 128 st .. + 31
@@ -554,6 +565,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   const int blocks = (a.I + kCols - 1) / kCols;  // of 128 outputs of h; a gate and an up panel each
   const int panels_a = 2 * blocks, panels_b = (a.H + kCols - 1) / kCols;
   const int units_a = (a.H + kSub - 1) / kSub, units_b = (a.I + kSub - 1) / kSub;
+  // (I and I_part are as many blocks and units)
   const Split sa = split(a.H, max(1, n_act) * panels_a), sb = split(a.I, max(1, n_act) * panels_b);
   const int items_a = n_act * sa.ranges * panels_a, items_b = n_act * sb.ranges * panels_b;
   const int items_c = (a.T + kTokens - 1) / kTokens * panels_b;
@@ -738,8 +750,9 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     const int units = min(down ? sb.units : sa.units, (down ? units_b : units_a) - unit0);
     if (!down) {
       const int block = panel < blocks ? panel : panel - blocks;
-      const int up = GIVEN && e >= a.E_local ? a.shared * a.I : a.I;  // columns from gate to up
-      const int col0 = kCols * block + (panel < blocks ? 0 : up), cols = min(kCols, a.I - kCols * block);
+      const int up = GIVEN && e >= a.E_local ? a.I_shared : a.I;  // columns from gate to up
+      // (a block past a narrower expert's columns has none, its sums and its h are zeros)
+      const int col0 = kCols * block + (panel < blocks ? 0 : up), cols = min(kCols, width_of<GIVEN>(a, e) - kCols * block);
       auto ready = [] { return true; };
       ask_next();
       auto put = [&](int gi) {
@@ -778,7 +791,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         for (int r0 = 0; r0 < rows; r0 += rp) {
           const int r = r0 + slot % rp;
           float gu[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (r < rows && oc < a.I) {
+          if (r < rows && oc < h_pitch<GIVEN>(a)) {
             const float* p = a.part_a + (int64_t(row0 + r) * sa.ranges * panels_a + block) * kCols + o;
             constexpr int B = kBatch / 2;  // of four loads each
             for (int q0 = grp; q0 < sa.ranges; q0 += B * ng) {
@@ -811,8 +824,8 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
 #pragma unroll
                 for (int c = 0; c < 8; ++c) gu[c] += s_sum[((slot + i * rp) * 8 + c) * 32 + (tid & 31)];
           }
-          if (grp == 0 && r < rows && oc < a.I) {
-            float* hp = a.h + int64_t(row0 + r) * a.I + oc;
+          if (grp == 0 && r < rows && oc < h_pitch<GIVEN>(a)) {
+            float* hp = a.h + int64_t(row0 + r) * h_pitch<GIVEN>(a) + oc;
             put2(hp, silu_mul(gu[0], gu[4]), silu_mul(gu[1], gu[5]));
             put2(hp + 2, silu_mul(gu[2], gu[6]), silu_mul(gu[3], gu[7]));
           }
@@ -918,16 +931,25 @@ bool few_supported(int T, int H, int I, int k, int E_local) {
          int64_t(T) * I < (int64_t(1) << 29) && int64_t(T) * H < (int64_t(1) << 30);
 }
 
-// The shared expert's k: it goes with the others where it is a whole number of their
-// size and the tables hold it.
+// The shared expert's k: it goes with the others where the tables hold it. Its parts have
+// as many columns as I has in whole blocks, which the items go by (1 and 16 tokens,
+// I 32, I_shared 1600, H 4096: parts of I 67 and 90 us, these 37 and 60; two products of
+// moe_gemm, which round h to bf16, 49 and 63).
+namespace few {
+int part_width(int I) { return int(ceil_div(I, kCols)) * kCols; }
+}  // namespace few
 int few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
-  if (I_shared <= 0 || I_shared % I != 0) return 0;
-  const int64_t n = I_shared / I;
-  return k + n <= 32 && E_local + n <= few::kMaxE && few_supported(T, H, I, int(k + n), int(E_local + n)) ? int(n) : 0;
+  if (I_shared <= 0) return 0;
+  I = few::part_width(I);
+  const int64_t n = ceil_div(I_shared, I);
+  return k + n <= few::kMaxPicks && T * (k + n) <= few::kMaxSel && E_local + n <= few::kMaxE &&
+                 few_supported(T, H, I, int(k + n), int(E_local + n))
+             ? int(n)
+             : 0;
 }
 
 size_t few_workspace_bytes(int T, int H, int I, int E, int k, int E_local, int shared) {
-  return few::layout(T, H, I, E, k, E_local, shared).total;
+  return few::layout(T, H, shared > 0 ? few::part_width(I) : I, E, k, E_local, shared).total;
 }
 
 namespace few {
@@ -952,7 +974,8 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
   using namespace few;
   if (sc && T > 16) return hipErrorInvalidValue;
   const int shared = sc ? sc->shared : 0;
-  const Layout L = layout(T, H, I, E, k, E_local, shared);
+  const int I_part = shared > 0 ? part_width(I) : I;
+  const Layout L = layout(T, H, I_part, E, k, E_local, shared);
   float* logits = reinterpret_cast<float*>(ws + L.logits);
   int* ctr = reinterpret_cast<int*>(ws + L.counters);
   hipError_t err = score(x, w_router, bias, T, H, E, L, ws, stream);
@@ -960,8 +983,8 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
     err = launch_select(logits, nullptr, 0, nullptr, sc->choice_bias, T, E, k, sc->choice, sc->topk_idx, sc->topk_w, stream);
   if (err != hipSuccess) return err;
   const Args a{x, logits, w_gate_up, w_down, T, H, I, E, k + shared, e0, E_local, renormalize, int(y_f32), polls, y,
-               sc ? sc->topk_idx : nullptr, sc ? sc->topk_w : nullptr, shared, sc ? sc->s_gate_up : nullptr,
-               sc ? sc->s_down : nullptr, ctr, ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b,
+               sc ? sc->topk_idx : nullptr, sc ? sc->topk_w : nullptr, shared, sc ? sc->I_shared : 0, I_part,
+               sc ? sc->s_gate_up : nullptr, sc ? sc->s_down : nullptr, ctr, ctr + L.cnt_a, ctr + L.cnt_h, ctr + L.cnt_b,
                reinterpret_cast<float*>(ws + L.part_a), reinterpret_cast<float*>(ws + L.part_b),
                reinterpret_cast<float*>(ws + L.h)};
   // (at least one workgroup per queue: return items are not taken from another's)

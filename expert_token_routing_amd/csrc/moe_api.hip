@@ -759,8 +759,9 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
 // The layer's own buffers (selection; where the shared expert is a product of its own,
 // the float32 share, h and the products' sums) and behind them the share's, in the form
 // that the sizes take. Up to 16 tokens that is the share for a few tokens, with the
-// shared expert among the local ones where it is a whole number of their size (DeepSeek-R1
-// TP=8 share, one token: 58 us with separate products, 43 without).
+// shared expert among the local ones, where its hidden values stay float32 (DeepSeek-R1
+// TP=8 share, one token: 58 us with separate products, 43 without; 11 tokens, I 736,
+// I_shared 1128, H 2680: 98 and 82).
 static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
 static int layer_few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
   return layer_is_few(T, H, I, k, E_local) ? few_shared(T, H, I, k, E_local, I_shared) : 0;
@@ -924,7 +925,7 @@ static int layer_impl(const moe_bf16* x, const float* w_router, const float* bia
   const bool share_f32 = shared || y_f32;
   hipError_t err;
   if (layer_is_few(T, H, I, k, E_local)) {
-    const FewScored scored{c, choice_bias, topk_idx, topk_w, inside, w_shared_gate_up, w_shared_down};
+    const FewScored scored{c, choice_bias, topk_idx, topk_w, inside, I_shared, w_shared_gate_up, w_shared_down};
     err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32,
                      workgroups, polls, ws + L.rest, stream, &scored);
   } else {

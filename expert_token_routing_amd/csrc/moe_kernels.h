@@ -132,13 +132,13 @@ constexpr int kFewPolls = 4096;
 bool few_supported(int T, int H, int I, int k, int E_local);
 // With `scored` (T <= 16), a kernel between the two chooses by it into topk_idx and topk_w [T, k]
 // (the choice's renormalize counts), and the expert that every token shares goes with
-// the local ones, as few_shared(..) > 0 experts of I (0: none).
+// the local ones, as few_shared(..) > 0 more of them (0: none).
 struct FewScored {
   Choice choice;
   const float* choice_bias;
   int32_t* topk_idx;
   float* topk_w;
-  int shared;
+  int shared, I_shared;
   const uint16_t* s_gate_up;
   const uint16_t* s_down;
 };

@@ -67,3 +67,67 @@ def test_items_put_aside(T, H, I, Is, E, El, e0, k, workgroups, polls):
         torch.cuda.synchronize()
         for y in ys:
             assert torch.equal(y.view(torch.int32), ref.view(torch.int32))
+
+
+def shared_alone(x, gate_up, down):
+    """swiglu(x G) D in float64, and tests/test_few.py's bound of its error in float32 sums: the
+    worst of it, and its root mean square."""
+    F64, u = torch.float64, 2.0 ** -24
+    I, H = down.shape
+    nA, nB = H / 4 + 64, I / 4 + 64
+    xe, we, d = x.to(F64), gate_up.to(F64), down.to(F64)
+    p, q = xe @ we, xe.abs() @ we.abs()
+    g, up, G, U = p[:, :I], p[:, I:], q[:, :I], q[:, I:]
+    h = g * torch.sigmoid(g) * up
+    spread, direct = (1.1 * G * up.abs() + g.abs() * U) @ d.abs(), h.abs() @ d.abs()
+    return (h @ d, u * (nA * spread + (nB + 16) * direct),
+            u * (nA ** 0.5 * spread + (nB ** 0.5 + 16) * direct))
+
+
+WIDTHS = [(1, 3176, 136, 96), (2, 328, 2760, 264), (11, 2680, 736, 1128), (16, 1024, 256, 264), (3, 200, 32, 1624),
+          (16, 264, 40, 8), (7, 520, 128, 129 * 8), (5, 136, 520, 1000), (4, 72, 8, 64), (13, 1032, 1024, 1016),
+          (16, 136, 32, 60 * 128), (1, 264, 136, 60 * 256 - 8)]
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,Is", WIDTHS)
+def test_a_shared_expert_of_any_width_keeps_float32(T, H, I, Is):
+    """With a scale of 0 only the shared expert is left: its hidden values are not rounded to bf16
+    (whose 2^-8 would be far outside), whatever its width beside the local ones'."""
+    d = weights(T, H, I, Is, 16, 8, T + Is)
+    print(f"[gpu] shared alone T={T} H={H} I={I} Is={Is}", flush=True)
+    a = (d["x"], d["w_router"], d["bias"], d["choice_bias"], d["w_gate_up"], d["w_down"], 4, 4)
+    kw = dict(KW, out_dtype=F32)
+    y = M.moe_layer_forward(*a, d["shared_gate_up"], d["shared_down"], **dict(kw, scale=0.0))[0].double()
+    ref, worst, rms = shared_alone(d["x"], d["shared_gate_up"], d["shared_down"])
+    err = (y - ref).abs()
+    assert bool((err <= 2.0 ** -24 * ref.abs() + worst).all())
+    assert float(err.norm()) <= float((2.0 ** -24 * ref).norm() + rms.norm())
+    # beside the local ones: sums of k + n products, in order, each rounded
+    whole = M.moe_layer_forward(*a, d["shared_gate_up"], d["shared_down"], **kw)[0].double()
+    local = M.moe_layer_forward(*a, None, None, **kw)[0].double()
+    terms = 4 - (-Is // I)
+    size = torch.maximum(local.abs(), y.abs()).max() * terms
+    assert float((whole - local - y).abs().max()) <= 2 * terms * 2.0 ** -24 * float(size)
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,Is", [(16, 520, 264, 712), (3, 136, 40, 8), (1, 2048, 256, 520)])
+def test_a_shared_expert_of_any_width_by_few_workgroups(T, H, I, Is):
+    """Its empty blocks and k ranges are items as the others are; nothing of it is read past its
+    matrices' ends (NaN behind them)."""
+    d = weights(T, H, I, Is, 16, 8, T + Is)
+    for name, n in (("shared_gate_up", H * 2 * Is), ("shared_down", Is * H)):
+        flat = torch.full((n + 4096,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        flat[:n] = d[name].flatten()
+        d[name] = flat[:n].view(d[name].shape)
+    ref, ws = M.moe_layer_forward(d["x"], d["w_router"], d["bias"], d["choice_bias"], d["w_gate_up"], d["w_down"], 4, 4,
+                                  d["shared_gate_up"], d["shared_down"], out_dtype=F32, **KW)
+    assert bool(torch.isfinite(ref).all())
+    y = torch.empty_like(ref)
+    for i, (workgroups, polls) in enumerate(((8, 1), (11, 2), (40, 1))):
+        print(f"[gpu] shared of any width, workgroups={workgroups} T={T} H={H} I={I} Is={Is}", flush=True)
+        ws.fill_(85 * i)
+        layer_with(workgroups, polls, d, 4, 4, y, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int32), ref.view(torch.int32))
