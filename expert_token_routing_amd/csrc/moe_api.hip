@@ -230,27 +230,29 @@ int moe_forward_workspace_layout(int T, int H, int I, int E, int k, int E_local,
   return MOE_OK;
 }
 
-static int forward_impl(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
-                        const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
-                        int renormalize, void* y, bool y_f32, void* workspace, size_t workspace_bytes,
-                        hipEvent_t* events, hipStream_t stream, bool fuse_combine = false) {
-  int st = check_route_dims(T, H, E, k);
-  if (st != MOE_OK) return st;
-  if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
-  if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
-  if (!expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
-  if (!rows_fit(min_capacity(T, k, E_local))) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
-  if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y))
-    return MOE_ERR_INVALID_ARG;
+// The router's logits, and the choice by their scores.
+static hipError_t route_scored(const moe_bf16* x, const float* w_router, const float* bias, const float* choice_bias,
+                               int T, int H, int E, int k, const Choice& choice, float* logits, int32_t* topk_idx,
+                               float* topk_w, uint16_t* planes, float* part, hipStream_t stream) {
+  bool split;
+  const hipError_t err = launch_route_logits(x, w_router, bias, T, H, E, logits, planes, part, &split, stream);
+  if (err != hipSuccess) return err;
+  return launch_select(logits, split ? part : nullptr, route_k_parts(T, H, E) - 1, bias, choice_bias, T, E, k, choice,
+                       topk_idx, topk_w, stream);
+}
+
+// The launches of a share: selection (by router logits, or with `choice` by scores), dispatch,
+// expert MLPs, combine. ws: forward_layout's.
+static hipError_t share_steps(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                              const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
+                              int renormalize, const Choice* choice, const float* choice_bias, void* y, bool y_f32,
+                              char* ws, hipEvent_t* events, hipStream_t stream, bool fuse_combine = false) {
   const ForwardLayout L = forward_layout(T, H, I, E, k, E_local);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 || workspace_bytes < L.total)
-    return MOE_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
   auto at = [&](size_t off) { return static_cast<void*>(ws + off); };
   const int64_t cap = min_capacity(T, k, E_local);
   float* logits = static_cast<float*>(at(L.logits));
+  float* part = static_cast<float*>(at(L.part));
+  uint16_t* planes = static_cast<uint16_t*>(at(L.planes));
   int32_t* topk_idx = static_cast<int32_t*>(at(L.topk_idx));
   float* topk_w = static_cast<float*>(at(L.topk_w));
   int32_t* counts = static_cast<int32_t*>(at(L.counts));
@@ -267,9 +269,10 @@ static int forward_impl(const moe_bf16* x, const float* w_router, const float* b
   auto mark = [&](int i) { return events ? hipEventRecord(events[i], stream) : hipSuccess; };
 
   hipError_t err = mark(0);
-  if (err == hipSuccess)
-    err = launch_route(x, w_router, bias, T, H, E, k, renormalize, logits, topk_idx, topk_w,
-                       static_cast<uint16_t*>(at(L.planes)), static_cast<float*>(at(L.part)), stream);
+  if (err == hipSuccess && choice)
+    err = route_scored(x, w_router, bias, choice_bias, T, H, E, k, *choice, logits, topk_idx, topk_w, planes, part, stream);
+  else if (err == hipSuccess)
+    err = launch_route(x, w_router, bias, T, H, E, k, renormalize, logits, topk_idx, topk_w, planes, part, stream);
   if (err == hipSuccess) err = mark(1);
   // GEMM1 reads the token vectors in place when it can, so dispatch only
   // builds the tables; otherwise the rows are copied out first.
@@ -295,7 +298,28 @@ static int forward_impl(const moe_bf16* x, const float* w_router, const float* b
   if (err == hipSuccess) err = mark(4);
   if (err == hipSuccess) err = launch_combine(out, inv, topk_w, T, H, k, y, y_f32, stream, fuse);
   if (err == hipSuccess) err = mark(5);
-  return hip_status(err);
+  return err;
+}
+
+static int forward_impl(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
+                        const moe_bf16* w_down, int T, int H, int I, int E, int k, int e0, int E_local,
+                        int renormalize, void* y, bool y_f32, void* workspace, size_t workspace_bytes,
+                        hipEvent_t* events, hipStream_t stream, bool fuse_combine = false) {
+  int st = check_route_dims(T, H, E, k);
+  if (st != MOE_OK) return st;
+  if ((st = check_local(E, e0, E_local)) != MOE_OK) return st;
+  if (I <= 0 || (I % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (!expert_weights_fit(H, I)) return MOE_ERR_UNSUPPORTED;
+  if (!rows_fit(min_capacity(T, k, E_local))) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router || !w_gate_up || !w_down || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+      workspace_bytes < forward_layout(T, H, I, E, k, E_local).total)
+    return MOE_ERR_WORKSPACE;
+  return hip_status(share_steps(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, nullptr,
+                                nullptr, y, y_f32, static_cast<char*>(workspace), events, stream, fuse_combine));
 }
 
 int moe_forward(const moe_bf16* x, const float* w_router, const float* bias, const moe_bf16* w_gate_up,
@@ -756,7 +780,7 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
   return MOE_OK;
 }
 
-// The layer's own buffers (selection; where the shared expert is a product of its own,
+// The layer's own buffers (up to 16 tokens the selection; where the shared expert is a product of its own,
 // the float32 share, h and the products' sums) and behind them the share's, in the form
 // that the sizes take. Up to 16 tokens that is the share for a few tokens, with the
 // shared expert among the local ones, where its hidden values stay float32 (DeepSeek-R1
@@ -778,9 +802,9 @@ static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k,
     return at;
   };
   const int inside = layer_few_shared(T, H, I, k, E_local, I_shared);
-  const bool apart = I_shared > 0 && inside == 0 && T > 0;
-  L.topk_idx = take(size_t(T) * k * sizeof(int32_t));
-  L.topk_w = take(size_t(T) * k * sizeof(float));
+  const bool few = layer_is_few(T, H, I, k, E_local), apart = I_shared > 0 && inside == 0 && T > 0;
+  L.topk_idx = take(few ? size_t(T) * k * sizeof(int32_t) : 0);
+  L.topk_w = take(few ? size_t(T) * k * sizeof(float) : 0);
   L.share = take(apart ? size_t(T) * H * sizeof(float) : 0);
   L.h = take(apart ? size_t(T) * I_shared * sizeof(uint16_t) : 0);
   if (apart)
@@ -788,8 +812,7 @@ static LayerLayout layer_layout(int T, int H, int I, int I_shared, int E, int k,
                             moe_gemm_workspace_size(T, H, I_shared, 1, MOE_ACT_NONE));
   L.part = take(L.part_bytes);
   L.rest = o;
-  L.total = o + (layer_is_few(T, H, I, k, E_local) ? few_workspace_bytes(T, H, I, E, k, E_local, inside)
-                                                   : forward_layout(T, H, I, E, k, E_local).total);
+  L.total = o + (few ? few_workspace_bytes(T, H, I, E, k, E_local, inside) : forward_layout(T, H, I, E, k, E_local).total);
   return L;
 }
 }  // namespace moe
@@ -821,13 +844,8 @@ int moe_route_scored(const moe_bf16* x, const float* w_router, const float* bias
     return MOE_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   float* part = reinterpret_cast<float*>(ws + align_up(size_t(3) * E * H * sizeof(uint16_t)));
-  bool split;
-  hipError_t err = launch_route_logits(x, w_router, bias, T, H, E, logits, reinterpret_cast<uint16_t*>(ws), part,
-                                       &split, stream);
-  if (err == hipSuccess)
-    err = launch_select(logits, split ? part : nullptr, route_k_parts(T, H, E) - 1, bias, choice_bias, T, E, k, c,
-                        topk_idx, topk_w, stream);
-  return hip_status(err);
+  return hip_status(route_scored(x, w_router, bias, choice_bias, T, H, E, k, c, logits, topk_idx, topk_w,
+                                 reinterpret_cast<uint16_t*>(ws), part, stream));
 }
 
 static int gemm_impl(const moe_bf16* a, const moe_bf16* w, const float* bias, const void* residual, int res_type,
@@ -916,8 +934,6 @@ static int layer_impl(const moe_bf16* x, const float* w_router, const float* bia
   const LayerLayout L = layer_layout(T, H, I, I_shared, E, k, E_local);
   if (!workspace || !aligned256(workspace) || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  int32_t* topk_idx = reinterpret_cast<int32_t*>(ws + L.topk_idx);
-  float* topk_w = reinterpret_cast<float*>(ws + L.topk_w);
   const int inside = layer_few_shared(T, H, I, k, E_local, I_shared);
   const bool y_f32 = y_type == MOE_TYPE_F32, shared = I_shared > 0 && inside == 0;
   // the share, float32 where the shared expert is added to it
@@ -925,42 +941,13 @@ static int layer_impl(const moe_bf16* x, const float* w_router, const float* bia
   const bool share_f32 = shared || y_f32;
   hipError_t err;
   if (layer_is_few(T, H, I, k, E_local)) {
-    const FewScored scored{c, choice_bias, topk_idx, topk_w, inside, I_shared, w_shared_gate_up, w_shared_down};
+    const FewScored scored{c, choice_bias, reinterpret_cast<int32_t*>(ws + L.topk_idx),
+                           reinterpret_cast<float*>(ws + L.topk_w), inside, I_shared, w_shared_gate_up, w_shared_down};
     err = launch_few(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, share, share_f32,
                      workgroups, polls, ws + L.rest, stream, &scored);
   } else {
-    const ForwardLayout F = forward_layout(T, H, I, E, k, E_local);
-    auto at = [&](size_t off) { return static_cast<void*>(ws + L.rest + off); };
-    const int64_t cap = min_capacity(T, k, E_local);
-    float* logits = static_cast<float*>(at(F.logits));
-    float* part = static_cast<float*>(at(F.part));
-    int32_t* offsets = static_cast<int32_t*>(at(F.offsets));
-    int32_t* perm_src = static_cast<int32_t*>(at(F.perm_src));
-    int32_t* inv = static_cast<int32_t*>(at(F.inv));
-    int32_t* counts = static_cast<int32_t*>(at(F.counts));
-    int32_t* chunks = static_cast<int32_t*>(at(F.chunks));
-    uint16_t* x_perm = static_cast<uint16_t*>(at(F.x_perm));
-    uint16_t* h = static_cast<uint16_t*>(at(F.h));
-    uint16_t* out = static_cast<uint16_t*>(at(F.out));
-    const bool gather = expert_gemm1_can_gather(T, H);
-    const int64_t rows_hint = ceil_div(int64_t(T) * k, E);
-    bool split;
-    err = launch_route_logits(x, w_router, bias, T, H, E, logits, static_cast<uint16_t*>(at(F.planes)), part, &split,
-                              stream);
-    if (err == hipSuccess)
-      err = launch_select(logits, split ? part : nullptr, route_k_parts(T, H, E) - 1, bias, choice_bias, T, E, k, c,
-                          topk_idx, topk_w, stream);
-    if (err == hipSuccess)
-      err = gather ? launch_dispatch_index(topk_idx, T, E, k, e0, E_local, counts, offsets, perm_src, inv, chunks, stream)
-                   : launch_dispatch(x, topk_idx, T, H, E, k, e0, E_local, counts, offsets, perm_src, inv, x_perm,
-                                     chunks, stream);
-    if (err == hipSuccess)
-      err = gather ? launch_expert_gemm1_gather(x, perm_src, T, k, offsets, w_gate_up, H, I, E_local, cap, h, stream,
-                                                rows_hint)
-                   : launch_expert_gemm1(x_perm, offsets, w_gate_up, H, I, E_local, cap, h, stream, rows_hint);
-    if (err == hipSuccess)
-      err = launch_expert_gemm2(h, offsets, w_down, H, I, E_local, cap, out, stream, rows_hint);
-    if (err == hipSuccess) err = launch_combine(out, inv, topk_w, T, H, k, share, share_f32, stream);
+    err = share_steps(x, w_router, bias, w_gate_up, w_down, T, H, I, E, k, e0, E_local, renormalize, &c, choice_bias,
+                      share, share_f32, ws + L.rest, nullptr, stream);
   }
   if (err == hipSuccess && shared) {
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
