@@ -479,7 +479,7 @@ __device__ __forceinline__ void gather_sums(float* s_sum, const f32x4v (&acc)[8]
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
 // TWO: an expert may have more than 16 rows (T > 16), which need two groups of
-// accumulators. GIVEN: the experts were chosen before (T <= 16).
+// accumulators. GIVEN: the experts were chosen before.
 template <bool TWO, bool GIVEN>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) few_experts_kernel(Args a) {
   __shared__ Tables s;
@@ -972,7 +972,6 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
                       const uint16_t* w_down, int T, int H, int I, int E, int k, int e0, int E_local, int renormalize,
                       void* y, bool y_f32, int workgroups, int polls, char* ws, hipStream_t stream, const FewScored* sc) {
   using namespace few;
-  if (sc && T > 16) return hipErrorInvalidValue;
   const int shared = sc ? sc->shared : 0;
   const int I_part = shared > 0 ? part_width(I) : I;
   const Layout L = layout(T, H, I_part, E, k, E_local, shared);
@@ -989,8 +988,8 @@ hipError_t launch_few(const uint16_t* x, const float* w_router, const float* bia
                reinterpret_cast<float*>(ws + L.h)};
   // (at least one workgroup per queue: return items are not taken from another's)
   const int grid = std::max(kQueues, workgroups > 0 ? workgroups : 2 * device_cu_count());
-  auto* kern = sc ? few_experts_kernel<false, true>
-                  : T > 16 ? few_experts_kernel<true, false> : few_experts_kernel<false, false>;
+  auto* kern = sc ? (T > 16 ? few_experts_kernel<true, true> : few_experts_kernel<false, true>)
+                  : (T > 16 ? few_experts_kernel<true, false> : few_experts_kernel<false, false>);
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(few::kThreads), 0, stream, a);
   return hipGetLastError();
 }

@@ -780,13 +780,17 @@ static int check_gemm(int64_t capacity, int N, int K, int E_local, int activatio
   return MOE_OK;
 }
 
-// The layer's own buffers (up to 16 tokens the selection; where the shared expert is a product of its own,
-// the float32 share, h and the products' sums) and behind them the share's, in the form
-// that the sizes take. Up to 16 tokens that is the share for a few tokens, with the
-// shared expert among the local ones, where its hidden values stay float32 (DeepSeek-R1
-// TP=8 share, one token: 58 us with separate products, 43 without; 11 tokens, I 736,
-// I_shared 1128, H 2680: 98 and 82).
-static bool layer_is_few(int T, int H, int I, int k, int E_local) { return T <= 16 && few_supported(T, H, I, k, E_local); }
+// The layer's own buffers (for a few tokens the selection; where the shared expert is a
+// product of its own, the float32 share, h and the products' sums) and behind them the
+// share's, in the form that the sizes take. Up to 32 tokens that is the share for a few
+// tokens, with the shared expert among the local ones: all hidden values stay float32, and
+// it is the faster one (us, the other form first: DeepSeek-R1 TP=8 share, 1 token 58 and 43,
+// EP=8, 24 tokens 316 and 236, 32 tokens 332 and 270; 17 tokens, H 5336, I 208, I_shared
+// 1936: 384 and 97). Layers whose experts are next to nothing (17 tokens, H 136, I 40: 51
+// and 28) keep the bits of the separate calls from 17 tokens on.
+static bool layer_is_few(int T, int H, int I, int k, int E_local) {
+  return T <= (int64_t(H) * I < 8192 ? 16 : MOE_FEW_TOKENS) && few_supported(T, H, I, k, E_local);
+}
 static int layer_few_shared(int T, int H, int I, int k, int E_local, int I_shared) {
   return layer_is_few(T, H, I, k, E_local) ? few_shared(T, H, I, k, E_local, I_shared) : 0;
 }

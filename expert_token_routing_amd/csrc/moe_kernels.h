@@ -130,7 +130,7 @@ hipError_t launch_block_norm(const void* y, int y_type, const void* r, bool r_f3
 // turns to other work. The results depend on neither.
 constexpr int kFewPolls = 4096;
 bool few_supported(int T, int H, int I, int k, int E_local);
-// With `scored` (T <= 16), a kernel between the two chooses by it into topk_idx and topk_w [T, k]
+// With `scored`, a kernel between the two chooses by it into topk_idx and topk_w [T, k]
 // (the choice's renormalize counts), and the expert that every token shares goes with
 // the local ones, as few_shared(..) > 0 more of them (0: none).
 struct FewScored {

@@ -616,13 +616,15 @@ int moe_gemm(const moe_bf16* a, const moe_bf16* w, const float* bias, const void
  *   ranks that a token passes through.
  *   y        [T, H] of y_type (MOE_TYPE_*), rounded once where it is bf16 and
  *            there is a shared expert or T is small (as in moe_forward_few)
- * The share is that of moe_forward_few_f32 up to 16 tokens where its limits allow (all
- * hidden values float32), of moe_forward_f32 otherwise (hidden values and each selected
- * expert's output rounded to bf16). In the first case the shared expert goes with the
- * local ones as n = ceil(I_shared / J) more of them, J being I rounded up to a multiple of
- * 128, its hidden values in float32 too, where k + n <= 64 and E_local + n <= 1024; else it is two products of moe_gemm, its
- * hidden values rounded to bf16 as moe_expert_ffn's are. I_shared is a multiple of 8, H * I_shared < 2^29;
- * other arguments and their checks are moe_forward's and moe_select's.
+ * The share is that of moe_forward_few_f32 up to MOE_FEW_TOKENS tokens (16 where
+ * H * I < 8192) where its limits allow: all hidden values float32. Otherwise it is
+ * moe_forward_f32's: hidden values and each selected expert's output rounded to
+ * bf16. In the first case the shared expert goes with the local ones, as n =
+ * ceil(I_shared / J) more of them, J being I rounded up to a multiple of 128, its
+ * hidden values float32 too, where k + n <= 64, T * (k + n) <= 1024 and E_local + n
+ * <= 1024; else it is two products of moe_gemm, its hidden values rounded to bf16
+ * as moe_expert_ffn's are. I_shared is a multiple of 8, H * I_shared < 2^29; other
+ * arguments and their checks are moe_forward's and moe_select's.
  * workspace: moe_layer_workspace_size bytes, 256-byte aligned; no part of it
  * needs to start at zero, calls that overlap need their own.
  */

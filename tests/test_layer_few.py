@@ -1,4 +1,4 @@
-"""moe_layer_forward up to 16 tokens, where the share for a few tokens takes the
+"""moe_layer_forward for a few tokens, where the share for a few tokens takes the
 experts that were chosen before and the shared expert beside them."""
 import ctypes
 
@@ -42,7 +42,8 @@ def test_internal_rejects(workgroups, polls):
 @gpu
 @pytest.mark.parametrize("T,H,I,Is,E,El,e0,k", [(1, 7168, 256, 256, 256, 256, 0, 8), (16, 2048, 1024, 1024, 64, 32, 16, 8),
                                                 (5, 136, 40, 120, 32, 8, 8, 6), (13, 520, 264, 0, 16, 16, 0, 3),
-                                                (3, 264, 128, 256, 8, 1, 7, 2)])
+                                                (3, 264, 128, 256, 8, 1, 7, 2), (32, 1024, 264, 520, 8, 8, 0, 2),
+                                                (17, 136, 64, 72, 32, 12, 8, 6), (25, 2048, 512, 0, 16, 4, 4, 3)])
 @pytest.mark.parametrize("workgroups,polls", [(8, 1), (11, 2), (40, 1), (0, 1)])
 def test_items_put_aside(T, H, I, Is, E, El, e0, k, workgroups, polls):
     """Workgroups that put waiting items aside for others', as in moe_forward_few's test of it: the
@@ -86,7 +87,9 @@ def shared_alone(x, gate_up, down):
 
 WIDTHS = [(1, 3176, 136, 96), (2, 328, 2760, 264), (11, 2680, 736, 1128), (16, 1024, 256, 264), (3, 200, 32, 1624),
           (16, 264, 40, 8), (7, 520, 128, 129 * 8), (5, 136, 520, 1000), (4, 72, 8, 64), (13, 1032, 1024, 1016),
-          (16, 136, 32, 60 * 128), (1, 264, 136, 60 * 256 - 8)]
+          (16, 136, 32, 60 * 128), (1, 264, 136, 60 * 256 - 8),
+          (17, 1024, 256, 256), (24, 264, 40, 8), (27, 5336, 208, 1936), (32, 520, 128, 28 * 128), (19, 976, 448, 40),
+          (32, 64, 128, 72)]
 
 
 @gpu
@@ -112,7 +115,7 @@ def test_a_shared_expert_of_any_width_keeps_float32(T, H, I, Is):
 
 
 @gpu
-@pytest.mark.parametrize("T,H,I,Is", [(16, 520, 264, 712), (3, 136, 40, 8), (1, 2048, 256, 520)])
+@pytest.mark.parametrize("T,H,I,Is", [(16, 520, 264, 712), (3, 136, 40, 8), (1, 2048, 256, 520), (29, 520, 264, 712)])
 def test_a_shared_expert_of_any_width_by_few_workgroups(T, H, I, Is):
     """Its empty blocks and k ranges are items as the others are; nothing of it is read past its
     matrices' ends (NaN behind them)."""
@@ -131,3 +134,29 @@ def test_a_shared_expert_of_any_width_by_few_workgroups(T, H, I, Is):
         layer_with(workgroups, polls, d, 4, 4, y, ws)
         torch.cuda.synchronize()
         assert torch.equal(y.view(torch.int32), ref.view(torch.int32))
+
+
+@gpu
+@pytest.mark.parametrize("T", [17, 24, 32])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, F32])
+def test_up_to_32_tokens_every_expert_keeps_float32(T, out_dtype):
+    """Local experts and shared one against the layer in float64, chosen by the GPU's logits. What
+    is off beside the sums' roundings: the weights, by those of logits of up to 8 (2^-24 for
+    each of at most H / 4 + 64 additions, in root mean square), at most 1e-4 of y, where bf16 hidden
+    values are 1e-3 off."""
+    H, I, Is, E, El, e0, k = 1024, 256, 264, 16, 8, 4, 4
+    d = weights(T, H, I, Is, E, El, T)
+    print(f"[gpu] layer in float32 T={T} {out_dtype}", flush=True)
+    y = M.moe_layer_forward(d["x"], d["w_router"], d["bias"], d["choice_bias"], d["w_gate_up"], d["w_down"], k, e0,
+                            d["shared_gate_up"], d["shared_down"], out_dtype=out_dtype, **KW)[0].double()
+    logits, idx, _ = M.moe_route_scored(d["x"], d["w_router"], d["bias"], d["choice_bias"], k, **KW)
+    s = torch.sigmoid(d["x"].double() @ d["w_router"].double().T + d["bias"].double()).gather(1, idx.long())
+    w = 2.5 * s / s.sum(1, keepdim=True)
+    ref = shared_alone(d["x"], d["shared_gate_up"], d["shared_down"])[0]
+    for e in range(El):
+        t, j = (idx == e + e0).nonzero(as_tuple=True)
+        if len(t):
+            ref.index_add_(0, t, w[t, j][:, None] * shared_alone(d["x"][t], d["w_gate_up"][e], d["w_down"][e])[0])
+    half = 2.0 ** -8 * ref.abs() if out_dtype is torch.bfloat16 else torch.zeros_like(ref)
+    over = ((y - ref).abs() - half).clamp(min=0)  # beyond y's own rounding
+    assert float(over.norm()) <= 1e-4 * float(ref.norm())
