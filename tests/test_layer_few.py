@@ -160,3 +160,24 @@ def test_up_to_32_tokens_every_expert_keeps_float32(T, out_dtype):
     half = 2.0 ** -8 * ref.abs() if out_dtype is torch.bfloat16 else torch.zeros_like(ref)
     over = ((y - ref).abs() - half).clamp(min=0)  # beyond y's own rounding
     assert float(over.norm()) <= 1e-4 * float(ref.norm())
+
+
+@gpu
+@pytest.mark.parametrize("T,H,I,Is,k", [(32, 128, 128, 20 * 128, 16), (4, 136, 64, 63 * 128, 4), (32, 264, 40, 1024, 32)])
+def test_a_shared_expert_too_wide_for_the_tables(T, H, I, Is, k):
+    """More parts than the kernel of a few tokens holds: two products onto the float32 share, whose
+    hidden values are rounded to bf16 (2^-9 each, at most; the sums' terms are of either sign)."""
+    E = 32
+    d = weights(T, H, I, Is, E, E, Is)
+    print(f"[gpu] shared too wide T={T} H={H} I={I} Is={Is} k={k}", flush=True)
+    a = (d["x"], d["w_router"], d["bias"], d["choice_bias"], d["w_gate_up"], d["w_down"], k, 0)
+    kw = dict(score="sigmoid", out_dtype=F32)
+    y = M.moe_layer_forward(*a, d["shared_gate_up"], d["shared_down"], scale=0.0, **kw)[0].double()
+    ref = shared_alone(d["x"], d["shared_gate_up"], d["shared_down"])[0]
+    h = d["x"].double() @ d["shared_gate_up"].double()
+    h = torch.nn.functional.silu(h[:, :Is]) * h[:, Is:]
+    bound = 2.0 ** -8 * (h.abs() @ d["shared_down"].double().abs())
+    assert bool(((y - ref).abs() <= bound).all())
+    whole = M.moe_layer_forward(*a, d["shared_gate_up"], d["shared_down"], **kw)[0].double()
+    local = M.moe_layer_forward(*a, None, None, **kw)[0].double()
+    assert float((whole - local - y).abs().max()) <= 4 * 2.0 ** -24 * float(torch.maximum(local.abs(), y.abs()).max())
