@@ -552,8 +552,8 @@ int moe_select(const float* logits, const float* bias, int T, int E, int k, int 
 
 /*
  * moe_route with moe_select's choice: logits = x . w_router^T + bias as
- * moe_route computes them (bias [E] f32 or NULL belongs to the logits), then
- * moe_select of them with choice_bias ([E] f32 or NULL). logits [T, E] OUT
+ * moe_route computes them, in float32 (bias [E] f32 or NULL belongs to the logits),
+ * then moe_select of them with choice_bias ([E] f32 or NULL). logits [T, E] OUT
  * holds what the choice was made from. workspace: moe_route_workspace_size
  * bytes, 256-byte aligned. Other arguments and checks are the two calls'.
  */
