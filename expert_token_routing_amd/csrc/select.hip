@@ -61,7 +61,9 @@ __device__ __forceinline__ void logits_of(const Args& a, int64_t row, int first,
 
 // ---------------------------------------------------------------------------
 // Reductions without LDS: DPP steps inside rows of 16 lanes (swap neighbours, swap
-// pairs, mirror the halves of 8, mirror the 16), on every lane of the row.
+// pairs, mirror the halves of 8, mirror the 16), on every lane of the row. A lane that is
+// switched off hands out 0, so every lane of the wave takes them: never behind a && or a ?:
+// whose condition differs between lanes.
 // ---------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ uint32_t peer(uint32_t v) {
@@ -586,7 +588,8 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   // (infinite values, whose difference is no number, among those that are never sure)
   if (by_logit) unsure = unsure || ((__ballot(is && r > 0 && ahead != v && !(fabs(ahead - v) > kSame)) >> (16 * row4)) & 0xFFFFu) != 0;
   int rank = r;
-  if (__ballot(is && r > 0 && !(peer<0x121>(v) > v)) != 0) rank = before(v, e);
+  const bool in_order = peer<0x121>(v) > v;
+  if (__ballot(is && r > 0 && !in_order) != 0) rank = before(v, e);
   const bool chosen = is && rank < a.k;
   // No expert beside the candidates may come before the last chosen one: their values
   // lie at most the MASK steps that a key drops above the next key's.

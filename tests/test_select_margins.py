@@ -161,3 +161,26 @@ def test_a_bias_does_not_bring_a_nan_logit_back(E, G, top, score):
     for rule in ("max", "top2"):
         idx, _ = check(logits, bias, 4, score=score, n_group=G, topk_group=top, group_score=rule)
         assert bool((idx[:, 0] == 4).all()) and not bool(((idx == 3) | (idx == per // 2)).any())
+
+
+@gpu
+@pytest.mark.parametrize("E,k,G,top", [(64, 1, 1, 1), (64, 2, 8, 8), (256, 4, 1, 1), (69, 2, 3, 1), (160, 6, 8, 3), (32, 8, 8, 6),
+                                       (100, 1, 5, 2)])
+@pytest.mark.parametrize("score,level", [("softmax", -4.0), ("softmax", -52.0), ("softmax", 3.0), ("sigmoid", -4.0)])
+def test_negative_values_in_the_last_bits_of_a_key(E, k, G, top, score, level):
+    """The largest two values of a row next to each other in the bits that a key drops, the larger
+    one at the higher id, every other value far from the next: the first candidates come the wrong
+    way round, and values below 0 have to be put right as those above are."""
+    g = torch.Generator().manual_seed(E)
+    logits = level - 0.5 - 0.05 * torch.rand(200, E, generator=g).argsort(1).float()
+    step = abs(level) * 2.0 ** -22
+    ends = torch.rand(200, E, generator=g).argsort(1)[:, :2].sort(1).values
+    for t, (a, b) in enumerate(ends.tolist()):
+        logits[t, a], logits[t, b] = level, level + step * (1 + t % 8)
+    check(logits, None, k, score=score, n_group=G, topk_group=top)
+    # choice values below 0 beside a bias
+    check(logits, torch.full((E,), -2.0), k, score="sigmoid", n_group=G, topk_group=top)
+    bias = -2.0 - 0.01 * torch.rand(E, generator=g).argsort().float()
+    a, b = sorted(torch.rand(E, generator=g).argsort()[:2].tolist())
+    bias[a], bias[b] = -1.5, -1.5 + 2.0 ** -21
+    check(torch.zeros(8, E), bias, k, score=score, n_group=G, topk_group=top)
