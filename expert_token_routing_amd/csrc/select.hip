@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
     const bool real = g < a.n_group;
     float v = a.rule == 0 || map.per == 1 ? b1 : b1 + b2;
     v = real && v == v ? v : -INFINITY;
-    bool kept = real && above(v) < (a.topk_group << map.log_l);
+    const int higher = above(v);
+    bool kept = real && higher < (a.topk_group << map.log_l);
     const float lo = over<16>(kept ? v : INFINITY, Min()), hi = over<16>(real && !kept ? v : -INFINITY, Max());
     const int lanes = __popc(uint32_t(__ballot(kept) >> (16 * row4)) & 0xFFFFu);
     // Up to two scores on both sides, and on each side a rounding of 2^-24 of a value for

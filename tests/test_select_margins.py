@@ -184,3 +184,21 @@ def test_negative_values_in_the_last_bits_of_a_key(E, k, G, top, score, level):
     a, b = sorted(torch.rand(E, generator=g).argsort()[:2].tolist())
     bias[a], bias[b] = -1.5, -1.5 + 2.0 ** -21
     check(torch.zeros(8, E), bias, k, score=score, n_group=G, topk_group=top)
+
+
+@gpu
+@pytest.mark.parametrize("E,G,top", [(160, 10, 4), (100, 5, 2), (96, 3, 2), (140, 7, 5)])
+def test_negative_groups_beside_lanes_without_one(E, G, top):
+    """Groups of negative value where lanes hold none: the definition's, and as quick as positive
+    ones (those lanes do not count as groups above)."""
+    g = torch.Generator().manual_seed(E)
+    logits, bias = torch.randn(300, E, generator=g), -1.0 - torch.rand(E, generator=g)
+    for score in ("sigmoid", "softmax"):
+        check(logits - 5, None, 4, score=score, n_group=G, topk_group=top, group_score="max")
+        check(logits, bias, 4, score=score, n_group=G, topk_group=top, group_score="top2")
+    dev = device()
+    l, b = torch.randn(65536, E, device=dev), bias.to(dev)
+    kw = dict(score="sigmoid", n_group=G, topk_group=top, group_score="top2")
+    below, above = seconds(lambda: M.moe_select(l, 4, b, **kw)), seconds(lambda: M.moe_select(l, 4, -b, **kw))
+    print(f"{G} groups below 0 {1e3 * below:.1f} us, above {1e3 * above:.1f} us")
+    assert below <= 1.5 * above
