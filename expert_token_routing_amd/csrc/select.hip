@@ -226,9 +226,10 @@ __device__ __forceinline__ void choose_exact(const Args& a, Exact<EPL>& s, int t
   const bool mine = lane < a.k;
   float ml = mine ? s.l[my_e] : -INFINITY;
   ml = ml == ml ? ml : -INFINITY;
-  // (renormalised sigmoids far below 0 without their common factor: none underflows)
+  // (renormalised sigmoids far below 0 without their common factor: none underflows; all of
+  // them at -infinity have none)
   const float top = wave_max_dpp(ml);
-  const bool far = a.score != 0 && a.renormalize && top < -600.f;
+  const bool far = a.score != 0 && a.renormalize && top < -600.f && top > -INFINITY;
   const double v = mine ? score64(a.score == 0 || far, ml, far ? top : m) : 0.0;
   if (a.renormalize) den = wave64(v, Add());
   if (mine) {

@@ -540,8 +540,9 @@ int moe_block_forward(const void* residual, int r_type, const float* w_pre, cons
  * logit counts as -infinity in the scores, and its expert's choice value is
  * -infinity whatever its bias; a NaN choice value or group value counts as
  * -infinity too (the ids are distinct and in [0, E) whatever the inputs hold). A
- * token without a logit above -infinity gets NaN weights; a logit of +infinity
- * has the softmax score 1 / (how many there are).
+ * token without a logit above -infinity gets NaN weights, and with renormalize one
+ * whose selected scores are all 0; a logit of +infinity has the softmax score 1 /
+ * (how many there are).
  * 1 <= k <= topk_group * (E / n_group), E a multiple of n_group,
  * 1 <= topk_group <= n_group, scale finite; E <= 1024, k <= 32, n_group <=
  * MOE_MAX_GROUPS, T * k < 2^31 (else MOE_ERR_UNSUPPORTED). n_group = 1: no

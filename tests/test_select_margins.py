@@ -202,3 +202,21 @@ def test_negative_groups_beside_lanes_without_one(E, G, top):
     below, above = seconds(lambda: M.moe_select(l, 4, b, **kw)), seconds(lambda: M.moe_select(l, 4, -b, **kw))
     print(f"{G} groups below 0 {1e3 * below:.1f} us, above {1e3 * above:.1f} us")
     assert below <= 1.5 * above
+
+
+@gpu
+@pytest.mark.parametrize("E,k,G,top", [(64, 1, 1, 1), (64, 3, 8, 2), (256, 8, 8, 4), (100, 4, 5, 2), (1000, 4, 10, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_renormalised_weights_of_scores_that_are_all_zero(E, k, G, top, score):
+    """A bias selects experts whose logits are -infinity, or NaN: 0 / 0 is NaN, as by the formula; with one
+    finite logit among them that one has the whole weight."""
+    g = torch.Generator().manual_seed(E)
+    per = E // G
+    logits, bias = torch.randn(12, E, generator=g), torch.zeros(E)
+    chosen = [per * (j % top) + j // top for j in range(k)]
+    for j, e in enumerate(chosen):
+        bias[e] = 50.0 - j
+        logits[:, e] = -float("inf")
+    logits[6:, chosen[-1]] = -700.0 if score == "sigmoid" else -30.0
+    _, w = check(logits, bias, k, score=score, n_group=G, topk_group=top)
+    assert bool(torch.isnan(w[:6]).all()) and bool((w[6:, -1] == 1).all())
