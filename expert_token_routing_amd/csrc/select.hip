@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Args a, Map map) {
   const double least = over<16>(chosen ? v : INFINITY, [](double x, double y) { return fmin(x, y); });
   const float limit = value_of<MASK>(next);
   unsure = unsure || (next != 0 && !(least > double(limit) + double(fabsf(limit) * (N == 16 ? 0x1p-14f : 0x1p-13f) + 2.f * s_off + kSame)));
-  // softmax scores so far below the largest that they are equal, and sigmoids whose sum
-  // would lose bits
-  const float low = over<16>(chosen ? ml : INFINITY, Min());
+  // softmax scores so far below the largest that they are equal, sigmoids whose sum
+  // would lose bits, and NaN logits, which come behind those at -infinity
+  const float low = over<16>(!chosen ? INFINITY : none ? -INFINITY : ml, Min());
   unsure = unsure || !((a.score == 0 ? low - m : low) > -600.f);
   const double sum = a.renormalize ? over<16>(chosen ? s : 0.0, Add()) : den;
   if (chosen && here && !unsure) {

@@ -220,3 +220,20 @@ def test_renormalised_weights_of_scores_that_are_all_zero(E, k, G, top, score):
     logits[6:, chosen[-1]] = -700.0 if score == "sigmoid" else -30.0
     _, w = check(logits, bias, k, score=score, n_group=G, topk_group=top)
     assert bool(torch.isnan(w[:6]).all()) and bool((w[6:, -1] == 1).all())
+
+
+@gpu
+@pytest.mark.parametrize("E,G,top,k", [(4, 1, 1, 3), (16, 1, 1, 6), (64, 8, 1, 6), (256, 8, 2, 8), (100, 5, 3, 12), (1000, 10, 1, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_minus_infinity_comes_before_nan(E, G, top, k, score):
+    """Fewer finite logits than selections: the experts at -infinity (score 0) before the NaN ones (no
+    choice value), also where these have the lower ids."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.full((20, E), float("nan"))
+    for t in range(20):
+        order = torch.rand(E, generator=g).argsort()
+        logits[t, order[: E // 2]] = -float("inf")
+        logits[t, order[: max(1, min(k - 1, t % k))]] = torch.randn(max(1, min(k - 1, t % k)), generator=g)
+    for renorm in (True, False):
+        for rule in ("max", "top2"):
+            check(logits, None, k, score=score, n_group=G, topk_group=top, group_score=rule, renormalize=renorm)
