@@ -181,3 +181,46 @@ def test_a_shared_expert_too_wide_for_the_tables(T, H, I, Is, k):
     whole = M.moe_layer_forward(*a, d["shared_gate_up"], d["shared_down"], **kw)[0].double()
     local = M.moe_layer_forward(*a, None, None, **kw)[0].double()
     assert float((whole - local - y).abs().max()) <= 4 * 2.0 ** -24 * float(torch.maximum(local.abs(), y.abs()).max())
+
+
+@gpu
+@pytest.mark.parametrize("T,Is", [(17, 136), (24, 128), (32, 264), (32, 0), (5, 72)])
+def test_a_few_tokens_in_a_graph_and_on_a_stream(T, Is):
+    H, I, E, k = 256, 128, 64, 8
+    d = weights(T, H, I, Is, E, E, T)
+    print(f"[gpu] few tokens in a graph T={T} Is={Is}", flush=True)
+
+    def call(**more):
+        return M.moe_layer_forward(d["x"], d["w_router"], None, d["choice_bias"], d["w_gate_up"], d["w_down"], k, 0,
+                                   d["shared_gate_up"], d["shared_down"], **KW, **more)
+    want = call()[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(stream=side)[0]
+    side.synchronize()
+    assert torch.equal(got, want)
+    ws = torch.full((M.layer_workspace_size(T, H, I, Is, E, k, E),), 0xFF, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(workspace=ws)[0]
+    for rep in range(3):
+        d["x"].copy_(torch.randn(T, H, device="cuda") * H ** -0.5)
+        want = call()[0]
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), rep
+
+
+@gpu
+def test_tokens_alone_or_among_others():
+    """A token's y by itself and among 16 and 32: the sums' order goes by the experts in use, so they
+    agree to float32 accuracy of its logits and sums (1e-5 of the largest), not to bf16's."""
+    H, I, Is, E, k = 512, 128, 200, 32, 4
+    d = weights(32, H, I, Is, E, E, 1)
+    a = (d["w_router"], d["bias"], d["choice_bias"], d["w_gate_up"], d["w_down"], k, 0, d["shared_gate_up"], d["shared_down"])
+    print("[gpu] tokens alone or among others", flush=True)
+    whole = M.moe_layer_forward(d["x"], *a, out_dtype=F32, **KW)[0]
+    for lo, n in ((0, 1), (7, 16), (31, 1), (3, 17)):
+        y = M.moe_layer_forward(d["x"][lo:lo + n], *a, out_dtype=F32, **KW)[0]
+        assert float((y - whole[lo:lo + n]).abs().max()) <= 1e-5 * float(whole.abs().max())
